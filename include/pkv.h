@@ -566,6 +566,108 @@ int pkv_version(void);
  */
 int pkv_selftest_wait_timeout(int32_t *d_error, uint32_t polls, pkv_stream_t s);
 
+/*
+ * ---------------------------------------------------------------------------
+ * A paged cache held in 8 bits, with a scale for each block of tokens and head
+ * ---------------------------------------------------------------------------
+ * The lines of pkv_kv_cache_write's caches hold e4m3 codes, and every (block,
+ * KV head) has one float32 scale for K and one for V: a value is code * scale.
+ *   k_cache, v_cache: [num_blocks * block_size][num_heads][head_dim] bytes, 16-byte aligned;
+ *   k_scale, v_scale: [num_blocks][num_heads], positive (pkv_kv8_store makes powers of two;
+ *                     a V scale below 2^-100 counts as 2^-100).
+ * head_dim is 64, 128 or 256; num_heads (KV heads) at most 1024; block_size any.
+ */
+#define PKV_BF16 0             /* element types of sources, queries and outputs */
+#define PKV_FP16 1
+
+typedef struct {
+    void *k_cache;
+    void *v_cache;
+    float *k_scale;
+    float *v_scale;
+    int64_t num_blocks;
+    int32_t block_size;
+    int32_t num_heads;
+    int32_t head_dim;
+} pkv_kv8_cache;
+
+/*
+ * Quantise each new token's K and V line into its slot.
+ *   k, v: device, PKV_BF16 or PKV_FP16 (dtype), token t's line of num_heads *
+ *   head_dim elements at k + t * k_stride_bytes; slot_mapping as in
+ *   pkv_kv_cache_write (-1: not stored).  The tokens of one block stand next to
+ *   each other, as pkv_prepare_batch lays them out.
+ * Of a block, the lines below the lowest offset stored now are held from
+ * before; the lines from it on that are not stored now are dead.  Per head the
+ * block's scale becomes the larger of its scale (if lines are held) and the
+ * smallest power of two (2^-64 at least) that brings the largest finite
+ * magnitude stored now to at most 448; held codes are rounded to the new scale
+ * when it grew.  Infinities become +-448, NaN stays NaN.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_ALIGN (pointers and strides: 16 bytes),
+ * and on the device PKV_DEVERR_SLOT for a slot past the cache (not stored).
+ * One launch, no workspace; capturable.
+ */
+int pkv_kv8_store(const pkv_kv8_cache *cache, const void *k, const void *v,
+                  int64_t k_stride_bytes, int64_t v_stride_bytes, int32_t dtype,
+                  const int64_t *slot_mapping, int32_t num_tokens, int32_t *d_error,
+                  pkv_stream_t stream);
+
+/* Bytes of device workspace that pkv_kv8_attention takes (the same for every
+   batch); its contents need no initialisation and may be reused by the next
+   call on the same stream. */
+int pkv_kv8_attention_workspace(int32_t num_heads, int32_t head_dim, int64_t *bytes);
+
+/*
+ * Attention of a prepared batch's queries over the cache.  Request i's tokens
+ * query_start_loc[i] .. query_start_loc[i + 1] - 1 are the last ones of its
+ * seq_lens[i] cached tokens (stored before this call); a query at position p
+ * sees the positions max(0, p - window + 1) .. p (window 0: all up to p) whose
+ * block, block_tables[i][position / block_size], is not -1.
+ *   q:    [num_tokens][num_q_heads][head_dim], dtype, tokens q_stride_bytes apart;
+ *         head h reads KV head h / (num_q_heads / num_heads);
+ *   out:  the same shape and type, tokens out_stride_bytes apart;
+ *   lse:  [num_tokens][num_q_heads] float32, the natural logarithm of each
+ *         row's softmax sum (NULL: not written);
+ *   weights: NULL, or [num_blocks * block_size] float32: each token's softmax
+ *         weight, summed over the step's queries and heads, is added to its
+ *         slot (needs lse; where requests of one call share a block their
+ *         sums are added in any order).
+ * A row that sees nothing gives 0 and -inf.  Tokens past query_start_loc[n] are
+ * not written.  Device errors: PKV_DEVERR_COUNT (query_start_loc descends or
+ * leaves the batch: the request is skipped), PKV_DEVERR_BLOCK (a block id past
+ * the cache or a position past the table: not seen).
+ * The products' operands are f16 (a code is exact in f16, a query after scaling its
+ * row by a power of two, a softmax weight times its value scale is rounded);
+ * sums and softmax statistics are fp32.
+ */
+int pkv_kv8_attention(const pkv_kv8_cache *cache, const void *q, int64_t q_stride_bytes,
+                      int32_t dtype, int32_t num_q_heads, const int32_t *block_tables,
+                      int32_t table_width, const int32_t *query_start_loc,
+                      const int32_t *seq_lens, int32_t n, int32_t num_tokens,
+                      float softmax_scale, int32_t window, void *out, int64_t out_stride_bytes,
+                      float *lse, float *weights, void *workspace, int64_t workspace_bytes,
+                      int32_t *d_error, pkv_stream_t stream);
+
+/*
+ * Shrink requests to `budget` tokens by weight.  Request i (seq_lens[i] cached
+ * tokens in block_tables[i]) keeps all of them if they are at most budget;
+ * otherwise the first keep_first, the last keep_last, and of those between the
+ * ones with the largest weights[slot] (equal ones: the lower position first;
+ * NaN below every number).  The kept tokens' lines and weights are copied, in
+ * order, into the blocks of new_block_tables[i], which no request's
+ * block_tables name; the old blocks keep their contents and may be shared.  A
+ * new block's scale is the largest of its tokens' scales, codes are rounded to it.
+ *   new_seq_lens[n]:  min(seq_lens[i], budget), or -1 for a request left alone
+ *                     because a table names no block where one is needed
+ *                     (PKV_DEVERR_BLOCK) or is too short (PKV_DEVERR_POSITION);
+ *   kept[n][budget]:  the old position of each kept token, ascending, then -1.
+ */
+int pkv_kv8_evict(const pkv_kv8_cache *cache, float *weights, const int32_t *block_tables,
+                  int32_t table_width, const int32_t *seq_lens, int32_t n,
+                  const int32_t *new_block_tables, int32_t new_table_width, int32_t budget,
+                  int32_t keep_first, int32_t keep_last, int32_t *new_seq_lens, int32_t *kept,
+                  int32_t *d_error, pkv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -56,7 +56,8 @@ EXPORTS = [
     "pkv_prefix_cache_insert", "pkv_prefix_cache_match", "pkv_pool_reset", "pkv_pool_size",
     "pkv_pool_read", "pkv_allocate_slots", "pkv_release_blocks", "pkv_get_error",
     "pkv_state_error_word", "pkv_row_info", "pkv_read_row", "pkv_last_cuda_error",
-    "pkv_version", "pkv_selftest_wait_timeout",
+    "pkv_version", "pkv_selftest_wait_timeout", "pkv_kv8_store", "pkv_kv8_attention_workspace",
+    "pkv_kv8_attention", "pkv_kv8_evict",
 ]
 
 
@@ -97,6 +98,12 @@ class StepDelta(C.Structure):
 class KvItem(C.Structure):
     _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_cache", C.c_void_p),
                 ("v_cache", C.c_void_p), ("slot_mapping", C.c_void_p), ("num_slots", C.c_int64)]
+
+
+class Kv8CacheArgs(C.Structure):
+    _fields_ = [("k_cache", C.c_void_p), ("v_cache", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("num_blocks", C.c_int64), ("block_size", C.c_int32),
+                ("num_heads", C.c_int32), ("head_dim", C.c_int32)]
 
 
 _P32 = C.POINTER(C.c_int32)
@@ -141,6 +148,12 @@ def _declare(lib):
         "pkv_last_cuda_error": [],
         "pkv_version": [],
         "pkv_selftest_wait_timeout": [_VP, C.c_uint32, _VP],
+        "pkv_kv8_store": [C.POINTER(Kv8CacheArgs), _VP, _VP, i64, i64, i32, _VP, i32, _VP, _VP],
+        "pkv_kv8_attention_workspace": [i32, i32, C.POINTER(i64)],
+        "pkv_kv8_attention": [C.POINTER(Kv8CacheArgs), _VP, i64, i32, i32, _VP, i32, _VP, _VP, i32,
+                              i32, C.c_float, i32, _VP, i64, _VP, _VP, _VP, i64, _VP, _VP],
+        "pkv_kv8_evict": [C.POINTER(Kv8CacheArgs), _VP, _VP, i32, _VP, i32, _VP, i32, i32, i32, i32,
+                          _VP, _VP, _VP, _VP],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -791,3 +804,177 @@ class PrefixCache:
                                             n, _ptr(hits), C.c_void_p(ids.data_ptr()),
                                             _stream_handle(stream)), "pkv_prefix_cache_match")
         return hits, ids[: int(keys.numel())]
+
+
+# -- the cache held in 8 bits -------------------------------------------------
+
+_KV8_DTYPES = {"torch.bfloat16": 0, "torch.float16": 1}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
+    """The C view of an 8-bit cache: lines [num_slots, heads * head_dim] of one byte per element
+    and scales [num_blocks, heads]."""
+    _need(k_scale.dim() == 2 and k_scale.shape == v_scale.shape and k_cache.shape == v_cache.shape,
+          "k_cache and v_cache, k_scale and v_scale have the same shapes; scales are [num_blocks, heads]")
+    blocks, heads = k_scale.shape
+    _need(blocks > 0 and heads > 0 and k_cache.dim() >= 1 and k_cache.shape[0] % blocks == 0
+          and k_cache.numel() % max(k_cache.shape[0] * heads, 1) == 0 and k_cache.shape[0] > 0,
+          "the caches hold num_blocks * block_size lines of heads * head_dim bytes")
+    for t in (k_cache, v_cache):
+        _need(t.element_size() == 1 and t.is_contiguous(), "the caches are contiguous, one byte an element")
+    for t in (k_scale, v_scale):
+        _need(str(t.dtype) == "torch.float32" and t.is_contiguous(), "the scales are contiguous float32")
+    slots = k_cache.shape[0]
+    return Kv8CacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                        blocks, slots // blocks, heads, k_cache.numel() // (slots * heads))
+
+
+def _kv8_int32(*tensors):
+    for t in tensors:
+        _need(str(t.dtype) == "torch.int32" and t.is_contiguous(), "tables, lengths and locations are contiguous int32")
+
+
+def _kv8_rows(x, width, what):
+    """Bytes between the tokens of x: [tokens, width] or [tokens, heads, head_dim], each token's
+    elements contiguous."""
+    inner = 1
+    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+        _need(size == 1 or stride == inner, f"{what}: a token's elements are contiguous")
+        inner *= size
+    _need(x.dim() >= 2 and inner == width, f"{what}: [tokens, heads, head_dim] of the cache's sizes")
+    return x.stride(0) * x.element_size() if x.shape[0] > 1 else width * x.element_size()
+
+
+def _kv8_dtype(*tensors):
+    kind = _KV8_DTYPES.get(str(tensors[0].dtype))
+    _need(kind is not None and all(t.dtype == tensors[0].dtype for t in tensors),
+          "bfloat16 or float16, the same for all")
+    return kind
+
+
+def kv8_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, d_error=None, stream=None,
+              check=True):
+    """Quantise each token's K and V line into the 8-bit cache at its slot (``pkv_kv8_store``).
+
+    k, v: bfloat16 or float16 [tokens, heads, head_dim] (or [tokens, heads * head_dim]), token
+    stride allowed; k_cache, v_cache: one byte per element, [num_blocks * block_size, heads *
+    head_dim]; k_scale, v_scale: float32 [num_blocks, heads]; slot_mapping: int64."""
+    cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    T = slot_mapping.numel()
+    _need(str(slot_mapping.dtype) == "torch.int64" and slot_mapping.is_contiguous(), "slot_mapping is contiguous int64")
+    _need(k.shape == v.shape and k.shape[0] >= T, "k and v have the same shape, a row for each slot")
+    width = cache.num_heads * cache.head_dim
+    rc = lib().pkv_kv8_store(C.byref(cache), _ptr(k), _ptr(v), _kv8_rows(k, width, "k"),
+                             _kv8_rows(v, width, "v"), _kv8_dtype(k, v), _ptr(slot_mapping), T,
+                             C.c_void_p(d_error) if d_error else None, _stream(stream))
+    if check:
+        _check(rc, "pkv_kv8_store")
+    return rc
+
+
+def kv8_attention_workspace(num_heads, head_dim):
+    """Bytes of device workspace an attention call takes (``pkv_kv8_attention_workspace``)."""
+    n = C.c_int64(0)
+    _check(lib().pkv_kv8_attention_workspace(int(num_heads), int(head_dim), C.byref(n)),
+           "pkv_kv8_attention_workspace")
+    return n.value
+
+
+def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_start_loc, seq_lens,
+                  softmax_scale=None, window=0, weights=None, out=None, lse=None, workspace=None,
+                  d_error=None, stream=None, check=True):
+    """Attention of a prepared batch's queries over the 8-bit cache (``pkv_kv8_attention``).
+
+    q: bfloat16 or float16 [tokens, q_heads, head_dim], token stride allowed; block_tables [n, W],
+    query_start_loc [n + 1] and seq_lens [n] as prepare_batch gives them.  window: a query sees
+    that many positions, its own among them (0: all).  weights: float32 [num_slots], each token's
+    softmax weight is added to it.  out, lse, workspace (uint8, kv8_attention_workspace bytes) are
+    allocated when not given.  Returns (out, lse); lse is float32 [tokens, q_heads]."""
+    import torch
+
+    cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    _kv8_int32(block_tables, query_start_loc, seq_lens)
+    n = seq_lens.numel()
+    _need(block_tables.dim() == 2 and block_tables.shape[0] >= n and query_start_loc.numel() >= n + 1,
+          "block_tables [n, W], query_start_loc [n + 1], seq_lens [n]")
+    _need(q.dim() == 3 and q.shape[2] == cache.head_dim, "q is [tokens, q_heads, head_dim]")
+    T, hq = q.shape[0], q.shape[1]
+    kind, q_stride = _kv8_dtype(q), _kv8_rows(q, hq * cache.head_dim, "q")
+    if weights is not None:
+        _need(str(weights.dtype) == "torch.float32" and weights.is_contiguous()
+              and weights.numel() == k_cache.shape[0], "weights is contiguous float32, one for each slot")
+    handle = _stream(stream)
+    made = []
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        made.append(out)
+    _need(out.shape == q.shape and out.dtype == q.dtype, "out has q's shape and type")
+    out_stride = _kv8_rows(out, hq * cache.head_dim, "out")
+    if lse is None:
+        lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+        made.append(lse)
+    _need(lse.shape == (T, hq) and lse.is_contiguous() and str(lse.dtype) == "torch.float32",
+          "lse is contiguous float32 [tokens, q_heads]")
+    if workspace is None:
+        workspace = torch.empty(kv8_attention_workspace(cache.num_heads, cache.head_dim),
+                                dtype=torch.uint8, device=q.device)
+        made.append(workspace)
+    if stream is not None and made and q.is_cuda:
+        # tensors made here were allocated on the current stream, the work runs on another
+        other = torch.cuda.ExternalStream(handle) if isinstance(stream, int) else stream
+        for t in made:
+            t.record_stream(other)
+    if softmax_scale is None:
+        softmax_scale = cache.head_dim ** -0.5
+    rc = lib().pkv_kv8_attention(C.byref(cache), _ptr(q), q_stride, kind, hq, _ptr(block_tables),
+                                 block_tables.shape[1], _ptr(query_start_loc), _ptr(seq_lens), n, T,
+                                 float(softmax_scale), int(window), _ptr(out), out_stride, _ptr(lse),
+                                 _ptr(weights), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                 C.c_void_p(d_error) if d_error else None, handle)
+    if check:
+        _check(rc, "pkv_kv8_attention")
+        return out, lse
+    return (out, lse) if rc == OK else rc
+
+
+def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_lens,
+              new_block_tables, budget, keep_first=0, keep_last=0, new_seq_lens=None, kept=None,
+              d_error=None, stream=None, check=True):
+    """Shrink requests to ``budget`` tokens by accumulated weight, into new blocks
+    (``pkv_kv8_evict``).  Returns (new_seq_lens [n], kept [n, budget])."""
+    import torch
+
+    cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    _kv8_int32(block_tables, new_block_tables, seq_lens)
+    n = seq_lens.numel()
+    _need(block_tables.dim() == 2 and new_block_tables.dim() == 2 and block_tables.shape[0] >= n
+          and new_block_tables.shape[0] >= n, "block_tables and new_block_tables are [n, width]")
+    _need(str(weights.dtype) == "torch.float32" and weights.is_contiguous()
+          and weights.numel() == k_cache.shape[0], "weights is contiguous float32, one for each slot")
+    handle = _stream(stream)
+    made = []
+    if new_seq_lens is None:
+        new_seq_lens = torch.empty(n, dtype=torch.int32, device=k_cache.device)
+        made.append(new_seq_lens)
+    if kept is None:
+        kept = torch.empty((n, max(int(budget), 0)), dtype=torch.int32, device=k_cache.device)
+        made.append(kept)
+    _kv8_int32(new_seq_lens, kept)
+    _need(new_seq_lens.numel() == n and kept.numel() == n * max(int(budget), 0), "new_seq_lens [n], kept [n, budget]")
+    if stream is not None and made and k_cache.is_cuda:
+        other = torch.cuda.ExternalStream(handle) if isinstance(stream, int) else stream
+        for t in made:
+            t.record_stream(other)
+    rc = lib().pkv_kv8_evict(C.byref(cache), _ptr(weights), _ptr(block_tables), block_tables.shape[1],
+                             _ptr(seq_lens), n, _ptr(new_block_tables), new_block_tables.shape[1],
+                             int(budget), int(keep_first), int(keep_last), _ptr(new_seq_lens),
+                             _ptr(kept), C.c_void_p(d_error) if d_error else None, handle)
+    if check:
+        _check(rc, "pkv_kv8_evict")
+        return new_seq_lens, kept
+    return (new_seq_lens, kept) if rc == OK else rc

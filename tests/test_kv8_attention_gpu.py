@@ -1,0 +1,335 @@
+"""kv8_attention on the GPU against its plain implementation in 64 bits.
+
+Tolerances, with A = sum p |v| of an output element, X = a row's largest sum
+|q k| softmax_scale and the half steps 2^-11 (f16), 2^-8 (bf16), 2^-24 (fp32):
+a logit is a sum of exact products in fp32, off by at most 2^-19 X (room for
+sixteen half-step roundings along it twice over), and the logarithm of the value
+scale (up to 26 here) rides on it, which costs two more half steps of values up
+to 64, 2^-17; a weight times its value
+scale is rounded to f16 once, 2^-11 of itself, or 2^-25 of the row's largest
+when it is far smaller; sums in fp32 add 2^-17; the output is rounded once."""
+import math
+
+import pytest
+
+import paged_kv_prep_gb300 as pkv
+import pkv_workloads as workloads
+from tests import kv8_reference as ref
+from tests.gpu_helpers import build_states
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_kv_prep_gb300 import build as pbuild
+    pbuild.build()
+    yield
+    torch.cuda.empty_cache()
+
+
+class Case:
+    def __init__(self, reqs, bs, heads, group, d, dtype=torch.bfloat16, seed=1, spread=2, pad=0, width=0, magnitude=1.0):
+        """reqs: (scheduled tokens, cached tokens) of each request."""
+        gen = torch.Generator().manual_seed(seed)
+        self.gen, self.reqs, self.bs, self.heads, self.group, self.d, self.dtype = gen, reqs, bs, heads, group, d, dtype
+        self.lens = [x for _, x in reqs]
+        self.starts = [0]
+        for c, _ in reqs:
+            self.starts.append(self.starts[-1] + c)
+        need = [max(0, -(-x // bs)) for x in self.lens]
+        self.blocks = sum(need) + 2
+        perm = torch.randperm(self.blocks, generator=gen).tolist()
+        self.tables = torch.full((len(reqs), max(max(need), 1) + width), -1, dtype=torch.int32)
+        for i, n in enumerate(need):
+            for j in range(n):
+                self.tables[i, j] = perm.pop()
+        slots = self.blocks * bs
+        # every byte a NaN code first: whatever is not a cached token must not be read into a sum
+        self.caches = [torch.full((slots, heads, d), 127, dtype=torch.uint8) for _ in range(2)]
+        self.scales = [torch.exp2(torch.randint(-spread, spread + 1, (self.blocks, heads), generator=gen).float() - 6)
+                       for _ in range(2)]
+        for i, x in enumerate(self.lens):
+            for s in range(max(x, 0)):
+                b = int(self.tables[i, s // bs])
+                for c in self.caches:
+                    c[b * bs + s % bs] = ref.encode(torch.randn(heads, d, generator=gen).double() * 64)
+        T, hq = self.starts[-1], heads * group
+        rows = (torch.randn(T, hq * d + pad, generator=gen) * magnitude).to(dtype)
+        self.q = rows[:, :hq * d].view(T, hq, d) if not pad else rows[:, :hq * d].unflatten(1, (hq, d))
+
+    def args(self):
+        kc, vc = [c.view(c.shape[0], -1).cuda() for c in self.caches]
+        ks, vs = [s.cuda() for s in self.scales]
+        rows = self.q.as_strided((self.q.shape[0], self.q.stride(0)), (self.q.stride(0), 1)) if self.q.shape[0] > 1 else None
+        if rows is not None and self.q.stride(0) != self.q.shape[1] * self.d:
+            q = rows.cuda()[:, :self.q.shape[1] * self.d].unflatten(1, self.q.shape[1:])
+        else:
+            q = self.q.contiguous().cuda()
+        return (q, kc, vc, ks, vs, self.tables.cuda(), torch.tensor(self.starts, dtype=torch.int32).cuda(),
+                torch.tensor(self.lens, dtype=torch.int32).cuda())
+
+    def reference(self, scale, window, weights=None):
+        return ref.attention(self.q, *self.caches, *self.scales, self.tables, self.starts, self.lens, scale, window, weights)
+
+
+def compare(case, out, lse, want, vmax=448.0):
+    w_out, w_lse, size, reach = want
+    out, lse = out.cpu().double(), lse.cpu().double()
+    assert torch.equal(torch.isinf(lse), torch.isinf(w_lse)) and torch.equal(lse.isnan(), w_lse.isnan())
+    fine = torch.isfinite(w_lse)
+    logit = 2.0 ** -19 * reach + 2.0 ** -22 * w_lse.abs().clamp(max=1e30) + 2.0 ** -17
+    assert (((lse - w_lse).abs() <= logit)[fine]).all(), float((lse - w_lse)[fine].abs().max())
+    assert torch.equal(out.isnan(), w_out.isnan())
+    largest = float(max(s.max() for s in case.scales[1:])) * vmax
+    most = max(list(case.lens) + [1])
+    tol = (2.0 ** -11 + 2.0 ** -17 + 2 * logit[..., None]) * size + most * 2.0 ** -25 * largest
+    tol = tol + HALF[case.dtype] * (w_out.abs() + tol) + 2.0 ** -25
+    bad = (out - w_out).abs() > tol
+    bad &= ~w_out.isnan()
+    assert not bad.any(), (int(bad.sum()), float(((out - w_out).abs() / tol)[bad].max()))
+
+
+def check(case, window=0, scale=None, weights=True):
+    scale = case.d ** -0.5 if scale is None else scale
+    a = case.args()
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    before = torch.rand(case.blocks * case.bs, generator=case.gen)
+    got = before.cuda()
+    out, lse = pkv.kv8_attention(*a, softmax_scale=scale, window=window, weights=got if weights else None,
+                                 d_error=word.data_ptr())
+    assert word.item() == 0
+    sums = torch.zeros(case.blocks * case.bs, dtype=torch.float64)
+    want = case.reference(scale, window, sums)
+    compare(case, out, lse, want)
+    if weights:
+        reach = float(want[3].max()) if want[3].numel() else 0.0
+        top = float(want[1][torch.isfinite(want[1])].abs().max()) if torch.isfinite(want[1]).any() else 0.0
+        rel = 4 * (2.0 ** -19 * reach + 2.0 ** -22 * top) + 2.0 ** -15
+        total = before.double() + sums
+        assert ((got.cpu().double() - total).abs() <= rel * sums + 2.0 ** -22 * total).all()
+        assert torch.equal(got.cpu()[sums == 0], before[sums == 0])
+    return out, lse
+
+
+DECODES = [(1, x) for x in (1, 15, 16, 17, 200, 33, 640, 1000)]
+MIXED = [(1, 1), (1, 77), (2, 2), (3, 50), (5, 5), (17, 100), (40, 90), (1, 300)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("heads,group,d", [(8, 4, 128), (2, 8, 128), (1, 1, 128), (3, 5, 64), (2, 7, 256), (1, 12, 64),
+                                           (5, 1, 64)])
+@pytest.mark.parametrize("reqs", [DECODES, MIXED], ids=["decodes", "mixed"])
+def test_matches_plain(reqs, heads, group, d, dtype):
+    check(Case(reqs, 16, heads, group, d, dtype, seed=heads * 100 + group))
+
+
+@pytest.mark.parametrize("bs", [1, 7, 24, 32, 48, 100])
+def test_block_sizes(bs):
+    check(Case(MIXED, bs, 2, 4, 128, seed=bs, width=2))
+
+
+@pytest.mark.parametrize("window", [1, 2, 16, 30, 64, 4096, 2 ** 31 - 1])
+def test_windows(window):
+    check(Case(MIXED + [(1, 1), (30, 33)], 16, 2, 4, 128, seed=window % 97), window=window)
+
+
+@pytest.mark.parametrize("group", [4, 16])
+def test_rows_that_see_nothing(group):
+    """More scheduled tokens than cached ones, no cached tokens, no scheduled tokens, freed blocks."""
+    case = Case([(1, 0), (0, 40), (9, 4), (1, 64), (3, 70)], 16, 2, group, 128, seed=2)
+    case.tables[3, :] = -1
+    case.tables[4, 1:3] = -1
+    out, lse = check(case)
+    assert (lse[0] == -math.inf).all() and (out[0] == 0).all()
+    assert (lse[1:6] == -math.inf).all() and torch.isfinite(lse[6:10]).all()
+    assert (lse[10] == -math.inf).all()
+
+
+def test_one_long_request_is_split():
+    check(Case([(1, 6000)], 32, 1, 4, 64, seed=3))
+    check(Case([(2, 3001), (1, 9)], 16, 2, 8, 64, seed=4), window=2500)
+
+
+@pytest.mark.parametrize("spread", [10, 20])
+def test_scales_that_differ_between_blocks(spread):
+    """Value scales up to 2^40 apart: the f16 operand carries the scale, so no row loses its own."""
+    case = Case([(1, 100), (1, 33), (6, 60)], 16, 2, 4, 128, seed=5, spread=spread)
+    case.scales[0] = torch.exp2(torch.randint(-8, -5, case.scales[0].shape, generator=case.gen).float())
+    check(case)
+
+
+def test_extreme_queries_and_logits():
+    """Queries far from 1, rows with tiny and large elements, a scale that saturates the softmax."""
+    case = Case([(1, 90), (1, 17), (4, 40)], 16, 2, 4, 128, seed=6)
+    case.q = case.q.clone()
+    case.q[0] *= 2.0 ** 40
+    case.q[1] *= 2.0 ** -60
+    case.q[2, :, ::2] *= 2.0 ** -12
+    case.q[3] = 0
+    for i in range(2):
+        case.scales[i] = torch.exp2(torch.randint(-8, -5, case.scales[i].shape, generator=case.gen).float())
+    check(case, scale=2.0 ** -38)
+    check(case, scale=0.0)
+    check(Case([(1, 300), (3, 20)], 16, 2, 4, 128, seed=7, magnitude=8.0), scale=1.0)
+
+
+def test_nan_and_infinity_stay_in_their_rows():
+    """A NaN key or value reaches the rows that see it and no other; so does an infinite query."""
+    case = Case([(8, 40), (1, 20), (1, 20), (2, 30)], 16, 2, 4, 128, seed=8)
+    b = case.tables
+    case.caches[1][int(b[0, 2]) * 16 + 5, 0, 3] = 127       # position 37: queries 5..7 of request 0, head 0, dim 3
+    case.caches[0][int(b[0, 2]) * 16 + 6, 1, 9] = 255       # position 38: queries 6, 7, head 1
+    case.caches[1][int(b[1, 0]) * 16 + 2, 1, 100] = 127
+    case.q = case.q.clone()
+    case.q[9, 0, 0] = math.nan
+    case.q[11, 3] = math.nan
+    scale = case.d ** -0.5
+    out, lse = pkv.kv8_attention(*case.args(), softmax_scale=scale)
+    want = case.reference(scale, 0)
+    assert want[0].isnan().any() and not want[0][:5].isnan().any()
+    w_out, w_lse, size, reach = want
+    assert torch.equal(out.cpu().isnan(), w_out.isnan()) and torch.equal(lse.cpu().isnan(), w_lse.isnan())
+    ok = ~w_out.isnan()
+    assert (out.cpu().double() - w_out)[ok].abs().max() < 0.05 * w_out[ok].abs().max()
+
+
+def test_bad_tables_are_reported_and_not_read():
+    case = Case([(1, 100), (1, 60), (1, 30), (2, 20)], 16, 2, 4, 128, seed=9)
+    case.tables[0, 2] = case.blocks
+    case.tables[1, 0] = 2 ** 31 - 1
+    a = list(case.args())
+    lens = a[7].clone()
+    lens[2] = case.tables.shape[1] * 16 + 40                # longer than the table: the rest is not seen
+    a[7] = lens
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = pkv.kv8_attention(*a, d_error=word.data_ptr())
+    assert word.item() == pkv.DEVERR_BLOCK
+    case.lens[2] = int(lens[2])
+    want = case.reference(case.d ** -0.5, 0)
+    compare(case, out, lse, want)
+
+
+def test_bad_locations_skip_the_request():
+    case = Case([(1, 30), (1, 40), (2, 20), (1, 10)], 16, 2, 4, 128, seed=10)
+    a = list(case.args())
+    a[6] = torch.tensor([0, 1, 2, 1, 900], dtype=torch.int32).cuda()
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = torch.full_like(a[0], 7.0)
+    out, lse = pkv.kv8_attention(*a, out=out, d_error=word.data_ptr())
+    assert word.item() == pkv.DEVERR_COUNT
+    want = case.reference(case.d ** -0.5, 0)
+    compare_rows = [0, 1]
+    assert (out.cpu().double() - want[0])[compare_rows].abs().max() < 0.05 * want[0].abs().max()
+    assert (out[2:] == 7.0).all()
+
+
+def test_strided_rows_and_given_buffers():
+    """q as a view of fused projection rows, out as a view of wider rows, a workspace kept by the caller."""
+    case = Case(MIXED, 16, 2, 4, 128, seed=11, pad=2 * 2 * 128)
+    a = case.args()
+    assert a[0].stride(0) == (8 + 4) * 128
+    wide = torch.full((a[0].shape[0], 8 * 128 + 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    out = wide[:, :8 * 128].unflatten(1, (8, 128))
+    lse = torch.empty(a[0].shape[0], 8, device="cuda")
+    ws = torch.full((pkv.kv8_attention_workspace(2, 128),), 255, dtype=torch.uint8, device="cuda")
+    want = case.reference(case.d ** -0.5, 0)
+    for _ in range(2):
+        pkv.kv8_attention(*a, out=out, lse=lse, workspace=ws)
+        compare(case, out, lse, want)
+        assert (wide[:, 8 * 128:] == 5.0).all()
+    assert pkv.kv8_attention(*a, workspace=ws[:1024], check=False) == pkv.ERR_INVALID_ARG
+
+
+def test_repeats_are_bit_identical_and_streams_and_capture():
+    case = Case(MIXED + [(1, 2000), (64, 400)], 16, 2, 4, 128, seed=12)
+    a = case.args()
+    first = pkv.kv8_attention(*a)
+    for _ in range(3):
+        again = pkv.kv8_attention(*a)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    other = pkv.kv8_attention(*a, stream=side)
+    side.synchronize()
+    assert torch.equal(first[0], other[0])
+    w = torch.zeros(case.blocks * case.bs, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out, lse = pkv.kv8_attention(*a, weights=w)
+    w.zero_()
+    out.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(first[0], out)
+    once = w.clone()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.allclose(w, 2 * once, rtol=2 ** -23, atol=0)
+
+
+def test_prepared_batch_runs_the_whole_step():
+    """prepare_batch -> kv8_store -> kv8_attention -> kv8_evict, as a step uses them."""
+    wl = workloads.random_small(seed=5, num_requests=12, max_ctx=120, max_chunk=30, decode_frac=0.5)
+    st, _, rows_map = build_states(wl)
+    rows, ns = workloads.schedule_arrays(wl, rows_map)
+    batch = st.prepare_batch(rows, ns)
+    T, heads, group, d = batch.total_tokens, 2, 4, 128
+    blocks, bs = wl.groups[0].num_blocks, wl.groups[0].block_size
+    n = batch.seq_lens.numel()
+    extra = n * 2
+    gen = torch.Generator().manual_seed(13)
+    codes = torch.randint(0, 120, ((blocks + extra) * bs, heads, d), generator=gen, dtype=torch.uint8)
+    scale = torch.full((blocks + extra, heads), 2.0 ** -6)
+    kc, vc, ks, vs = codes.clone(), codes.clone(), scale.clone(), scale.clone()
+    dev = [kc.view(-1, heads * d).cuda(), vc.view(-1, heads * d).cuda(), ks.cuda(), vs.cuda()]
+    k, v = [torch.randn(T, heads, d, generator=gen).bfloat16() for _ in range(2)]
+    q = torch.randn(T, heads * group, d, generator=gen).bfloat16()
+    weights = torch.zeros((blocks + extra) * bs, device="cuda")
+    slots = batch.slot_mapping[0]
+    pkv.kv8_store(k.cuda(), v.cuda(), *dev, slots)
+    out, lse = pkv.kv8_attention(q.cuda(), *dev, batch.block_tables[0], batch.query_start_loc, batch.seq_lens, weights=weights)
+    fresh = (torch.arange(extra, dtype=torch.int32).view(n, 2) + blocks).cuda()
+    new, kept = pkv.kv8_evict(*dev, weights, batch.block_tables[0], batch.seq_lens, fresh, 2 * bs - 3, keep_first=1, keep_last=4)
+
+    ref.store(k, v, kc, vc, ks, vs, slots.cpu(), blocks + extra)
+    case = Case([(1, 1)], bs, heads, group, d)
+    case.scales, case.lens, case.dtype = [ks, vs], batch.seq_lens.tolist(), torch.bfloat16
+    want = ref.attention(q, kc, vc, ks, vs, batch.block_tables[0].cpu(), batch.query_start_loc.tolist(), case.lens, d ** -0.5, 0)
+    compare(case, out, lse, want)
+    w = weights.cpu().clone()
+    w.view(-1, bs)[blocks:] = 0
+    want_new, want_kept = ref.evict(kc, vc, ks, vs, w, batch.block_tables[0].cpu(), case.lens, fresh.cpu(), 2 * bs - 3, 1, 4)
+    assert new.tolist() == want_new and torch.equal(kept.cpu(), want_kept)
+    assert ref.same_codes(dev[0].cpu().view(kc.shape), kc) and ref.same_codes(dev[1].cpu().view(vc.shape), vc)
+    st.close()
+
+
+def test_cache_past_32_bits():
+    """Blocks whose bytes start past 2^32."""
+    heads, group, d, bs = 8, 4, 128, 16
+    blocks = 300000
+    small = Case([(1, 60), (3, 20)], bs, heads, group, d, seed=14)
+    q, kc, vc, ks, vs, tab, qsl, lens = small.args()
+    shift = blocks - small.blocks
+    big = [torch.full((blocks * bs, heads * d), 127, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    scale = [torch.ones(blocks, heads, device="cuda") for _ in range(2)]
+    for b, c in zip(big, (kc, vc)):
+        b[shift * bs:] = c
+    for b, c in zip(scale, (ks, vs)):
+        b[shift:] = c
+    want = pkv.kv8_attention(q, kc, vc, ks, vs, tab, qsl, lens)
+    w = torch.zeros(blocks * bs, device="cuda")
+    got = pkv.kv8_attention(q, *big, *scale, torch.where(tab >= 0, tab + shift, tab), qsl, lens, weights=w)
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+    assert float(w.sum()) == pytest.approx(4 * heads * group, rel=1e-4)
+
+
+def test_no_tokens():
+    case = Case([(1, 5)], 16, 1, 1, 64)
+    q, kc, vc, ks, vs, tab, qsl, lens = case.args()
+    out, lse = pkv.kv8_attention(q[:0], kc, vc, ks, vs, tab[:0], qsl[:1], lens[:0])
+    assert out.shape == (0, 1, 64) and lse.shape == (0, 1)
