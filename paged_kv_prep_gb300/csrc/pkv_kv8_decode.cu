@@ -324,7 +324,8 @@ struct Tile {
                 const int f = rt * 8 * NT + nt * 8 + 2 * t + col;
                 if (f >= rows) continue;
                 const int j = f / p.G, hq = head * p.G + f - j * p.G;
-                const bool none = top[nt][col] == -INFINITY;       // nothing visible
+                // nothing visible (a row of NaN logits leaves top at -inf too, but its sum is NaN)
+                const bool none = top[nt][col] == -INFINITY && sum[nt][col] == 0.f;
                 const float inv = none ? 0.f : 1.f / sum[nt][col];
                 char *row = p.out + static_cast<int64_t>(r.start + j) * p.out_stride + 2 * static_cast<int64_t>(hq) * D;
 #pragma unroll
@@ -461,25 +462,25 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
         for (int k = lane; k < pieces; k += 32) top = fmaxf(top, part(k)[row]);
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        const bool none = top == -INFINITY;
         float sum = 0.f, acc[kPer];
 #pragma unroll
         for (int c = 0; c < kPer; c++) acc[c] = 0.f;
-        if (!none) {
 #pragma unroll 8
-            for (int k = 0; k < pieces; k++) {
-                const float *a = part(k);
-                const float m = a[row], f2 = m == -INFINITY ? 0.f : exp2_fast(m - top);
-                sum += f2 * a[kRows + row];
-                const float *o = a + 2 * kRows + row * D + lane * kPer;
+        for (int k = 0; k < pieces; k++) {
+            const float *a = part(k);
+            const float m = a[row], l = a[kRows + row];
+            // a piece without a top adds nothing, unless its logits were NaN
+            const float f2 = m == -INFINITY ? (l == 0.f ? 0.f : NAN) : exp2_fast(m - top);
+            sum += f2 * l;
+            const float *o = a + 2 * kRows + row * D + lane * kPer;
 #pragma unroll
-                for (int c = 0; c < kPer; c += 2) {
-                    const float2 y = *reinterpret_cast<const float2 *>(o + c);
-                    acc[c] += f2 == 0.f ? 0.f : f2 * y.x;
-                    acc[c + 1] += f2 == 0.f ? 0.f : f2 * y.y;
-                }
+            for (int c = 0; c < kPer; c += 2) {
+                const float2 y = *reinterpret_cast<const float2 *>(o + c);
+                acc[c] += f2 == 0.f ? 0.f : f2 * y.x;
+                acc[c + 1] += f2 == 0.f ? 0.f : f2 * y.y;
             }
         }
+        const bool none = top == -INFINITY && sum == 0.f;
         const int j = f / p.G, hq = head * p.G + f - j * p.G;
         const float inv = none ? 0.f : 1.f / sum;
         char *out = p.out + static_cast<int64_t>(r.start + j) * p.out_stride + 2 * (static_cast<int64_t>(hq) * D + lane * kPer);
