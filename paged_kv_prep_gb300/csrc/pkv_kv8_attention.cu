@@ -17,8 +17,12 @@ namespace pkv {
 
 int64_t kv8_decode_workspace(int32_t head_dim, int sms);
 int kv8_launch_decode(const AttnParams &p, int32_t head_dim, bool one_tile, int sms, cudaStream_t s);
+int64_t kv8_prefill_workspace(int32_t head_dim, int sms);
+int kv8_launch_prefill(const AttnParams &p, int32_t head_dim, int sms, cudaStream_t s);
 
 namespace {
+
+constexpr int kPrefillRows = 32;
 
 constexpr int kWTokens = 64;
 constexpr int kWWarps = 8;
@@ -26,7 +30,7 @@ constexpr int kWWarps = 8;
 __device__ __forceinline__ int64_t weight_units(const AttnParams &p, const Req &r) {
     if (r.count <= 0) return 0;
     const int lo = r.lo & ~(kWTokens - 1);
-    return r.len > lo ? (r.len - lo + kWTokens - 1) / kWTokens : 0;
+    return r.keys > lo ? (r.keys - lo + kWTokens - 1) / kWTokens : 0;
 }
 
 template <int D>
@@ -144,6 +148,11 @@ __global__ void __launch_bounds__(32 * kWWarps) kv8_weights_kernel(const AttnPar
     }
 }
 
+int64_t workspace_of(int32_t head_dim, int sms) {
+    const int64_t a = kv8_decode_workspace(head_dim, sms), b = kv8_prefill_workspace(head_dim, sms);
+    return a > b ? a : b;
+}
+
 int launch_weights(const AttnParams &p, int32_t head_dim, int sms, cudaStream_t s) {
     const dim3 grid(2 * sms), block(32 * kWWarps);
     if (head_dim == 64)
@@ -165,7 +174,7 @@ int pkv_kv8_attention_workspace(int32_t num_heads, int32_t head_dim, int64_t *by
     int sms = 0;
     const int rc = pkv::kv8_sm_count(&sms);
     if (rc != PKV_OK) return rc;
-    *bytes = pkv::kv8_decode_workspace(head_dim, sms);
+    *bytes = pkv::workspace_of(head_dim, sms);
     return PKV_OK;
 }
 
@@ -197,7 +206,7 @@ int pkv_kv8_attention(const pkv_kv8_cache *cache, const void *q, int64_t q_strid
     int sms = 0;
     rc = pkv::kv8_sm_count(&sms);
     if (rc != PKV_OK) return rc;
-    if (workspace_bytes < pkv::kv8_decode_workspace(cache->head_dim, sms)) return PKV_ERR_INVALID_ARG;
+    if (workspace_bytes < pkv::workspace_of(cache->head_dim, sms)) return PKV_ERR_INVALID_ARG;
     pkv::AttnParams p = {};
     p.q = static_cast<const char *>(q);
     p.q_stride = q_stride_bytes;
@@ -227,8 +236,18 @@ int pkv_kv8_attention(const pkv_kv8_cache *cache, const void *q, int64_t q_strid
     p.part = reinterpret_cast<float *>(p.meta + static_cast<int64_t>(sms) * 16);
     p.err = d_error;
     cudaStream_t s = pkv::as_stream(stream);
+    // The prefill kernel takes the requests with more than kPrefillRows rows.  It needs head_dim <= 128
+    // (two accumulators beside two score tiles in TMEM) and 16-token groups that lie in one block;
+    // otherwise the decode kernel's row tiles take everything.
+    const bool prefill = cache->head_dim <= 128 && p.bs % 16 == 0 &&
+                         static_cast<int64_t>(num_tokens - n + 1) * p.G > pkv::kPrefillRows && num_tokens > n;
+    p.short_rows = prefill ? pkv::kPrefillRows : 0x7fffffff;
     // one 8-row tile holds every request of a pure decode step
     const bool one_tile = num_tokens <= n && p.G <= 8;
+    if (prefill) {
+        rc = pkv::kv8_launch_prefill(p, cache->head_dim, sms, s);
+        if (rc != PKV_OK) return rc;
+    }
     rc = pkv::kv8_launch_decode(p, cache->head_dim, one_tile, sms, s);
     if (rc != PKV_OK || !weights) return rc;
     return pkv::launch_weights(p, cache->head_dim, sms, s);

@@ -27,7 +27,7 @@ struct AttnParams {
     int32_t window;
     int32_t fp16;
     float scale_log2;              // softmax_scale * log2(e)
-    int32_t short_rows;            // requests with more (query, head) rows than this are another kernel's
+    int32_t short_rows;            // requests with more (query, head) rows than this take the prefill kernel
     float *part;                   // partial results, see pkv_kv8_decode.cu
     int4 *meta;
     int32_t *err;
@@ -42,6 +42,7 @@ struct Req {
     int32_t count;                 // scheduled tokens (0: nothing to do)
     int32_t len;                   // cached tokens, those of this step included
     int32_t lo;                    // first key that any of its queries sees
+    int32_t keys;                  // keys that its block table can name
 };
 
 __device__ __forceinline__ Req request_of(const AttnParams &p, int i, bool report = false) {
@@ -56,6 +57,7 @@ __device__ __forceinline__ Req request_of(const AttnParams &p, int i, bool repor
     }
     const int64_t cap = static_cast<int64_t>(p.W) * p.bs;
     if (r.len > cap && report && p.err && r.count > 0) atomicOr(p.err, PKV_DEVERR_BLOCK);
+    r.keys = r.len < cap ? r.len : static_cast<int32_t>(cap);
     r.lo = 0;
     if (p.window > 0) {
         const int64_t lo = static_cast<int64_t>(r.len) - r.count - p.window + 1;
@@ -63,6 +65,15 @@ __device__ __forceinline__ Req request_of(const AttnParams &p, int i, bool repor
     }
     return r;
 }
+
+// First position that a query at `pos` sees.
+__device__ __forceinline__ int32_t lo_of(const AttnParams &p, int32_t pos) {
+    return p.window > 0 ? max(0, pos - p.window + 1) : 0;
+}
+
+// Value scales below 2^-100 (an unwritten block's zero among them) count as 2^-100, so that their
+// logarithm and reciprocal stay finite.
+__device__ __forceinline__ float value_scale(float s) { return s < 0x1p-100f ? 0x1p-100f : s; }
 
 // Block id of a position, -1 where there is none to read.
 __device__ __forceinline__ int32_t block_of(const AttnParams &p, const int32_t *table, int32_t pos) {
@@ -172,6 +183,10 @@ __device__ __forceinline__ int row_exponent(float largest) {
     return e < -100 ? -100 : e;
 }
 __device__ __forceinline__ float power2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Merge partial results (kv8_merge_kernel in pkv_kv8_decode.cu): worker w's note names a tile of
+// `rows` rows that begins with it and how many workers, `stride` apart, hold a piece of it.
+int kv8_launch_merge(const AttnParams &p, int32_t head_dim, int rows, int workers, int stride, cudaStream_t s);
 
 template <int kBytes>
 __device__ __forceinline__ void cp_async(uint32_t dst, const void *src, bool live) {

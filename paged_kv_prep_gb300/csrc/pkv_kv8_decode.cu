@@ -39,10 +39,6 @@ struct Stage {
     float ks[kUnit], vs[kUnit];
 };
 
-// Value scales below 2^-100 (an unwritten block's zero among them) count as 2^-100, so that their
-// logarithm and reciprocal stay finite.
-__device__ __forceinline__ float value_scale(float s) { return s < 0x1p-100f ? 0x1p-100f : s; }
-
 template <int D, int NT>
 constexpr int warps_of() { return NT == 1 && D <= 128 ? 16 : 8; }
 
@@ -53,7 +49,7 @@ __device__ __forceinline__ int64_t units_of_request(const AttnParams &p, const R
     const int64_t rows = static_cast<int64_t>(r.count) * p.G;
     if (r.count <= 0 || rows > p.short_rows) return 0;
     const int lo = r.lo & ~(kUnit - 1);
-    const int u = r.len > lo ? (r.len - lo + kUnit - 1) / kUnit : 1;
+    const int u = r.keys > lo ? (r.keys - lo + kUnit - 1) / kUnit : 1;   // a request without keys writes zeros
     *per_tile = u;
     return static_cast<int64_t>(u) * ((rows + 8 * NT - 1) / (8 * NT));
 }
@@ -100,7 +96,7 @@ struct Tile {
         const int pos_first = r.len - r.count + first_row / p.G, pos_last = r.len - r.count + last_row / p.G;
         const int base = r.lo & ~(kUnit - 1);
         // keys that some row of the tile sees, and those that every row sees
-        const int some_lo = p.window > 0 ? max(0, pos_first - p.window + 1) : 0, some_hi = pos_last + 1;
+        const int some_lo = p.window > 0 ? max(0, pos_first - p.window + 1) : 0, some_hi = min(pos_last + 1, r.keys);
         const int all_lo = p.window > 0 ? max(0, pos_last - p.window + 1) : 0, all_hi = pos_first + 1;
         ua = max(ua, (some_lo - base) / kUnit);
         ub = min(ub, some_hi > base ? (some_hi - base + kUnit - 1) / kUnit : 0);
@@ -425,7 +421,7 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
                 x.spill(p.part + (2LL * worker + (ua == 0)) * kPart);
                 if (ua == 0) {
                     const int64_t last = ((tile + per) * ranges - 1) / total; // the range with the tile's last unit
-                    note = make_int4(i, rt, static_cast<int>(last), 0);
+                    note = make_int4(i, rt, static_cast<int>(last - range) + 1, head);
                 }
             }
             u = tile + ub;
@@ -434,62 +430,57 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
     if (lane == 0) p.meta[worker] = note;
 }
 
-// Merge the partial results of the tiles that were cut: in each CTA, a warp per row of the tiles
-// that begin with one of its kMergeWorkers workers.
+// Merge the partial results of the tiles that were cut, a warp per (worker, row).
 constexpr int kMergeThreads = 256;
-constexpr int kMergeWorkers = 8;
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnParams p, int workers) {
-    constexpr int kPart = 8 * NT * (D + 2), kRows = 8 * NT, kPer = D / 32;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnParams p, int rows, int workers, int stride) {
+    constexpr int kPer = D / 32;
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int job = warp; job < kMergeWorkers * kRows; job += kMergeThreads / 32) {
-        const int worker = blockIdx.x * kMergeWorkers + job / kRows, row = job % kRows;
-        if (worker >= workers) continue;
-        const int4 note = p.meta[worker];
-        if (note.x < 0) continue;
-        const Req r = request_of(p, note.x);
-        const int f = note.y * kRows + row;
-        if (f >= r.count * p.G) continue;
-        const int range = worker / p.Hkv, head = worker - range * p.Hkv;
-        const int pieces = note.z - range + 1;
-        auto part = [&](int k) {
-            return p.part + (2LL * (worker + static_cast<int64_t>(k) * p.Hkv) + (k == 0)) * kPart;
-        };
-        float top = -INFINITY;
-        for (int k = lane; k < pieces; k += 32) top = fmaxf(top, part(k)[row]);
+    const int lane = threadIdx.x & 31;
+    const int job = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    const int worker = job / rows, row = job - worker * rows;
+    if (worker >= workers) return;
+    const int4 note = p.meta[worker];                // request, row tile, pieces, KV head
+    if (note.x < 0) return;
+    const Req r = request_of(p, note.x);
+    const int64_t f64 = static_cast<int64_t>(note.y) * rows + row;
+    if (f64 >= static_cast<int64_t>(r.count) * p.G) return;
+    const int f = static_cast<int>(f64), pieces = note.z, head = note.w;
+    const int64_t size = static_cast<int64_t>(rows) * (D + 2);
+    auto part = [&](int k) { return p.part + (2LL * (worker + static_cast<int64_t>(k) * stride) + (k == 0)) * size; };
+    float top = -INFINITY;
+    for (int k = lane; k < pieces; k += 32) top = fmaxf(top, part(k)[row]);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-        float sum = 0.f, acc[kPer];
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    float sum = 0.f, acc[kPer];
 #pragma unroll
-        for (int c = 0; c < kPer; c++) acc[c] = 0.f;
+    for (int c = 0; c < kPer; c++) acc[c] = 0.f;
 #pragma unroll 8
-        for (int k = 0; k < pieces; k++) {
-            const float *a = part(k);
-            const float m = a[row], l = a[kRows + row];
-            // a piece without a top adds nothing, unless its logits were NaN
-            const float f2 = m == -INFINITY ? (l == 0.f ? 0.f : NAN) : exp2_fast(m - top);
-            sum += f2 * l;
-            const float *o = a + 2 * kRows + row * D + lane * kPer;
+    for (int k = 0; k < pieces; k++) {
+        const float *a = part(k);
+        const float m = a[row], l = a[rows + row];
+        // a piece without a top adds nothing, unless its logits were NaN
+        const float f2 = m == -INFINITY ? (l == 0.f ? 0.f : NAN) : exp2_fast(m - top);
+        sum += f2 * l;
+        const float *o = a + 2 * rows + row * D + lane * kPer;
 #pragma unroll
-            for (int c = 0; c < kPer; c += 2) {
-                const float2 y = *reinterpret_cast<const float2 *>(o + c);
-                acc[c] += f2 == 0.f ? 0.f : f2 * y.x;
-                acc[c + 1] += f2 == 0.f ? 0.f : f2 * y.y;
-            }
+        for (int c = 0; c < kPer; c += 2) {
+            const float2 y = *reinterpret_cast<const float2 *>(o + c);
+            acc[c] += f2 == 0.f ? 0.f : f2 * y.x;
+            acc[c + 1] += f2 == 0.f ? 0.f : f2 * y.y;
         }
-        const bool none = top == -INFINITY && sum == 0.f;
-        const int j = f / p.G, hq = head * p.G + f - j * p.G;
-        const float inv = none ? 0.f : 1.f / sum;
-        char *out = p.out + static_cast<int64_t>(r.start + j) * p.out_stride + 2 * (static_cast<int64_t>(hq) * D + lane * kPer);
-#pragma unroll
-        for (int c = 0; c < kPer; c += 2)
-            *reinterpret_cast<uint32_t *>(out + 2 * c) = pack_out(acc[c] * inv, acc[c + 1] * inv, p.fp16);
-        if (lane == 0 && p.lse)
-            p.lse[static_cast<int64_t>(r.start + j) * p.Hkv * p.G + hq] = none ? -INFINITY : (top + log2f(sum)) * kLn2;
     }
+    const bool none = top == -INFINITY && sum == 0.f;
+    const int j = f / p.G, hq = head * p.G + f - j * p.G;
+    const float inv = none ? 0.f : 1.f / sum;
+    char *out = p.out + static_cast<int64_t>(r.start + j) * p.out_stride + 2 * (static_cast<int64_t>(hq) * D + lane * kPer);
+#pragma unroll
+    for (int c = 0; c < kPer; c += 2)
+        *reinterpret_cast<uint32_t *>(out + 2 * c) = pack_out(acc[c] * inv, acc[c + 1] * inv, p.fp16);
+    if (lane == 0 && p.lse)
+        p.lse[static_cast<int64_t>(r.start + j) * p.Hkv * p.G + hq] = none ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 template <int D, int NT>
@@ -505,10 +496,7 @@ int launch(const AttnParams &p, int sms, cudaStream_t s) {
         if (dev >= 0 && dev < 64) set[dev] = true;
     }
     PKV_CUDA_TRY(launch_pdl(kv8_decode_kernel<D, NT>, dim3(sms), dim3(32 * kWarps), smem, s, p));
-    const int workers = sms * kWarps;
-    PKV_CUDA_TRY(launch_pdl(kv8_merge_kernel<D, NT>, dim3((workers + kMergeWorkers - 1) / kMergeWorkers),
-                            dim3(kMergeThreads), 0, s, p, workers));
-    return PKV_OK;
+    return kv8_launch_merge(p, D, 8 * NT, sms * kWarps, p.Hkv, s);
 }
 
 template <int D>
@@ -517,6 +505,17 @@ int launch_rows(const AttnParams &p, bool one_tile, int sms, cudaStream_t s) {
 }
 
 }  // namespace
+
+int kv8_launch_merge(const AttnParams &p, int32_t head_dim, int rows, int workers, int stride, cudaStream_t s) {
+    const dim3 grid((static_cast<unsigned>(workers) * rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32)), block(kMergeThreads);
+    if (head_dim == 64)
+        PKV_CUDA_TRY(launch_pdl(kv8_merge_kernel<64>, grid, block, 0, s, p, rows, workers, stride));
+    else if (head_dim == 128)
+        PKV_CUDA_TRY(launch_pdl(kv8_merge_kernel<128>, grid, block, 0, s, p, rows, workers, stride));
+    else
+        PKV_CUDA_TRY(launch_pdl(kv8_merge_kernel<256>, grid, block, 0, s, p, rows, workers, stride));
+    return PKV_OK;
+}
 
 int64_t kv8_decode_workspace(int32_t head_dim, int sms) {
     // the widest variant: 16 workers an SM, two partial results each of 16 rows

@@ -333,3 +333,64 @@ def test_no_tokens():
     q, kc, vc, ks, vs, tab, qsl, lens = case.args()
     out, lse = pkv.kv8_attention(q[:0], kc, vc, ks, vs, tab[:0], qsl[:1], lens[:0])
     assert out.shape == (0, 1, 64) and lse.shape == (0, 1)
+
+
+CHUNKS = [(1, 20), (9, 9), (33, 33), (64, 64), (65, 200), (130, 131), (200, 1500), (257, 700)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("heads,group,d", [(2, 4, 128), (1, 8, 128), (3, 1, 128), (2, 5, 64), (1, 33, 64)])
+def test_chunks_match_plain(heads, group, d, dtype):
+    """Prompt chunks: row tiles of one and two halves, odd lengths, ranges cut inside a tile."""
+    check(Case(CHUNKS, 16, heads, group, d, dtype, seed=heads * 10 + group))
+
+
+@pytest.mark.parametrize("window", [1, 17, 100, 128, 1000])
+@pytest.mark.parametrize("bs", [16, 48])
+def test_chunks_with_windows(window, bs):
+    case = Case(CHUNKS, bs, 1, 4, 128, seed=window + bs)
+    for i, (c, x) in enumerate(CHUNKS):                     # blocks before the window are freed
+        case.tables[i, :max(0, x - c - window + 1) // bs] = -1
+    check(case, window=window)
+
+
+def test_chunks_that_see_little():
+    """Chunks longer than their cache, freed blocks in the middle, far-apart value scales, a negative scale."""
+    case = Case([(60, 30), (50, 50), (40, 300), (90, 200)], 16, 2, 4, 128, seed=3)
+    case.tables[1, 0] = -1
+    case.tables[2, 3:12] = -1
+    out, lse = check(case)
+    assert (lse[:30] == -math.inf).all() and (out[:30] == 0).all() and (lse[60:76] == -math.inf).all()
+    check(Case([(40, 100), (100, 300)], 16, 2, 4, 128, seed=4, spread=18))
+    check(Case([(40, 100), (100, 300)], 16, 2, 4, 64, seed=5), scale=-0.2)
+
+
+def test_chunks_nan_stays_in_its_rows():
+    case = Case([(120, 200), (40, 40), (64, 500)], 16, 2, 4, 128, seed=8)
+    b = case.tables
+    case.caches[1][int(b[0, 9]) * 16 + 5, 0, 3] = 127        # position 149: queries 69.. of request 0, head 0
+    case.caches[1][int(b[0, 9]) * 16 + 7, 0, 101] = 255
+    case.caches[0][int(b[1, 1]) * 16 + 6, 1, 9] = 255        # position 22: queries 22.. of request 1, head 1
+    case.q = case.q.clone()
+    case.q[170, 0, 0] = math.nan
+    scale = case.d ** -0.5
+    w = torch.zeros(case.blocks * case.bs, device="cuda")
+    out, lse = pkv.kv8_attention(*case.args(), softmax_scale=scale)
+    w_out, w_lse, size, reach = case.reference(scale, 0)
+    assert w_out.isnan().any() and not w_out[:60].isnan().any()
+    assert torch.equal(out.cpu().isnan(), w_out.isnan()) and torch.equal(lse.cpu().isnan(), w_lse.isnan())
+    ok = ~w_out.isnan()
+    assert (out.cpu().double() - w_out)[ok].abs().max() < 0.05 * w_out[ok].abs().max()
+    # a NaN value changes no weight: request 0 keeps its sums
+    pkv.kv8_attention(*case.args(), softmax_scale=scale, weights=w)
+    slots = (b[0, :12].long()[:, None] * 16 + torch.arange(16)).view(-1)
+    assert torch.isfinite(w.cpu()[slots]).all()
+
+
+def test_chunks_repeat_bit_identically():
+    case = Case([(1, 900), (100, 3000), (300, 333)], 16, 2, 4, 128, seed=12)
+    a = case.args()
+    first = pkv.kv8_attention(*a)
+    for _ in range(5):
+        again = pkv.kv8_attention(*a)
+        assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
