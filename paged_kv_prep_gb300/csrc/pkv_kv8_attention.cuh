@@ -31,6 +31,12 @@ struct AttnParams {
     float *part;                   // partial results, see pkv_kv8_decode.cu
     int4 *meta;
     int32_t *err;
+
+    // The table's entry for a position, unchecked but for the table's end (-1 past it).
+    __device__ __forceinline__ int32_t table_at(const int32_t *table, int32_t pos) const {
+        const int32_t j = pos / bs;
+        return j < W ? table[j] : -1;
+    }
 };
 
 constexpr float kLn2 = 0.6931471805599453f;
@@ -77,9 +83,7 @@ __device__ __forceinline__ float value_scale(float s) { return s < 0x1p-100f ? 0
 
 // Block id of a position, -1 where there is none to read.
 __device__ __forceinline__ int32_t block_of(const AttnParams &p, const int32_t *table, int32_t pos) {
-    const int32_t j = pos / p.bs;
-    if (j >= p.W) return -1;
-    const int32_t b = table[j];
+    const int32_t b = p.table_at(table, pos);
     if (b >= p.num_blocks) {
         if (p.err) atomicOr(p.err, PKV_DEVERR_BLOCK);
         return -1;

@@ -35,6 +35,7 @@ constexpr int kKeys = 128;              // tokens per unit
 constexpr int kSub = kKeys / 16;
 constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 1);
+static_assert((kThreads + 1 + kThreads / 32) * 8 <= 2 * kKeys * 64, "the plan's sums lie in the raw codes' place");
 constexpr uint32_t kTries = 1u << 19;   // polls of about a microsecond before a wait gives up
 constexpr float kSlack = 8.f;           // growth of a row's maximum (log2) that R does not follow
 
@@ -43,10 +44,9 @@ struct Smem {
     char q[2][128 * D * 2];
     char k[2][kKeys * D * 2];
     char v[2][kKeys * D * 2];
+    char raw[2][kKeys * D];             // codes of the unit that is converted next: keys, values
     float ks[4][kSub], lv[4][kSub], iv[4][kSub];   // per 16 tokens: k_scale, log2(v_scale), 1 / v_scale
     uint64_t q_full[2], k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2], o_full[2], done;
-    int64_t prefix[kThreads + 1];
-    int64_t warp_sum[kThreads / 32];
     uint32_t tmem;
     int32_t failed;
     int32_t nan_seen;                   // this CTA has met a V code that is NaN
@@ -90,8 +90,8 @@ struct Walk {
     int i, rt;
     int64_t rt_first;                   // first unit of the row tile `rt`
 
-    __device__ __forceinline__ Walk(const AttnParams &p_, const Smem<D> &sm, int64_t u0, int64_t u1) : p(p_), u(u0), end(u1) {
-        i = plan_find<kThreads>(sm.prefix, p.n, u, [&](int k) { return units_of_request(p, request_of(p, k)); }, &first);
+    __device__ __forceinline__ Walk(const AttnParams &p_, const int64_t *prefix, int64_t u0, int64_t u1) : p(p_), u(u0), end(u1) {
+        i = plan_find<kThreads>(prefix, p.n, u, [&](int k) { return units_of_request(p, request_of(p, k)); }, &first);
         rt = 0;
         rt_first = first;
     }
@@ -139,9 +139,79 @@ __device__ __forceinline__ bool wait(Smem<D> *sm, uint64_t *bar, uint32_t parity
     return false;
 }
 
+// The loops over 32 columns are not unrolled: the body of a whole unit would not stay in the
+// instruction cache beside the other warps' code.
+
+// Largest x of a row in the unit (columns lo .. hi where not kWhole).
+template <int D, bool kWhole>
+__device__ __forceinline__ float row_max(const Smem<D> *sm, uint32_t ts, int ring, float cf, int lo, int hi) {
+    float most = -INFINITY;
+#pragma unroll 1
+    for (int c = 0; c < 4; c++) {
+        uint32_t s[32];
+        tmem_ld32(s, ts + 32 * c);
+        const float2 ks = *reinterpret_cast<const float2 *>(&sm->ks[ring][2 * c]);
+        const float2 lv = *reinterpret_cast<const float2 *>(&sm->lv[ring][2 * c]);
+        tc_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            if (!kWhole) {
+#pragma unroll
+                for (int k = 0; k < 16; k++) {
+                    const int col = 32 * c + 16 * h + k;
+                    if (col > hi || col < lo) s[16 * h + k] = 0xff800000u;
+                }
+            }
+            float mx = __uint_as_float(s[16 * h]);
+#pragma unroll
+            for (int k = 1; k < 15; k += 2) mx = max3(mx, __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]));
+            mx = fmaxf(mx, __uint_as_float(s[16 * h + 15]));
+            const float x = fmaf(mx, cf * (h ? ks.y : ks.x), h ? lv.y : lv.x);
+            most = fmaxf(most, mx == -INFINITY ? -INFINITY : x);
+        }
+    }
+    return most;
+}
+
+// w = 2^(x - ref) as f16 in the place of S, and the row's softmax sum over the unit.
+template <int D, bool kWhole>
+__device__ __forceinline__ float row_weights(const Smem<D> *sm, uint32_t ts, int ring, float cf, float ref, int lo, int hi) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 4; c++) {
+        uint32_t s[32], w[16];
+        tmem_ld32(s, ts + 32 * c);
+        const float2 ks = *reinterpret_cast<const float2 *>(&sm->ks[ring][2 * c]);
+        const float2 lv = *reinterpret_cast<const float2 *>(&sm->lv[ring][2 * c]);
+        const float2 iv = *reinterpret_cast<const float2 *>(&sm->iv[ring][2 * c]);
+        tc_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const float a = cf * (h ? ks.y : ks.x), b = (h ? lv.y : lv.x) - ref;
+            const uint64_t aa = pair_of(a, a), bb = pair_of(b, b);
+            uint64_t part = 0;
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+                const uint64_t x = fma2(pair_of(__uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1])), aa, bb);
+                float y0 = exp2_fast(low_of(x)), y1 = exp2_fast(high_of(x));
+                if (!kWhole) {
+                    const int col = 32 * c + 16 * h + k;
+                    if (col > hi || col < lo) y0 = 0.f;
+                    if (col + 1 > hi || col + 1 < lo) y1 = 0.f;
+                }
+                part = add2(part, pair_of(y0, y1));
+                w[8 * h + k / 2] = pack_f16(y0, y1);
+            }
+            sum = fmaf(low_of(part) + high_of(part), h ? iv.y : iv.x, sum);
+        }
+        tmem_st16(ts + 16 * c, w);
+    }
+    return sum;
+}
+
 // ---- softmax warps: a thread per row ----------------------------------------------------------
 template <int D>
-__device__ void softmax_role(const AttnParams &p, Smem<D> *sm, int64_t u0, int64_t u1, int64_t total, int64_t ranges) {
+__device__ void softmax_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk, int64_t total, int64_t ranges) {
     constexpr int kPart = kRows * (D + 2);
     const int m = threadIdx.x >> 7, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;      // TMEM lane of the warp
@@ -150,7 +220,6 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> *sm, int64_t u0, int64
     char *qs = sm->q[m];
     uint32_t unit = 0, s_phase = 0, o_phase = 0;
     int4 note = make_int4(-1, 0, 0, 0);
-    Walk<D> walk(p, *sm, u0, u1);
     Item x;
     while (walk.next(x)) {
         const int nu = x.ub - x.ua;
@@ -215,29 +284,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> *sm, int64_t u0, int64
             const bool whole = s0 + kKeys - 1 <= pos0 && (p.window <= 0 || s0 > pos1 - p.window);
             const int hi = pos - s0;                                         // columns lo .. hi are visible
             const int lo = p.window > 0 ? pos - p.window + 1 - s0 : -0x7fffffff;
-            float most = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 4; c++) {
-                uint32_t s[32];
-                tmem_ld32(s, ts + 32 * c);
-                tc_wait_ld();
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    float mx = -INFINITY;
-                    if (whole) {
-#pragma unroll
-                        for (int k = 0; k < 16; k++) mx = fmaxf(mx, __uint_as_float(s[16 * h + k]));
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 16; k++) {
-                            const int col = 32 * c + 16 * h + k;
-                            mx = fmaxf(mx, col <= hi && col >= lo ? __uint_as_float(s[16 * h + k]) : -INFINITY);
-                        }
-                    }
-                    const float a = cf * sm->ks[ring][2 * c + h], lv = sm->lv[ring][2 * c + h];
-                    most = fmaxf(most, mx == -INFINITY ? -INFINITY : fmaf(mx, a, lv));
-                }
-            }
+            const float most = whole ? row_max<D, true>(sm, ts, ring, cf, lo, hi) : row_max<D, false>(sm, ts, ring, cf, lo, hi);
             const bool grow = most > top + kSlack || (top == -INFINITY && most > -INFINITY);
             if (__any_sync(~0u, grow)) {
                 const float f2 = grow ? exp2_fast(top - most) : 1.f;
@@ -256,31 +303,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> *sm, int64_t u0, int64
                 }
             }
             const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-            for (int c = 0; c < 4; c++) {
-                uint32_t s[32], w[16];
-                tmem_ld32(s, ts + 32 * c);
-                tc_wait_ld();
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const float a = cf * sm->ks[ring][2 * c + h], b = sm->lv[ring][2 * c + h] - ref;
-                    float part = 0.f;
-#pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        float y0 = exp2_fast(fmaf(__uint_as_float(s[16 * h + k]), a, b));
-                        float y1 = exp2_fast(fmaf(__uint_as_float(s[16 * h + k + 1]), a, b));
-                        if (!whole) {
-                            const int col = 32 * c + 16 * h + k;
-                            y0 = col <= hi && col >= lo ? y0 : 0.f;
-                            y1 = col + 1 <= hi && col + 1 >= lo ? y1 : 0.f;
-                        }
-                        part += y0 + y1;
-                        w[8 * h + k / 2] = pack_f16(y0, y1);
-                    }
-                    sum = fmaf(part, sm->iv[ring][2 * c + h], sum);
-                }
-                tmem_st16(ts + 16 * c, w);
-            }
+            sum += whole ? row_weights<D, true>(sm, ts, ring, cf, ref, lo, hi) : row_weights<D, false>(sm, ts, ring, cf, ref, lo, hi);
             tc_wait_st();
             tc_fence_before();
             mbar_arrive(&sm->p_full[m]);
@@ -350,146 +373,176 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> *sm, int64_t u0, int64
 }
 
 // ---- converting warps: codes to f16 operand tiles ---------------------------------------------
+// What a unit's copies need: for the 16-token group (lane & 7), where its codes begin (-1: not
+// read) and its scales; klo, khi: the unit's tokens that some row sees.
+struct Feed {
+    int64_t at;
+    int klo, khi;
+    float ks, vs;
+};
+
 template <int D>
-__device__ void convert_role(const AttnParams &p, Smem<D> *sm, int64_t u0, int64_t u1) {
+__device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
     constexpr int kC = D / 16;                       // 16-byte pieces of a token's codes
-    constexpr int kTok = 128 / kC;                   // tokens per round of the 128 threads
+    constexpr int kTok = 128 / kC;                   // tokens per round of the 128 threads: 16 or 32
     constexpr int kRounds = kKeys / kTok;
     const int i = threadIdx.x - 32 * kSoftWarps, lane = i & 31;
     const int c = i % kC, tok = i / kC;              // this thread's piece, and its token within a round
     const int64_t line = static_cast<int64_t>(p.Hkv) * D;
+    const int64_t mine = (tok & 15) * line + 16 * c; // this thread's place within a group of 16 tokens
+    // places of the two halves of 16 converted codes; threads of the upper 64 dimensions write
+    // their second half first, so that eight neighbours write to eight bank groups
+    const int second = (c >> 2) & 1;
+    const uint32_t row = (c >> 2) * (kKeys * 128) + tok * 128;
+    const uint32_t to0 = row + ((((c & 3) * 2 + second) ^ (tok & 7)) << 4);
+    const uint32_t to1 = row + ((((c & 3) * 2 + (second ^ 1)) ^ (tok & 7)) << 4);
 
-    Walk<D> walk(p, *sm, u0, u1);
     Item x;
+    int t = 0;
     bool more = walk.next(x);
-    int t = x.ua;
-    // block id of 16-token group (lane & 7) of unit t, -1 where no row of the item sees it
-    auto groups = [&]() {
-        const int s = x.s.base + t * kKeys + 16 * (lane & 7);
-        return s < x.s.hi && s + 16 > x.s.lo ? block_of(p, x.table, s) : -1;
-    };
-    auto load = [&](uint4 (&y)[kRounds], const uint8_t *cache, int blocks, const Item &it, int tu) {
-#pragma unroll
-        for (int r = 0; r < kRounds; r++) {
-            const int k = r * kTok + tok;            // token of the unit
-            const int b = __shfl_sync(~0u, blocks, k >> 4);
-            const int s = it.s.base + tu * kKeys + k;
-            y[r] = make_uint4(0, 0, 0, 0);
-            if (b >= 0 && s >= it.s.lo && s < it.s.hi)
-                y[r] = __ldg(reinterpret_cast<const uint4 *>(cache + (static_cast<int64_t>(b) * p.bs + s % p.bs) * line +
-                                                             it.head * D + 16 * c));
-        }
-    };
-    auto lay = [&](const uint4 (&y)[kRounds], char *dst) {
-#pragma unroll
-        for (int r = 0; r < kRounds; r++) {
-            const int k = r * kTok + tok;
-            const uint32_t w[4] = {y[r].x, y[r].y, y[r].z, y[r].w};
-            uint4 h[2];
-            h[0] = make_uint4(f16x2_of(w[0]), f16x2_of(w[0] >> 16), f16x2_of(w[1]), f16x2_of(w[1] >> 16));
-            h[1] = make_uint4(f16x2_of(w[2]), f16x2_of(w[2] >> 16), f16x2_of(w[3]), f16x2_of(w[3] >> 16));
-            char *panel = dst + (c >> 2) * (kKeys * 128) + k * 128;
-            // the upper panel's threads write their second half first: eight neighbours, eight bank groups
-            const int first = (c >> 2) & 1;
-#pragma unroll
-            for (int g = 0; g < 2; g++) {
-                const int half = g ^ first;
-                *reinterpret_cast<uint4 *>(panel + ((((c & 3) * 2 + half) ^ (k & 7)) << 4)) = half ? h[1] : h[0];
-            }
-        }
-    };
     if (!more) return;
-    uint4 kreg[kRounds], vreg[kRounds];
-    int blocks = groups();
-    load(kreg, p.kc, blocks, x, t);
-    uint32_t unit = 0;
-    bool ok = true;
-    while (more && ok) {
-        load(vreg, p.vc, blocks, x, t);
-        const int stage = unit & 1;
-        const uint32_t parity = ((unit >> 1) & 1) ^ 1;
-        ok = wait(sm, &sm->k_free[stage], parity);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
-        if (i < kSub) {
-            // i == lane & 7 here: this thread knows the group's block
-            const int64_t at = static_cast<int64_t>(blocks) * p.Hkv + x.head;
-            const int ring = unit & 3;
-            float k = 0.f, lv = -INFINITY, iv = 0.f;
-            if (blocks >= 0) {
-                k = p.ks[at];
-                const float v = value_scale(p.vs[at]);
-                lv = __log2f(v);
-                iv = __frcp_rn(v);
-            }
-            sm->ks[ring][i] = k;
-            sm->lv[ring][i] = lv;
-            sm->iv[ring][i] = iv;
+    t = x.ua;
+    // a block id that has been asked for but not yet looked at
+    int32_t id = -1;
+    auto ask = [&]() {
+        const int s = x.s.base + t * kKeys + 16 * (lane & 7);
+        id = -1;
+        if (s < x.s.hi && s + 16 > x.s.lo) id = p.table_at(x.table, s);
+    };
+    auto resolve = [&]() {
+        Feed f;
+        const int s = x.s.base + t * kKeys + 16 * (lane & 7);
+        if (id >= p.num_blocks) {
+            if (p.err) atomicOr(p.err, PKV_DEVERR_BLOCK);
+            id = -1;
         }
-        lay(kreg, sm->k[stage]);
-        fence_async_shared();
-        mbar_arrive(&sm->k_full[stage]);
-        // the next unit's keys are on their way while this unit's values are laid out
+        f.at = -1;
+        f.ks = 0.f;
+        f.vs = -1.f;                                 // no block
+        if (id >= 0) {
+            f.at = (static_cast<int64_t>(id) * p.bs + s % p.bs) * line + x.head * D;
+            if (i < kSub) {
+                f.ks = p.ks[static_cast<int64_t>(id) * p.Hkv + x.head];
+                f.vs = p.vs[static_cast<int64_t>(id) * p.Hkv + x.head];
+            }
+        }
+        f.klo = x.s.lo - x.s.base - t * kKeys;
+        f.khi = x.s.hi - x.s.base - t * kKeys;
+        return f;
+    };
+    auto advance = [&]() {
         t++;
-        const bool last = t == x.ub;
-        if (last) {
+        if (t == x.ub) {
             more = walk.next(x);
             t = x.ua;
         }
-        if (more) {
-            blocks = groups();
-            load(kreg, p.kc, blocks, x, t);
-        }
-        ok = wait(sm, &sm->v_free[stage], parity);
-        ok = __all_sync(~0u, ok);
-        if (!ok) break;
-        {
-            bool nan = false;
-#pragma unroll
-            for (int r = 0; r < kRounds; r++) {
-                uint32_t *w = reinterpret_cast<uint32_t *>(&vreg[r]);
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    // 0x7f + 1 carries into the sign bit of its byte
-                    if ((((w[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
-                        w[k] &= ~__vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                        nan = true;
-                    }
+        if (more) ask();
+    };
+    // Each thread copies its own 16-byte pieces and reads only those back: no barrier.
+    auto fetch = [&](const uint8_t *cache, const Feed &f, int r, char *raw) {
+        const int k = r * kTok + tok;
+        const int64_t from = __shfl_sync(~0u, f.at, k >> 4);
+        const bool live = from >= 0 && k >= f.klo && k < f.khi;
+        cp_async<16>(smem_addr(raw + r * 2048 + i * 16), cache + (live ? from + mine : 0), live);
+    };
+    // Turn a half (keys or values) of unit `a` into f16, and refill its pieces with the next unit's.
+    auto half = [&](const uint8_t *cache, char *raw, char *dst, const Feed &b, bool next, bool values) {
+        bool nan = false;
+#pragma unroll 2
+        for (int r = 0; r < kRounds; r++) {
+            uint4 y = *reinterpret_cast<const uint4 *>(raw + r * 2048 + i * 16);
+            if (values) {
+                // 0x7f + 1 carries into the sign bit of its byte: NaN codes leave the product (the
+                // softmax warps bring them back for the rows that see their token)
+                const uint32_t hit = ((y.x & 0x7f7f7f7fu) + 0x01010101u) | ((y.y & 0x7f7f7f7fu) + 0x01010101u) |
+                                     ((y.z & 0x7f7f7f7fu) + 0x01010101u) | ((y.w & 0x7f7f7f7fu) + 0x01010101u);
+                if (hit & 0x80808080u) {
+                    y.x &= ~__vcmpeq4(y.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    y.y &= ~__vcmpeq4(y.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    y.z &= ~__vcmpeq4(y.z & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    y.w &= ~__vcmpeq4(y.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    nan = true;
                 }
             }
-            if (nan) *static_cast<volatile int32_t *>(&sm->nan_seen) = 1;
+            const uint4 h0 = make_uint4(f16x2_of(y.x), f16x2_of(y.x >> 16), f16x2_of(y.y), f16x2_of(y.y >> 16));
+            const uint4 h1 = make_uint4(f16x2_of(y.z), f16x2_of(y.z >> 16), f16x2_of(y.w), f16x2_of(y.w >> 16));
+            *reinterpret_cast<uint4 *>(dst + to0 + r * kTok * 128) = second ? h1 : h0;
+            *reinterpret_cast<uint4 *>(dst + to1 + r * kTok * 128) = second ? h0 : h1;
+            if (next) fetch(cache, b, r, raw);
         }
-        lay(vreg, sm->v[stage]);
+        if (nan) *static_cast<volatile int32_t *>(&sm->nan_seen) = 1;
+        cp_commit();
+    };
+
+    ask();
+    Feed a = resolve();
+#pragma unroll 1
+    for (int r = 0; r < kRounds; r++) fetch(p.kc, a, r, sm->raw[0]);
+    cp_commit();
+#pragma unroll 1
+    for (int r = 0; r < kRounds; r++) fetch(p.vc, a, r, sm->raw[1]);
+    cp_commit();
+    advance();
+    bool ok = true, now = true;
+    for (uint32_t unit = 0; now; unit++) {
+        const bool next = more;
+        Feed b = {};
+        if (next) {
+            b = resolve();
+            advance();                               // the block ids of the unit after it are on their way
+        }
+        const int stage = unit & 1;
+        const uint32_t parity = ((unit >> 1) & 1) ^ 1;
+        cp_wait<1>();
+        ok = wait(sm, &sm->k_free[stage], parity);
+        if (!__all_sync(~0u, ok)) break;
+        if (i < kSub) {
+            const int ring = unit & 3;
+            const bool named = a.at >= 0;
+            const float v = value_scale(a.vs);
+            sm->ks[ring][i] = named ? a.ks : 0.f;
+            sm->lv[ring][i] = named ? __log2f(v) : -INFINITY;
+            sm->iv[ring][i] = named ? __frcp_rn(v) : 0.f;
+        }
+        half(p.kc, sm->raw[0], sm->k[stage], b, next, false);
+        fence_async_shared();
+        mbar_arrive(&sm->k_full[stage]);
+        cp_wait<1>();
+        ok = wait(sm, &sm->v_free[stage], parity);
+        if (!__all_sync(~0u, ok)) break;
+        half(p.vc, sm->raw[1], sm->v[stage], b, next, true);
         fence_async_shared();
         mbar_arrive(&sm->v_full[stage]);
-        unit++;
+        a = b;
+        now = next;
     }
+    cp_wait<0>();
 }
 
 // ---- issuing thread ----------------------------------------------------------------------------
 template <int D>
-__device__ void issue_role(const AttnParams &p, Smem<D> *sm, int64_t u0, int64_t u1) {
+__device__ void issue_role(Smem<D> *sm, Walk<D> &walk) {
     constexpr uint32_t kQk = f16_idesc(128, kKeys, false), kPv = f16_idesc(128, D, true);
     const uint32_t tmem = sm->tmem;
     uint32_t unit = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-    Walk<D> walk(p, *sm, u0, u1);
     Item x;
     bool ok = true;
     auto qk = [&](int m, int stage) {
         const uint32_t a = smem_addr(sm->q[m]), b = smem_addr(sm->k[stage]);
-#pragma unroll
+        const uint64_t da = smem_desc(a, 16), db = smem_desc(b, 16);
+#pragma unroll 1
         for (int k = 0; k < D / 16; k++) {
-            const uint32_t off = (k >> 2) * (128 * 128) + (k & 3) * 32;
-            mma_ss(tmem + m * 128, smem_desc(a + off, 16), smem_desc(b + off, 16), kQk, k > 0);
+            const uint64_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+            mma_ss(tmem + m * 128, da + off, db + off, kQk, k > 0);
         }
         mbar_arrive(&sm->s_full[m]);
         tc_commit(&sm->s_full[m]);
     };
     auto pv = [&](int m, int stage, bool add) {
-        const uint32_t b = smem_addr(sm->v[stage]);
-#pragma unroll
+        const uint64_t db = smem_desc(smem_addr(sm->v[stage]), kKeys * 128);
+#pragma unroll 1
         for (int k = 0; k < kKeys / 16; k++)
-            mma_ts(tmem + 256 + m * D, tmem + m * 128 + 8 * k, smem_desc(b + k * 2048, kKeys * 128), kPv, add || k > 0);
+            mma_ts(tmem + 256 + m * D, tmem + m * 128 + 8 * k, db + k * (2048 >> 4), kPv, add || k > 0);
     };
     while (ok && walk.next(x)) {
         const int nu = x.ub - x.ua;
@@ -561,18 +614,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const AttnPara
     tc_fence_after();
     pdl_wait();
     pdl_trigger();
-    const int64_t total = plan_prefix<kThreads>(sm->prefix, sm->warp_sum, p.n, [&](int i) {
+    int64_t *prefix = reinterpret_cast<int64_t *>(sm->raw);
+    const int64_t total = plan_prefix<kThreads>(prefix, prefix + kThreads + 1, p.n, [&](int i) {
         return units_of_request(p, request_of(p, i, blockIdx.x == 0));
     });
     const int64_t ranges = total < gridDim.x ? total : gridDim.x;
-    const int64_t u0 = ranges ? blockIdx.x * total / ranges : 0, u1 = ranges ? (blockIdx.x + 1) * total / ranges : 0;
     if (blockIdx.x < ranges) {
+        Walk<D> walk(p, prefix, blockIdx.x * total / ranges, (blockIdx.x + 1) * total / ranges);
+        __syncthreads();                             // the sums' place is the converting warps' from here on
         if (warp < kSoftWarps)
-            softmax_role<D>(p, sm, u0, u1, total, ranges);
+            softmax_role<D>(p, sm, walk, total, ranges);
         else if (warp < kSoftWarps + kConvWarps)
-            convert_role<D>(p, sm, u0, u1);
+            convert_role<D>(p, sm, walk);
         else if ((threadIdx.x & 31) == 0)
-            issue_role<D>(p, sm, u0, u1);
+            issue_role<D>(sm, walk);
     } else if (threadIdx.x == 0) {
         p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
