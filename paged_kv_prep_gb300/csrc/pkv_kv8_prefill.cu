@@ -36,7 +36,7 @@ constexpr int kSub = kKeys / 16;
 constexpr int kSoftWarps = 8, kConvWarps = 4;
 constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 1);
 static_assert((kThreads + 1 + kThreads / 32) * 8 <= 2 * kKeys * 64, "the plan's sums lie in the raw codes' place");
-constexpr uint32_t kTries = 1u << 19;   // polls of about a microsecond before a wait gives up
+constexpr uint32_t kTries = 1u << 22;   // polls before a wait gives up (half a second or more)
 constexpr float kSlack = 8.f;           // growth of a row's maximum (log2) that R does not follow
 
 template <int D>
@@ -130,10 +130,11 @@ struct Walk {
 
 template <int D>
 __device__ __forceinline__ bool wait(Smem<D> *sm, uint64_t *bar, uint32_t parity) {
+    if (mbar_try(bar, parity)) return true;
     volatile int32_t *failed = &sm->failed;
     for (uint32_t k = 0; k < kTries; k++) {
-        if (mbar_wait(bar, parity, 1)) return true;
-        if (*failed) return false;
+        if (mbar_try(bar, parity)) return true;
+        if ((k & 63) == 63 && *failed) return false;
     }
     *failed = 1;
     return false;
@@ -448,27 +449,43 @@ __device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
     // Turn a half (keys or values) of unit `a` into f16, and refill its pieces with the next unit's.
     auto half = [&](const uint8_t *cache, char *raw, char *dst, const Feed &b, bool next, bool values) {
         bool nan = false;
-#pragma unroll 2
-        for (int r = 0; r < kRounds; r++) {
-            uint4 y = *reinterpret_cast<const uint4 *>(raw + r * 2048 + i * 16);
+#pragma unroll 1
+        for (int r0 = 0; r0 < kRounds; r0 += 4) {
+            uint4 y[4];
+#pragma unroll
+            for (int r = 0; r < 4; r++) y[r] = *reinterpret_cast<const uint4 *>(raw + (r0 + r) * 2048 + i * 16);
             if (values) {
                 // 0x7f + 1 carries into the sign bit of its byte: NaN codes leave the product (the
                 // softmax warps bring them back for the rows that see their token)
-                const uint32_t hit = ((y.x & 0x7f7f7f7fu) + 0x01010101u) | ((y.y & 0x7f7f7f7fu) + 0x01010101u) |
-                                     ((y.z & 0x7f7f7f7fu) + 0x01010101u) | ((y.w & 0x7f7f7f7fu) + 0x01010101u);
+                uint32_t hit = 0;
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+                    hit |= ((y[r].x & 0x7f7f7f7fu) + 0x01010101u) | ((y[r].y & 0x7f7f7f7fu) + 0x01010101u) |
+                           ((y[r].z & 0x7f7f7f7fu) + 0x01010101u) | ((y[r].w & 0x7f7f7f7fu) + 0x01010101u);
                 if (hit & 0x80808080u) {
-                    y.x &= ~__vcmpeq4(y.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                    y.y &= ~__vcmpeq4(y.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                    y.z &= ~__vcmpeq4(y.z & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                    y.w &= ~__vcmpeq4(y.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+#pragma unroll
+                    for (int r = 0; r < 4; r++) {
+                        y[r].x &= ~__vcmpeq4(y[r].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        y[r].y &= ~__vcmpeq4(y[r].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        y[r].z &= ~__vcmpeq4(y[r].z & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        y[r].w &= ~__vcmpeq4(y[r].w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                    }
                     nan = true;
                 }
             }
-            const uint4 h0 = make_uint4(f16x2_of(y.x), f16x2_of(y.x >> 16), f16x2_of(y.y), f16x2_of(y.y >> 16));
-            const uint4 h1 = make_uint4(f16x2_of(y.z), f16x2_of(y.z >> 16), f16x2_of(y.w), f16x2_of(y.w >> 16));
-            *reinterpret_cast<uint4 *>(dst + to0 + r * kTok * 128) = second ? h1 : h0;
-            *reinterpret_cast<uint4 *>(dst + to1 + r * kTok * 128) = second ? h0 : h1;
-            if (next) fetch(cache, b, r, raw);
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                // the half that goes first (see to0)
+                const uint32_t w0 = second ? y[r].z : y[r].x, w1 = second ? y[r].w : y[r].y;
+                const uint32_t w2 = second ? y[r].x : y[r].z, w3 = second ? y[r].y : y[r].w;
+                *reinterpret_cast<uint4 *>(dst + to0 + (r0 + r) * kTok * 128) =
+                    make_uint4(f16x2_of(w0), f16x2_of(w0 >> 16), f16x2_of(w1), f16x2_of(w1 >> 16));
+                *reinterpret_cast<uint4 *>(dst + to1 + (r0 + r) * kTok * 128) =
+                    make_uint4(f16x2_of(w2), f16x2_of(w2 >> 16), f16x2_of(w3), f16x2_of(w3 >> 16));
+            }
+            if (next)
+#pragma unroll
+                for (int r = 0; r < 4; r++) fetch(cache, b, r0 + r, raw);
         }
         if (nan) *static_cast<volatile int32_t *>(&sm->nan_seen) = 1;
         cp_commit();
@@ -519,71 +536,85 @@ __device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
     cp_wait<0>();
 }
 
-// ---- issuing thread ----------------------------------------------------------------------------
+// ---- issuing warp ------------------------------------------------------------------------------
+// The whole warp walks the units, so that addresses and descriptors stay in uniform registers; one
+// lane issues.
 template <int D>
 __device__ void issue_role(Smem<D> *sm, Walk<D> &walk) {
     constexpr uint32_t kQk = f16_idesc(128, kKeys, false), kPv = f16_idesc(128, D, true);
-    const uint32_t tmem = sm->tmem;
+    const uint32_t tmem = __shfl_sync(~0u, sm->tmem, 0);
     uint32_t unit = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+    const bool leader = elect_one();
     Item x;
     bool ok = true;
+    auto all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(~0u, wait(sm, bar, parity)) != 0; };
     auto qk = [&](int m, int stage) {
-        const uint32_t a = smem_addr(sm->q[m]), b = smem_addr(sm->k[stage]);
-        const uint64_t da = smem_desc(a, 16), db = smem_desc(b, 16);
-#pragma unroll 1
-        for (int k = 0; k < D / 16; k++) {
-            const uint64_t off = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
-            mma_ss(tmem + m * 128, da + off, db + off, kQk, k > 0);
+        const uint64_t da = smem_desc(smem_addr(sm->q[m]), 16), db = smem_desc(smem_addr(sm->k[stage]), 16);
+        if (leader) {
+#pragma unroll
+            for (int k = 0; k < D / 16; k++) {
+                constexpr int kPanel = 128 * 128;
+                const uint64_t off = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
+                mma_ss(tmem + m * 128, da + off, db + off, kQk, k > 0);
+            }
+            mbar_arrive(&sm->s_full[m]);
+            tc_commit(&sm->s_full[m]);
         }
-        mbar_arrive(&sm->s_full[m]);
-        tc_commit(&sm->s_full[m]);
+        __syncwarp();
     };
     auto pv = [&](int m, int stage, bool add) {
         const uint64_t db = smem_desc(smem_addr(sm->v[stage]), kKeys * 128);
-#pragma unroll 1
-        for (int k = 0; k < kKeys / 16; k++)
-            mma_ts(tmem + 256 + m * D, tmem + m * 128 + 8 * k, db + k * (2048 >> 4), kPv, add || k > 0);
+        if (leader) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 16; k++)
+                mma_ts(tmem + 256 + m * D, tmem + m * 128 + 8 * k, db + k * (2048 >> 4), kPv, add || k > 0);
+        }
+        __syncwarp();
+    };
+    auto commit = [&](uint64_t *bar) {
+        if (leader) tc_commit(bar);
+        __syncwarp();
     };
     while (ok && walk.next(x)) {
-        const int nu = x.ub - x.ua;
-        for (int m = 0; m < x.tiles && ok; m++) {
-            ok = wait(sm, &sm->q_full[m], q_phase[m]);
+        const int nu = __shfl_sync(~0u, x.ub - x.ua, 0), tiles = __shfl_sync(~0u, x.tiles, 0);
+        for (int m = 0; m < tiles && ok; m++) {
+            ok = all(&sm->q_full[m], q_phase[m]);
             q_phase[m] ^= 1;
         }
-        ok = ok && wait(sm, &sm->k_full[unit & 1], (unit >> 1) & 1);
+        ok = ok && all(&sm->k_full[unit & 1], (unit >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        for (int m = 0; m < x.tiles; m++) qk(m, unit & 1);
-        tc_commit(&sm->k_free[unit & 1]);
+        for (int m = 0; m < tiles; m++) qk(m, unit & 1);
+        commit(&sm->k_free[unit & 1]);
         for (int t = 0; t < nu && ok; t++, unit++) {
-            const int stage = unit & 1, next = (unit + 1) & 1;
-            for (int m = 0; m < x.tiles && ok; m++) {
-                if (m == 0) ok = wait(sm, &sm->v_full[stage], (unit >> 1) & 1);
-                ok = ok && wait(sm, &sm->p_full[m], p_phase[m]);
+            const int stage = unit & 1, next = stage ^ 1;
+            for (int m = 0; m < tiles && ok; m++) {
+                if (m == 0) ok = all(&sm->v_full[stage], (unit >> 1) & 1);
+                ok = ok && all(&sm->p_full[m], p_phase[m]);
                 p_phase[m] ^= 1;
                 if (!ok) break;
                 tc_fence_after();
                 pv(m, stage, t > 0);
                 if (t + 1 < nu) {
                     if (m == 0) {
-                        ok = wait(sm, &sm->k_full[next], ((unit + 1) >> 1) & 1);
+                        ok = all(&sm->k_full[next], ((unit + 1) >> 1) & 1);
                         if (!ok) break;
                         tc_fence_after();
                     }
                     qk(m, next);
                 } else {
-                    tc_commit(&sm->o_full[m]);
+                    commit(&sm->o_full[m]);
                 }
             }
             if (!ok) break;
-            tc_commit(&sm->v_free[stage]);
-            if (t + 1 < nu) tc_commit(&sm->k_free[next]);
+            commit(&sm->v_free[stage]);
+            if (t + 1 < nu) commit(&sm->k_free[next]);
         }
     }
     // the products end before the TMEM is freed
-    tc_commit(&sm->done);
+    commit(&sm->done);
     for (uint32_t k = 0; k < kTries; k++)
-        if (mbar_wait(&sm->done, 0, 1)) break;
+        if (mbar_try(&sm->done, 0)) break;
 }
 
 template <int D>
@@ -626,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const AttnPara
             softmax_role<D>(p, sm, walk, total, ranges);
         else if (warp < kSoftWarps + kConvWarps)
             convert_role<D>(p, sm, walk);
-        else if ((threadIdx.x & 31) == 0)
+        else
             issue_role<D>(sm, walk);
     } else if (threadIdx.x == 0) {
         p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
