@@ -4,10 +4,11 @@
 // Mathematics: as in pkv_kv8_decode.cu.  x = S * a_b + lv_b with S = q . code_k
 // from the tensor core, a_b = k_scale * softmax_scale * log2(e) and lv_b =
 // log2(v_scale), both constant over 16 tokens; w = 2^(x - R) goes into the
-// second product as f16, the softmax sum adds w / v_scale in fp32.  R follows
-// the running maximum lazily: it moves only when a row's maximum has grown by
-// more than 2^8, so that the accumulator is rarely rescaled and w stays below
-// 2^8, far inside f16's range.
+// second product as f16, the softmax sum adds w / v_scale in fp32.  R is the
+// row's maximum over its first unit and then follows lazily: it moves only
+// when the sum of 32 w, which is needed anyway, exceeds 2^14.  So later units
+// take no pass for the maximum, the accumulator is hardly ever rescaled, and w
+// stays inside f16's range with all its bits.
 //
 // Bound: the tensor pipe (4 D flops per visible pair); beside it per tile of
 // 256 rows x 128 tokens 32768 exponentials and 32768 codes turned into f16.
@@ -34,10 +35,13 @@ constexpr int kRows = 256;              // rows of a CTA, two tiles of 128
 constexpr int kKeys = 128;              // tokens per unit
 constexpr int kSub = kKeys / 16;
 constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 1);
+constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 4);   // and a warpgroup whose first warp issues
+// Registers a thread: launched with 128; 256 x 176 + 128 x 104 + 128 x 56 = 512 x 128.
+constexpr int kSoftRegs = 176, kConvRegs = 104, kIssueRegs = 56;
+static_assert(32 * (kSoftWarps * kSoftRegs + kConvWarps * kConvRegs + 4 * kIssueRegs) <= 65536, "registers");
 static_assert((kThreads + 1 + kThreads / 32) * 8 <= 2 * kKeys * 64, "the plan's sums lie in the raw codes' place");
 constexpr uint32_t kTries = 1u << 22;   // polls before a wait gives up (half a second or more)
-constexpr float kSlack = 8.f;           // growth of a row's maximum (log2) that R does not follow
+constexpr float kMostSum = 16384.f;     // sum of 32 w that makes R follow the row's maximum
 
 template <int D>
 struct Smem {
@@ -174,40 +178,102 @@ __device__ __forceinline__ float row_max(const Smem<D> *sm, uint32_t ts, int rin
     return most;
 }
 
-// w = 2^(x - ref) as f16 in the place of S, and the row's softmax sum over the unit.
-template <int D, bool kWhole>
-__device__ __forceinline__ float row_weights(const Smem<D> *sm, uint32_t ts, int ring, float cf, float ref, int lo, int hi) {
-    float sum = 0.f;
-#pragma unroll 1
-    for (int c = 0; c < 4; c++) {
-        uint32_t s[32], w[16];
-        tmem_ld32(s, ts + 32 * c);
-        const float2 ks = *reinterpret_cast<const float2 *>(&sm->ks[ring][2 * c]);
-        const float2 lv = *reinterpret_cast<const float2 *>(&sm->lv[ring][2 * c]);
-        const float2 iv = *reinterpret_cast<const float2 *>(&sm->iv[ring][2 * c]);
-        tc_wait_ld();
+// w = 2^(x - top) of 32 columns as f16; returns the two groups' sums.
+template <bool kWhole>
+__device__ __forceinline__ float2 weights32(const uint32_t (&s)[32], uint32_t (&w)[16], float2 a, float2 b, int lo, int hi) {
+    float2 sums;
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            const float a = cf * (h ? ks.y : ks.x), b = (h ? lv.y : lv.x) - ref;
-            const uint64_t aa = pair_of(a, a), bb = pair_of(b, b);
-            uint64_t part = 0;
+    for (int h = 0; h < 2; h++) {
+        const uint64_t aa = h ? pair_of(a.y, a.y) : pair_of(a.x, a.x), bb = h ? pair_of(b.y, b.y) : pair_of(b.x, b.x);
+        uint64_t part = 0;
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-                const uint64_t x = fma2(pair_of(__uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1])), aa, bb);
-                float y0 = exp2_fast(low_of(x)), y1 = exp2_fast(high_of(x));
-                if (!kWhole) {
-                    const int col = 32 * c + 16 * h + k;
-                    if (col > hi || col < lo) y0 = 0.f;
-                    if (col + 1 > hi || col + 1 < lo) y1 = 0.f;
-                }
-                part = add2(part, pair_of(y0, y1));
-                w[8 * h + k / 2] = pack_f16(y0, y1);
+        for (int k = 0; k < 16; k += 2) {
+            const uint64_t x = fma2(pair_of(__uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1])), aa, bb);
+            float y0 = exp2_fast(low_of(x)), y1 = exp2_fast(high_of(x));
+            if (!kWhole) {
+                const int col = 16 * h + k;
+                if (col > hi || col < lo) y0 = 0.f;
+                if (col + 1 > hi || col + 1 < lo) y1 = 0.f;
             }
-            sum = fmaf(low_of(part) + high_of(part), h ? iv.y : iv.x, sum);
+            part = add2(part, pair_of(y0, y1));
+            w[8 * h + k / 2] = pack_f16(y0, y1);
         }
-        tmem_st16(ts + 16 * c, w);
+        (h ? sums.y : sums.x) = low_of(part) + high_of(part);
     }
-    return sum;
+    return sums;
+}
+
+// Columns 32 c .. + 31 of a unit: weights in the place of S (32 columns of scores become 16 of packed
+// f16); `top` moves up where they outgrow it, with what has been added up so far.  o_cols: columns
+// of the accumulator to rescale, 0 while it holds nothing.
+template <int D, bool kWhole>
+__device__ __forceinline__ void columns32(const Smem<D> *sm, const uint32_t (&s)[32], int c, uint32_t ts, uint32_t to, int o_cols,
+                                          int ring, float cf, float &top, float &sum, int lo, int hi) {
+    uint32_t w[16];
+    float2 a = *reinterpret_cast<const float2 *>(&sm->ks[ring][2 * c]);
+    const float2 lv = *reinterpret_cast<const float2 *>(&sm->lv[ring][2 * c]);
+    const float2 iv = *reinterpret_cast<const float2 *>(&sm->iv[ring][2 * c]);
+    a.x *= cf;
+    a.y *= cf;
+    float ref = top == -INFINITY ? 0.f : top;
+    float2 part = weights32<kWhole>(s, w, a, make_float2(lv.x - ref, lv.y - ref), lo - 32 * c, hi - 32 * c);
+    const bool grow = part.x + part.y > kMostSum;
+    if (__any_sync(~0u, grow)) {
+        if (grow) {
+            float most = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 32; k++) {
+                const float x = fmaf(__uint_as_float(s[k]), k < 16 ? a.x : a.y, k < 16 ? lv.x : lv.y);
+                if (kWhole || (32 * c + k <= hi && 32 * c + k >= lo)) most = fmaxf(most, x);
+            }
+            ref = most;
+        }
+        __syncwarp();
+        const float f = grow ? exp2_fast(top - ref) : 1.f;
+        if (grow) top = ref;
+        sum *= f;
+        tc_wait_st();
+        for (int k = 0; k < c; k++) {                // this unit's weights so far
+            uint32_t y[16];
+            tmem_ld16(y, ts + 16 * k);
+            tc_wait_ld();
+            const __half2 ff = __float2half2_rn(f);
+#pragma unroll
+            for (int q = 0; q < 16; q++) {
+                const __half2 z = __hmul2(*reinterpret_cast<const __half2 *>(&y[q]), ff);
+                y[q] = *reinterpret_cast<const uint32_t *>(&z);
+            }
+            tmem_st16(ts + 16 * k, y);
+        }
+        for (int k = 0; k < o_cols; k += 16) {
+            uint32_t y[16];
+            tmem_ld16(y, to + k);
+            tc_wait_ld();
+#pragma unroll
+            for (int q = 0; q < 16; q++) y[q] = __float_as_uint(__uint_as_float(y[q]) * f);
+            tmem_st16(to + k, y);
+        }
+        part = weights32<kWhole>(s, w, a, make_float2(lv.x - ref, lv.y - ref), lo - 32 * c, hi - 32 * c);
+    }
+    sum = fmaf(part.x, iv.x, fmaf(part.y, iv.y, sum));
+    tmem_st16(ts + 16 * c, w);
+}
+
+// All of a unit's columns; the next 32 are on their way while 32 are worked on.
+template <int D, bool kWhole>
+__device__ __forceinline__ void row_weights(const Smem<D> *sm, uint32_t ts, uint32_t to, int o_cols, int ring, float cf,
+                                            float &top, float &sum, int lo, int hi) {
+    uint32_t s0[32], s1[32];
+    tmem_ld32(s0, ts);
+#pragma unroll 1
+    for (int c = 0; c < 4; c += 2) {
+        tc_wait_ld();
+        tmem_ld32(s1, ts + 32 * (c + 1));
+        columns32<D, kWhole>(sm, s0, c, ts, to, o_cols, ring, cf, top, sum, lo, hi);
+        tc_wait_ld();
+        if (c == 0) tmem_ld32(s0, ts + 64);
+        columns32<D, kWhole>(sm, s1, c + 1, ts, to, o_cols, ring, cf, top, sum, lo, hi);
+    }
 }
 
 // ---- softmax warps: a thread per row ----------------------------------------------------------
@@ -284,27 +350,17 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk, in
             const int s0 = x.s.base + (x.ua + t) * kKeys, ring = unit & 3;
             const bool whole = s0 + kKeys - 1 <= pos0 && (p.window <= 0 || s0 > pos1 - p.window);
             const int hi = pos - s0;                                         // columns lo .. hi are visible
-            const int lo = p.window > 0 ? pos - p.window + 1 - s0 : -0x7fffffff;
-            const float most = whole ? row_max<D, true>(sm, ts, ring, cf, lo, hi) : row_max<D, false>(sm, ts, ring, cf, lo, hi);
-            const bool grow = most > top + kSlack || (top == -INFINITY && most > -INFINITY);
-            if (__any_sync(~0u, grow)) {
-                const float f2 = grow ? exp2_fast(top - most) : 1.f;
-                if (grow) top = most;
-                sum *= f2;
-                if (t > 0) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; c++) {
-                        uint32_t o[32];
-                        tmem_ld32(o, to + 32 * c);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f2);
-                        tmem_st32(to + 32 * c, o);
-                    }
-                }
+            const int lo = p.window > 0 && p.window <= pos ? pos - p.window + 1 - s0 : -0x40000000;
+            // the first unit that shows a row anything sets its reference (no weight has been added before)
+            if (__any_sync(~0u, top == -INFINITY)) {
+                const float most = whole ? row_max<D, true>(sm, ts, ring, cf, lo, hi) : row_max<D, false>(sm, ts, ring, cf, lo, hi);
+                if (top == -INFINITY) top = most;
             }
-            const float ref = top == -INFINITY ? 0.f : top;
-            sum += whole ? row_weights<D, true>(sm, ts, ring, cf, ref, lo, hi) : row_weights<D, false>(sm, ts, ring, cf, ref, lo, hi);
+            const int o_cols = t > 0 ? D : 0;
+            if (whole)
+                row_weights<D, true>(sm, ts, to, o_cols, ring, cf, top, sum, lo, hi);
+            else
+                row_weights<D, false>(sm, ts, to, o_cols, ring, cf, top, sum, lo, hi);
             tc_wait_st();
             tc_fence_before();
             mbar_arrive(&sm->p_full[m]);
@@ -385,8 +441,8 @@ struct Feed {
 template <int D>
 __device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
     constexpr int kC = D / 16;                       // 16-byte pieces of a token's codes
-    constexpr int kTok = 128 / kC;                   // tokens per round of the 128 threads: 16 or 32
-    constexpr int kRounds = kKeys / kTok;
+    constexpr int kTok = 32 * kConvWarps / kC;       // tokens per round of the threads, a multiple of 16
+    constexpr int kRounds = kKeys / kTok, kStep = kRounds < 4 ? kRounds : 4, kRaw = 32 * kConvWarps * 16;
     const int i = threadIdx.x - 32 * kSoftWarps, lane = i & 31;
     const int c = i % kC, tok = i / kC;              // this thread's piece, and its token within a round
     const int64_t line = static_cast<int64_t>(p.Hkv) * D;
@@ -444,27 +500,27 @@ __device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
         const int k = r * kTok + tok;
         const int64_t from = __shfl_sync(~0u, f.at, k >> 4);
         const bool live = from >= 0 && k >= f.klo && k < f.khi;
-        cp_async<16>(smem_addr(raw + r * 2048 + i * 16), cache + (live ? from + mine : 0), live);
+        cp_async<16>(smem_addr(raw + r * kRaw + i * 16), cache + (live ? from + mine : 0), live);
     };
     // Turn a half (keys or values) of unit `a` into f16, and refill its pieces with the next unit's.
     auto half = [&](const uint8_t *cache, char *raw, char *dst, const Feed &b, bool next, bool values) {
         bool nan = false;
 #pragma unroll 1
-        for (int r0 = 0; r0 < kRounds; r0 += 4) {
-            uint4 y[4];
+        for (int r0 = 0; r0 < kRounds; r0 += kStep) {
+            uint4 y[kStep];
 #pragma unroll
-            for (int r = 0; r < 4; r++) y[r] = *reinterpret_cast<const uint4 *>(raw + (r0 + r) * 2048 + i * 16);
+            for (int r = 0; r < kStep; r++) y[r] = *reinterpret_cast<const uint4 *>(raw + (r0 + r) * kRaw + i * 16);
             if (values) {
                 // 0x7f + 1 carries into the sign bit of its byte: NaN codes leave the product (the
                 // softmax warps bring them back for the rows that see their token)
                 uint32_t hit = 0;
 #pragma unroll
-                for (int r = 0; r < 4; r++)
+                for (int r = 0; r < kStep; r++)
                     hit |= ((y[r].x & 0x7f7f7f7fu) + 0x01010101u) | ((y[r].y & 0x7f7f7f7fu) + 0x01010101u) |
                            ((y[r].z & 0x7f7f7f7fu) + 0x01010101u) | ((y[r].w & 0x7f7f7f7fu) + 0x01010101u);
                 if (hit & 0x80808080u) {
 #pragma unroll
-                    for (int r = 0; r < 4; r++) {
+                    for (int r = 0; r < kStep; r++) {
                         y[r].x &= ~__vcmpeq4(y[r].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
                         y[r].y &= ~__vcmpeq4(y[r].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
                         y[r].z &= ~__vcmpeq4(y[r].z & 0x7f7f7f7fu, 0x7f7f7f7fu);
@@ -474,7 +530,7 @@ __device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
                 }
             }
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
+            for (int r = 0; r < kStep; r++) {
                 // the half that goes first (see to0)
                 const uint32_t w0 = second ? y[r].z : y[r].x, w1 = second ? y[r].w : y[r].y;
                 const uint32_t w2 = second ? y[r].x : y[r].z, w3 = second ? y[r].y : y[r].w;
@@ -485,7 +541,7 @@ __device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
             }
             if (next)
 #pragma unroll
-                for (int r = 0; r < 4; r++) fetch(cache, b, r0 + r, raw);
+                for (int r = 0; r < kStep; r++) fetch(cache, b, r0 + r, raw);
         }
         if (nan) *static_cast<volatile int32_t *>(&sm->nan_seen) = 1;
         cp_commit();
@@ -653,12 +709,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const AttnPara
     if (blockIdx.x < ranges) {
         Walk<D> walk(p, prefix, blockIdx.x * total / ranges, (blockIdx.x + 1) * total / ranges);
         __syncthreads();                             // the sums' place is the converting warps' from here on
-        if (warp < kSoftWarps)
+        if (warp < kSoftWarps) {
+            more_registers<kSoftRegs>();
             softmax_role<D>(p, sm, walk, total, ranges);
-        else if (warp < kSoftWarps + kConvWarps)
+        } else if (warp < kSoftWarps + kConvWarps) {
+            fewer_registers<kConvRegs>();
             convert_role<D>(p, sm, walk);
-        else
-            issue_role<D>(sm, walk);
+        } else {
+            fewer_registers<kIssueRegs>();
+            if (warp == kSoftWarps + kConvWarps) issue_role<D>(sm, walk);
+        }
     } else if (threadIdx.x == 0) {
         p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
     }
