@@ -144,43 +144,45 @@ __device__ __forceinline__ bool wait(Smem<D> *sm, uint64_t *bar, uint32_t parity
     return false;
 }
 
-// The loops over 32 columns are not unrolled: the body of a whole unit would not stay in the
-// instruction cache beside the other warps' code.
+// Scores outside columns lo .. hi become -inf (of 32 columns).
+__device__ __forceinline__ void hide(uint32_t (&s)[32], int lo, int hi) {
+#pragma unroll
+    for (int k = 0; k < 32; k++)
+        if (k > hi || k < lo) s[k] = 0xff800000u;
+}
 
-// Largest x of a row in the unit (columns lo .. hi where not kWhole).
-template <int D, bool kWhole>
+// The factors of two 16-token groups; never zero, so that a hidden score stays -inf.
+__device__ __forceinline__ float2 factors(float cf, float2 ks) {
+    const float a = cf * ks.x, b = cf * ks.y;
+    return make_float2(a < 1e-37f ? 1e-37f : a, b < 1e-37f ? 1e-37f : b);
+}
+
+// Largest x of a row in the unit.
+template <int D>
 __device__ __forceinline__ float row_max(const Smem<D> *sm, uint32_t ts, int ring, float cf, int lo, int hi) {
     float most = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < 4; c++) {
         uint32_t s[32];
         tmem_ld32(s, ts + 32 * c);
-        const float2 ks = *reinterpret_cast<const float2 *>(&sm->ks[ring][2 * c]);
+        const float2 a = factors(cf, *reinterpret_cast<const float2 *>(&sm->ks[ring][2 * c]));
         const float2 lv = *reinterpret_cast<const float2 *>(&sm->lv[ring][2 * c]);
         tc_wait_ld();
+        hide(s, lo - 32 * c, hi - 32 * c);
 #pragma unroll
         for (int h = 0; h < 2; h++) {
-            if (!kWhole) {
-#pragma unroll
-                for (int k = 0; k < 16; k++) {
-                    const int col = 32 * c + 16 * h + k;
-                    if (col > hi || col < lo) s[16 * h + k] = 0xff800000u;
-                }
-            }
             float mx = __uint_as_float(s[16 * h]);
 #pragma unroll
             for (int k = 1; k < 15; k += 2) mx = max3(mx, __uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1]));
             mx = fmaxf(mx, __uint_as_float(s[16 * h + 15]));
-            const float x = fmaf(mx, cf * (h ? ks.y : ks.x), h ? lv.y : lv.x);
-            most = fmaxf(most, mx == -INFINITY ? -INFINITY : x);
+            most = fmaxf(most, fmaf(mx, h ? a.y : a.x, h ? lv.y : lv.x));
         }
     }
     return most;
 }
 
-// w = 2^(x - top) of 32 columns as f16; returns the two groups' sums.
-template <bool kWhole>
-__device__ __forceinline__ float2 weights32(const uint32_t (&s)[32], uint32_t (&w)[16], float2 a, float2 b, int lo, int hi) {
+// w = 2^(a s + b) of 32 columns as f16; returns the two groups' sums.
+__device__ __forceinline__ float2 weights32(const uint32_t (&s)[32], uint32_t (&w)[16], float2 a, float2 b) {
     float2 sums;
 #pragma unroll
     for (int h = 0; h < 2; h++) {
@@ -189,12 +191,7 @@ __device__ __forceinline__ float2 weights32(const uint32_t (&s)[32], uint32_t (&
 #pragma unroll
         for (int k = 0; k < 16; k += 2) {
             const uint64_t x = fma2(pair_of(__uint_as_float(s[16 * h + k]), __uint_as_float(s[16 * h + k + 1])), aa, bb);
-            float y0 = exp2_fast(low_of(x)), y1 = exp2_fast(high_of(x));
-            if (!kWhole) {
-                const int col = 16 * h + k;
-                if (col > hi || col < lo) y0 = 0.f;
-                if (col + 1 > hi || col + 1 < lo) y1 = 0.f;
-            }
+            const float y0 = exp2_fast(low_of(x)), y1 = exp2_fast(high_of(x));
             part = add2(part, pair_of(y0, y1));
             w[8 * h + k / 2] = pack_f16(y0, y1);
         }
@@ -203,41 +200,37 @@ __device__ __forceinline__ float2 weights32(const uint32_t (&s)[32], uint32_t (&
     return sums;
 }
 
-// Columns 32 c .. + 31 of a unit: weights in the place of S (32 columns of scores become 16 of packed
-// f16); `top` moves up where they outgrow it, with what has been added up so far.  o_cols: columns
-// of the accumulator to rescale, 0 while it holds nothing.
-template <int D, bool kWhole>
-__device__ __forceinline__ void columns32(const Smem<D> *sm, const uint32_t (&s)[32], int c, uint32_t ts, uint32_t to, int o_cols,
-                                          int ring, float cf, float &top, float &sum, int lo, int hi) {
-    uint32_t w[16];
-    float2 a = *reinterpret_cast<const float2 *>(&sm->ks[ring][2 * c]);
-    const float2 lv = *reinterpret_cast<const float2 *>(&sm->lv[ring][2 * c]);
-    const float2 iv = *reinterpret_cast<const float2 *>(&sm->iv[ring][2 * c]);
-    a.x *= cf;
-    a.y *= cf;
-    float ref = top == -INFINITY ? 0.f : top;
-    float2 part = weights32<kWhole>(s, w, a, make_float2(lv.x - ref, lv.y - ref), lo - 32 * c, hi - 32 * c);
-    const bool grow = part.x + part.y > kMostSum;
-    if (__any_sync(~0u, grow)) {
-        if (grow) {
-            float most = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < 32; k++) {
-                const float x = fmaf(__uint_as_float(s[k]), k < 16 ? a.x : a.y, k < 16 ? lv.x : lv.y);
-                if (kWhole || (32 * c + k <= hi && 32 * c + k >= lo)) most = fmaxf(most, x);
-            }
-            ref = most;
-        }
-        __syncwarp();
-        const float f = grow ? exp2_fast(top - ref) : 1.f;
-        if (grow) top = ref;
-        sum *= f;
+// Columns 32 c .. of a unit from `c` on, where some row's weights outgrow its reference: the reference
+// moves up to their largest x, with the row's sum, its weights of this unit so far and its
+// accumulator (o_cols columns, 0 while it holds nothing).  Rare.
+template <int D>
+__device__ __forceinline__ void grow_rows(const Smem<D> *sm, int c, uint32_t ts, uint32_t to, int o_cols, int ring, float cf,
+                                          float &top, float &sum, int lo, int hi) {
+#pragma unroll 1
+    for (; c < 4; c++) {
+        uint32_t s[32], w[16];
         tc_wait_st();
-        for (int k = 0; k < c; k++) {                // this unit's weights so far
+        tmem_ld32(s, ts + 32 * c);
+        const float2 a = factors(cf, *reinterpret_cast<const float2 *>(&sm->ks[ring][2 * c]));
+        const float2 lv = *reinterpret_cast<const float2 *>(&sm->lv[ring][2 * c]);
+        const float2 iv = *reinterpret_cast<const float2 *>(&sm->iv[ring][2 * c]);
+        tc_wait_ld();
+        hide(s, lo - 32 * c, hi - 32 * c);
+        float most = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 32; k++) most = fmaxf(most, fmaf(__uint_as_float(s[k]), k < 16 ? a.x : a.y, k < 16 ? lv.x : lv.y));
+        const bool grow = most > top;
+        // an infinite maximum cannot be followed: its row is NaN
+        if (most == INFINITY) most = NAN;
+        const float f = grow ? exp2_fast(top - most) : 1.f;
+        if (grow) top = most;
+        sum *= f;
+        const __half2 ff = __float2half2_rn(f);
+#pragma unroll 1
+        for (int k = 0; k < c; k++) {
             uint32_t y[16];
             tmem_ld16(y, ts + 16 * k);
             tc_wait_ld();
-            const __half2 ff = __float2half2_rn(f);
 #pragma unroll
             for (int q = 0; q < 16; q++) {
                 const __half2 z = __hmul2(*reinterpret_cast<const __half2 *>(&y[q]), ff);
@@ -245,6 +238,7 @@ __device__ __forceinline__ void columns32(const Smem<D> *sm, const uint32_t (&s)
             }
             tmem_st16(ts + 16 * k, y);
         }
+#pragma unroll 1
         for (int k = 0; k < o_cols; k += 16) {
             uint32_t y[16];
             tmem_ld16(y, to + k);
@@ -253,26 +247,55 @@ __device__ __forceinline__ void columns32(const Smem<D> *sm, const uint32_t (&s)
             for (int q = 0; q < 16; q++) y[q] = __float_as_uint(__uint_as_float(y[q]) * f);
             tmem_st16(to + k, y);
         }
-        part = weights32<kWhole>(s, w, a, make_float2(lv.x - ref, lv.y - ref), lo - 32 * c, hi - 32 * c);
+        const float ref = top == -INFINITY ? 0.f : top;
+        const float2 part = weights32(s, w, a, make_float2(lv.x - ref, lv.y - ref));
+        sum = fmaf(part.x, iv.x, fmaf(part.y, iv.y, sum));
+        tmem_st16(ts + 16 * c, w);
     }
-    sum = fmaf(part.x, iv.x, fmaf(part.y, iv.y, sum));
-    tmem_st16(ts + 16 * c, w);
 }
 
-// All of a unit's columns; the next 32 are on their way while 32 are worked on.
-template <int D, bool kWhole>
+// Columns 32 c .. + 31 of a unit: weights in the place of S (32 columns of scores become 16 of packed
+// f16).  False, with nothing written, where a row's weights outgrow its reference.
+template <int D>
+__device__ __forceinline__ bool columns32(const Smem<D> *sm, uint32_t (&s)[32], int c, uint32_t ts, int ring, float cf, float ref,
+                                          float &sum, bool whole, int lo, int hi) {
+    uint32_t w[16];
+    const float2 a = factors(cf, *reinterpret_cast<const float2 *>(&sm->ks[ring][2 * c]));
+    const float2 lv = *reinterpret_cast<const float2 *>(&sm->lv[ring][2 * c]);
+    const float2 iv = *reinterpret_cast<const float2 *>(&sm->iv[ring][2 * c]);
+    if (!whole) hide(s, lo - 32 * c, hi - 32 * c);
+    const float2 part = weights32(s, w, a, make_float2(lv.x - ref, lv.y - ref));
+    if (__any_sync(~0u, part.x + part.y > kMostSum)) return false;
+    sum = fmaf(part.x, iv.x, fmaf(part.y, iv.y, sum));
+    tmem_st16(ts + 16 * c, w);
+    return true;
+}
+
+// All of a unit's columns; the next 32 are on their way while 32 are worked on.  The loop is not
+// unrolled further: the body of a whole unit would not stay in the instruction cache beside the
+// other warps' code.
+template <int D>
 __device__ __forceinline__ void row_weights(const Smem<D> *sm, uint32_t ts, uint32_t to, int o_cols, int ring, float cf,
-                                            float &top, float &sum, int lo, int hi) {
+                                            float &top, float &sum, bool whole, int lo, int hi) {
+    const float ref = top == -INFINITY ? 0.f : top;
     uint32_t s0[32], s1[32];
     tmem_ld32(s0, ts);
+    int c = 0;
 #pragma unroll 1
-    for (int c = 0; c < 4; c += 2) {
+    for (; c < 4; c += 2) {
         tc_wait_ld();
         tmem_ld32(s1, ts + 32 * (c + 1));
-        columns32<D, kWhole>(sm, s0, c, ts, to, o_cols, ring, cf, top, sum, lo, hi);
+        if (!columns32<D>(sm, s0, c, ts, ring, cf, ref, sum, whole, lo, hi)) break;
         tc_wait_ld();
         if (c == 0) tmem_ld32(s0, ts + 64);
-        columns32<D, kWhole>(sm, s1, c + 1, ts, to, o_cols, ring, cf, top, sum, lo, hi);
+        if (!columns32<D>(sm, s1, c + 1, ts, ring, cf, ref, sum, whole, lo, hi)) {
+            c++;
+            break;
+        }
+    }
+    if (c < 4) {
+        tc_wait_ld();
+        grow_rows<D>(sm, c, ts, to, o_cols, ring, cf, top, sum, lo, hi);
     }
 }
 
@@ -353,14 +376,10 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk, in
             const int lo = p.window > 0 && p.window <= pos ? pos - p.window + 1 - s0 : -0x40000000;
             // the first unit that shows a row anything sets its reference (no weight has been added before)
             if (__any_sync(~0u, top == -INFINITY)) {
-                const float most = whole ? row_max<D, true>(sm, ts, ring, cf, lo, hi) : row_max<D, false>(sm, ts, ring, cf, lo, hi);
-                if (top == -INFINITY) top = most;
+                const float most = row_max<D>(sm, ts, ring, cf, lo, hi);
+                if (top == -INFINITY) top = most == INFINITY ? NAN : most;
             }
-            const int o_cols = t > 0 ? D : 0;
-            if (whole)
-                row_weights<D, true>(sm, ts, to, o_cols, ring, cf, top, sum, lo, hi);
-            else
-                row_weights<D, false>(sm, ts, to, o_cols, ring, cf, top, sum, lo, hi);
+            row_weights<D>(sm, ts, to, t > 0 ? D : 0, ring, cf, top, sum, whole, lo, hi);
             tc_wait_st();
             tc_fence_before();
             mbar_arrive(&sm->p_full[m]);
