@@ -575,7 +575,8 @@ int pkv_selftest_wait_timeout(int32_t *d_error, uint32_t polls, pkv_stream_t s);
  *   k_cache, v_cache: [num_blocks * block_size][num_heads][head_dim] bytes, 16-byte aligned;
  *   k_scale, v_scale: [num_blocks][num_heads], positive (pkv_kv8_store makes powers of two;
  *                     a V scale below 2^-100 counts as 2^-100).
- * head_dim is 64, 128 or 256; num_heads (KV heads) at most 1024; block_size any.
+ * head_dim is 64, 128 or 256; num_heads (KV heads) at most 1024; any block_size,
+ * with fewer than 2^32 slots.
  */
 #define PKV_BF16 0             /* element types of sources, queries and outputs */
 #define PKV_FP16 1

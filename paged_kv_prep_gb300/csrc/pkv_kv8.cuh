@@ -53,7 +53,8 @@ inline bool kv8_head_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }
 inline int kv8_check_cache(const pkv_kv8_cache *c) {
     if (!c) return PKV_ERR_INVALID_ARG;
     if (c->num_blocks < 0 || c->block_size < 1 || c->num_heads < 1 || c->num_heads > 1024 ||
-        !kv8_head_dim(c->head_dim) || c->num_blocks > 0x7fffffff)
+        !kv8_head_dim(c->head_dim) || c->num_blocks > 0x7fffffff ||
+        c->num_blocks * c->block_size > 0xffffffffLL)    // slots fit 32 bits
         return PKV_ERR_INVALID_ARG;
     if (c->num_blocks == 0) return PKV_OK;
     if (!c->k_cache || !c->v_cache || !c->k_scale || !c->v_scale) return PKV_ERR_INVALID_ARG;

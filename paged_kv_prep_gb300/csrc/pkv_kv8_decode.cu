@@ -3,15 +3,15 @@
 //
 // Mathematics.  Row r = (query j, head of the KV head's group), key s in block
 // b: x = (q . code_k) * k_scale[b] * softmax_scale * log2(e) + log2(v_scale[b]).
-// With R = the running maximum of x, w = 2^(x - R) <= 1 already carries the
-// value scale, so it can be rounded to f16 for the second product without
-// leaving f16's range whatever the scales are; the softmax sum adds
+// With R = a row's reference, at most 14 below the running maximum of x, w =
+// 2^(x - R) <= 2^14 already carries the value scale, so it can be rounded to f16
+// for the second product without leaving f16's range whatever the scales are; the softmax sum adds
 // w / v_scale[b] in fp32.  out = sum w * code_v / sum, lse = R ln 2 + ln sum.
 //
 // Bound: HBM, 2 * D bytes per (cached token, KV head), each read once.
 //
 // Layout.  Every warp works alone: it owns one KV head and a contiguous range
-// of 16-token units of the batch; the warps of the KV heads of one range are
+// of 32-token units of the batch; the warps of the KV heads of one range are
 // neighbours, so a token's line is read by one CTA at one time.  Keys are the
 // M side of the products (S^T = K Q^T, O^T = V^T P^T), so eight rows fill the
 // N side.  Each lane copies with cp.async exactly the codes that its own
@@ -26,23 +26,24 @@
 namespace pkv {
 namespace {
 
-constexpr int kUnit = 16;          // tokens per unit
-constexpr int kStages = 3;
+constexpr int kUnit = 32;          // tokens per unit, two groups of 16
+constexpr int kStages = 2;
+constexpr float kSlack = 14.f;     // growth of a row's maximum (log2) that R does not follow
 
 template <int D>
 struct Stage {
     static constexpr int kKPieces = D / 64;                   // 16-byte pieces per lane and token row
     static constexpr int kVBytes = D / 8 < 16 ? D / 8 : 16;   // bytes per piece
     static constexpr int kVPieces = D / 8 / kVBytes;
-    uint4 k[2][kKPieces][32];
-    char v[4][kVPieces][32 * kVBytes];
-    float ks[kUnit], vs[kUnit];
+    uint4 k[2][2][kKPieces][32];
+    char v[2][4][kVPieces][32 * kVBytes];
+    float ks[kUnit], vs[kUnit];                               // by token, or by group
 };
 
 template <int D, int NT>
-constexpr int warps_of() { return NT == 1 && D <= 128 ? 16 : 8; }
+constexpr int warps_of() { return D > 128 ? 6 : NT == 1 ? 12 : 8; }
 
-// Units of a request: 16-token units of its visible range, once per tile of 8 * NT rows.
+// Units of a request: 32-token units of its visible range, once per tile of 8 * NT rows.
 template <int NT>
 __device__ __forceinline__ int64_t units_of_request(const AttnParams &p, const Req &r, int *per_tile) {
     *per_tile = 1;
@@ -54,8 +55,9 @@ __device__ __forceinline__ int64_t units_of_request(const AttnParams &p, const R
     return static_cast<int64_t>(u) * ((rows + 8 * NT - 1) / (8 * NT));
 }
 
-// One warp's pass over units ua..ub-1 of row tile `rt` of a request and one KV head.
-template <int D, int NT>
+// One warp's pass over units ua..ub-1 of row tile `rt` of a request and one KV head.  kGrouped: 16
+// tokens from a multiple of 16 on lie in one block, so a group has one address and one pair of scales.
+template <int D, int NT, bool kGrouped>
 struct Tile {
     float o[NT][D / 16][4];
     float top[NT][2], sum[NT][2];          // of columns 2t, 2t + 1
@@ -96,126 +98,200 @@ struct Tile {
         const int pos_first = r.len - r.count + first_row / p.G, pos_last = r.len - r.count + last_row / p.G;
         const int base = r.lo & ~(kUnit - 1);
         // keys that some row of the tile sees, and those that every row sees
-        const int some_lo = p.window > 0 ? max(0, pos_first - p.window + 1) : 0, some_hi = min(pos_last + 1, r.keys);
-        const int all_lo = p.window > 0 ? max(0, pos_last - p.window + 1) : 0, all_hi = pos_first + 1;
+        const int some_lo = lo_of(p, pos_first), some_hi = min(pos_last + 1, r.keys);
+        const int all_lo = lo_of(p, pos_last), all_hi = min(pos_first + 1, r.keys);
         ua = max(ua, (some_lo - base) / kUnit);
         ub = min(ub, some_hi > base ? (some_hi - base + kUnit - 1) / kUnit : 0);
         if (ua >= ub) return;
 
         const int64_t line = static_cast<int64_t>(p.Hkv) * D;
-        const uint8_t *kh = p.kc + head * D + 16 * t;
-        const uint8_t *vh = p.vc + head * D + St::kVBytes * g;
+        // this lane's place in a group: rows g and g + 8 of K, tokens 2t, 2t + 1, 2t + 8, 2t + 9 of V
+        const uint8_t *kh = p.kc + head * D + 16 * t + (kGrouped ? g * line : 0);
+        const uint8_t *vh = p.vc + head * D + St::kVBytes * g + (kGrouped ? 2 * t * line : 0);
 
-        auto block_at = [&](int u) {           // block id of token (lane & 15) of unit u, -1 if not read
-            const int s = base + u * kUnit + (lane & 15);
-            return u < ub && s >= some_lo && s < some_hi ? block_of(p, table, s) : -1;
+        // slot of token `lane` of unit u, kNone where it is not read; an id that is asked for one unit
+        // ahead is looked at here
+        auto ask = [&](int u) {
+            const int s = base + u * kUnit + (kGrouped ? lane & 16 : lane);
+            return u < ub && s < some_hi ? p.table_at(table, s) : -1;
         };
         auto issue = [&](int u, int block) {
             if (u < ub) {
-                St &st = ring[(u - ua) % kStages];
-                const int s = base + u * kUnit + (lane & 15);
-                const int64_t slot = block >= 0 ? static_cast<int64_t>(block) * p.bs + s % p.bs : -1;
-                const uint32_t mask = __ballot_sync(~0u, block >= 0) & 0xffffu;
-                if (lane == 0) valid[(u - ua) % kStages] = mask;
-                const float *sc = (lane < 16 ? p.ks : p.vs) + (block >= 0 ? static_cast<int64_t>(block) * p.Hkv + head : 0);
-                cp_async<4>(smem_addr(lane < 16 ? &st.ks[lane] : &st.vs[lane - 16]), sc, block >= 0);
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const int64_t x = __shfl_sync(~0u, slot, g + 8 * h);
-                    const uint8_t *src = kh + (x >= 0 ? x * line : 0);
-#pragma unroll
-                    for (int c = 0; c < St::kKPieces; c++) cp_async<16>(smem_addr(&st.k[h][c][lane]), src + 64 * c, x >= 0);
+                St &st = ring[u % kStages];
+                const int s0 = base + u * kUnit, s = s0 + lane;
+                if (block >= p.num_blocks) {
+                    if (p.err && s >= some_lo && s < some_hi) atomicOr(p.err, PKV_DEVERR_BLOCK);
+                    block = -1;
                 }
+                const bool live = block >= 0 && s >= some_lo && s < some_hi;
+                const uint32_t slot = static_cast<uint32_t>(block) * static_cast<uint32_t>(p.bs) + static_cast<uint32_t>(s) % static_cast<uint32_t>(p.bs);
+                const uint32_t mask = __ballot_sync(~0u, live);
+                if (lane == 0) valid[u % kStages] = mask;
+                if constexpr (kGrouped) {
+                    // lanes 0, 16: K scales; lanes 1, 17: V scales
+                    if ((lane & 15) < 2) {
+                        const float *sc = lane & 1 ? p.vs : p.ks;
+                        float *to = lane & 1 ? st.vs : st.ks;
+                        cp_async<4>(smem_addr(&to[lane >> 4]), sc + (block >= 0 ? static_cast<int64_t>(block) * p.Hkv + head : 0),
+                                    block >= 0);
+                    }
 #pragma unroll
-                for (int h = 0; h < 4; h++) {
-                    const int64_t x = __shfl_sync(~0u, slot, 2 * t + (h & 1) + 8 * (h >> 1));
-                    const uint8_t *src = vh + (x >= 0 ? x * line : 0);
+                    for (int q = 0; q < 2; q++) {
+                        const int64_t at = static_cast<int64_t>(__shfl_sync(~0u, slot, 16 * q)) * line;
+                        const uint32_t m = mask >> (16 * q);
 #pragma unroll
-                    for (int c = 0; c < St::kVPieces; c++)
-                        cp_async<St::kVBytes>(smem_addr(&st.v[h][c][lane * St::kVBytes]), src + 128 * c, x >= 0);
+                        for (int h = 0; h < 2; h++) {
+                            const bool on = (m >> (g + 8 * h)) & 1;
+                            const uint8_t *src = kh + (on ? at + 8 * h * line : 0);
+#pragma unroll
+                            for (int c = 0; c < St::kKPieces; c++) cp_async<16>(smem_addr(&st.k[q][h][c][lane]), src + 64 * c, on);
+                        }
+#pragma unroll
+                        for (int h = 0; h < 4; h++) {
+                            const int tok = (h & 1) + 8 * (h >> 1);
+                            const bool on = (m >> (2 * t + tok)) & 1;
+                            const uint8_t *src = vh + (on ? at + tok * line : 0);
+#pragma unroll
+                            for (int c = 0; c < St::kVPieces; c++)
+                                cp_async<St::kVBytes>(smem_addr(&st.v[q][h][c][lane * St::kVBytes]), src + 128 * c, on);
+                        }
+                    }
+                } else {
+                    const int64_t sc = live ? static_cast<int64_t>(block) * p.Hkv + head : 0;
+                    cp_async<4>(smem_addr(&st.ks[lane]), p.ks + sc, live);
+                    cp_async<4>(smem_addr(&st.vs[lane]), p.vs + sc, live);
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const int tok = 16 * q + g + 8 * h;
+                            const uint32_t x = __shfl_sync(~0u, slot, tok);
+                            const bool on = (mask >> tok) & 1;
+                            const uint8_t *src = kh + (on ? x * line : 0);
+#pragma unroll
+                            for (int c = 0; c < St::kKPieces; c++) cp_async<16>(smem_addr(&st.k[q][h][c][lane]), src + 64 * c, on);
+                        }
+#pragma unroll
+                        for (int h = 0; h < 4; h++) {
+                            const int tok = 16 * q + 2 * t + (h & 1) + 8 * (h >> 1);
+                            const uint32_t x = __shfl_sync(~0u, slot, tok);
+                            const bool on = (mask >> tok) & 1;
+                            const uint8_t *src = vh + (on ? x * line : 0);
+#pragma unroll
+                            for (int c = 0; c < St::kVPieces; c++)
+                                cp_async<St::kVBytes>(smem_addr(&st.v[q][h][c][lane * St::kVBytes]), src + 128 * c, on);
+                        }
+                    }
                 }
             }
             cp_commit();
         };
 
         __syncwarp();
-        int ahead = block_at(ua);
-#pragma unroll
-        for (int k = 0; k < kStages - 1; k++) {
-            const int b = ahead;
-            ahead = block_at(ua + k + 1);
-            issue(ua + k, b);
+        {
+            const int b = ask(ua);
+            issue(ua, b);
         }
+        int ahead = ask(ua + 1);
         for (int u = ua; u < ub; u++) {
-            cp_wait<kStages - 2>();
-            __syncwarp();
+            __syncwarp();                      // everyone has left the stage that is filled next
             {
                 const int b = ahead;
-                ahead = block_at(u + kStages);
-                issue(u + kStages - 1, b);
+                ahead = ask(u + 2);
+                issue(u + 1, b);
             }
-            const St &st = ring[(u - ua) % kStages];
-            const uint32_t mask = valid[(u - ua) % kStages];
+            cp_wait<1>();
+            __syncwarp();
+            const St &st = ring[u % kStages];
+            const uint32_t mask = valid[u % kStages];
             const int s0 = base + u * kUnit;
 
-            float x[NT][4];
+            float x[2][NT][4];
+#pragma unroll
+            for (int q = 0; q < 2; q++) {
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int c = 0; c < 4; c++) x[q][nt][c] = 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < St::kKPieces; c++) {
+                uint4 ka[2], kb[2];
+#pragma unroll
+                for (int q = 0; q < 2; q++) {
+                    ka[q] = st.k[q][0][c][lane];
+                    kb[q] = st.k[q][1][c][lane];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {
+                        const uint32_t wa = i == 0 ? ka[q].x : i == 1 ? ka[q].y : i == 2 ? ka[q].z : ka[q].w;
+                        const uint32_t wb = i == 0 ? kb[q].x : i == 1 ? kb[q].y : i == 2 ? kb[q].z : kb[q].w;
+                        const uint32_t a[4] = {f16x2_of(wa), f16x2_of(wb), f16x2_of(wa >> 16), f16x2_of(wb >> 16)};
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++) mma_f16(x[q][nt], a, qb[nt][4 * c + i][0], qb[nt][4 * c + i][1]);
+                    }
+            }
+            const bool whole = mask == ~0u && s0 >= all_lo && s0 + kUnit <= all_hi;
+            float iv[2][2];                    // of the lane's tokens g, g + 8 of both groups
+            uint32_t seen[NT];                 // bit 4 q + c: the lane's value is visible
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) seen[nt] = 255;
+#pragma unroll
+            for (int q = 0; q < 2; q++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int at = kGrouped ? q : 16 * q + g + 8 * h;
+                    const float ks = st.ks[at], vs = value_scale(st.vs[at]), lv = __log2f(vs);
+                    iv[q][h] = __frcp_rn(vs);
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int col = 0; col < 2; col++) {
+                            float &y = x[q][nt][2 * h + col];
+                            y = fmaf(y, cf[nt][col] * ks, lv);
+                        }
+                }
+            if (!whole) {
+#pragma unroll
+                for (int q = 0; q < 2; q++)
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            const int tok = 16 * q + g + 8 * (c >> 1), s = s0 + tok;
+                            const bool ok = ((mask >> tok) & 1) && s <= pos[nt][c & 1] && s >= lo_of(p, pos[nt][c & 1]);
+                            if (!ok) {
+                                x[q][nt][c] = -INFINITY;
+                                seen[nt] &= ~(1u << (4 * q + c));
+                            }
+                        }
+            }
+            // R follows the maximum only where a row's values outgrow it (or it has seen nothing yet)
+            bool grow = false;
+            float most[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                for (int c = 0; c < 4; c++) x[nt][c] = 0.f;
-#pragma unroll
-            for (int c = 0; c < St::kKPieces; c++) {
-                const uint4 ka = st.k[0][c][lane], kb = st.k[1][c][lane];
-                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const uint32_t a[4] = {f16x2_of(wa[i]), f16x2_of(wb[i]), f16x2_of(wa[i] >> 16), f16x2_of(wb[i] >> 16)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; nt++) mma_f16(x[nt], a, qb[nt][4 * c + i][0], qb[nt][4 * c + i][1]);
-                }
-            }
-            const float ks[2] = {st.ks[g], st.ks[g + 8]}, vs[2] = {value_scale(st.vs[g]), value_scale(st.vs[g + 8])};
-            const float lv[2] = {__log2f(vs[0]), __log2f(vs[1])}, iv[2] = {__frcp_rn(vs[0]), __frcp_rn(vs[1])};
-            const bool whole = mask == 0xffffu && s0 >= all_lo && s0 + kUnit <= all_hi;
-            uint32_t pb[NT][2], seen[NT];
-            bool moved = false;
-            float next[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; nt++) {
-                seen[nt] = 15;
-#pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    const int h = c >> 1, col = c & 1;
-                    x[nt][c] = fmaf(x[nt][c], cf[nt][col] * ks[h], lv[h]);
-                    if (!whole) {
-                        const int s = s0 + g + 8 * h;
-                        const bool ok = ((mask >> (g + 8 * h)) & 1) && s <= pos[nt][col] &&
-                                        (p.window <= 0 || s > pos[nt][col] - p.window);
-                        if (!ok) {
-                            x[nt][c] = -INFINITY;
-                            seen[nt] &= ~(1u << c);
-                        }
-                    }
-                }
-#pragma unroll
                 for (int col = 0; col < 2; col++) {
-                    float m = fmaxf(x[nt][col], x[nt][2 + col]);
-                    m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
-                    m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
-                    m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
-                    next[nt][col] = fmaxf(top[nt][col], m);
-                    moved |= next[nt][col] > top[nt][col];
+                    most[nt][col] = fmaxf(fmaxf(x[0][nt][col], x[0][nt][2 + col]), fmaxf(x[1][nt][col], x[1][nt][2 + col]));
+                    grow |= most[nt][col] > top[nt][col] + kSlack;
                 }
-            }
-            if (__any_sync(~0u, moved)) {
+            if (__any_sync(~0u, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
                     float a[2];
 #pragma unroll
                     for (int col = 0; col < 2; col++) {
-                        a[col] = next[nt][col] > top[nt][col] ? exp2_fast(top[nt][col] - next[nt][col]) : 1.f;
+                        float m = most[nt][col];
+                        m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
+                        m = fmaxf(m, top[nt][col]);
+                        a[col] = m > top[nt][col] ? exp2_fast(top[nt][col] - m) : 1.f;
+                        top[nt][col] = m;
                         sum[nt][col] *= a[col];
-                        top[nt][col] = next[nt][col];
                     }
 #pragma unroll
                     for (int j = 0; j < S; j++)
@@ -223,77 +299,55 @@ struct Tile {
                         for (int c = 0; c < 4; c++) o[nt][j][c] *= a[c & 1];
                 }
             }
+            uint32_t pb[2][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
-                float w[4];
+                const float ref[2] = {top[nt][0] == -INFINITY ? 0.f : top[nt][0], top[nt][1] == -INFINITY ? 0.f : top[nt][1]};
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    w[c] = (seen[nt] >> c) & 1 ? exp2_fast(x[nt][c] - top[nt][c & 1]) : 0.f;
-                    sum[nt][c & 1] += (seen[nt] >> c) & 1 ? w[c] * iv[c >> 1] : 0.f;
+                for (int q = 0; q < 2; q++) {
+                    float w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        w[c] = exp2_fast(x[q][nt][c] - ref[c & 1]);
+                        sum[nt][c & 1] = fmaf(w[c], iv[q][c >> 1], sum[nt][c & 1]);
+                    }
+                    pb[q][nt][0] = transpose8x8(pack_f16(w[0], w[1]));
+                    pb[q][nt][1] = transpose8x8(pack_f16(w[2], w[3]));
                 }
-                pb[nt][0] = transpose8x8(pack_f16(w[0], w[1]));
-                pb[nt][1] = transpose8x8(pack_f16(w[2], w[3]));
             }
 #pragma unroll
-            for (int c = 0; c < St::kVPieces; c++) {
-                uint32_t w[4][St::kVBytes / 4];
+            for (int q = 0; q < 2; q++)
 #pragma unroll
-                for (int h = 0; h < 4; h++) {
-                    if constexpr (St::kVBytes == 16) {
-                        const uint4 y = *reinterpret_cast<const uint4 *>(&st.v[h][c][lane * 16]);
-                        w[h][0] = y.x;
-                        w[h][1] = y.y;
-                        w[h][2] = y.z;
-                        w[h][3] = y.w;
-                    } else {
-                        const uint2 y = *reinterpret_cast<const uint2 *>(&st.v[h][c][lane * 8]);
-                        w[h][0] = y.x;
-                        w[h][1] = y.y;
-                    }
-                }
-                bool nan = false;
-                if (!whole && r.count > 1) {
-                    // A row must not see a NaN code in a token that only other rows see: such codes leave
-                    // the product and come back below for the rows that do see them.
+                for (int c = 0; c < St::kVPieces; c++) {
+                    uint32_t w[4][St::kVBytes / 4];
 #pragma unroll
-                    for (int h = 0; h < 4; h++)
-#pragma unroll
-                        for (int i = 0; i < St::kVBytes / 4; i++)
-                            nan |= __vcmpeq4(w[h][i] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
-                    nan = __any_sync(~0u, nan);
-                }
-#pragma unroll
-                for (int i = 0; i < St::kVBytes / 4; i++) {
-#pragma unroll
-                    for (int half = 0; half < 2; half++) {
-                        // dimensions 4 i + 2 half (row g) and + 1 (row g + 8), tokens (2t, 2t+1) and (2t+8, 2t+9)
-                        const uint32_t sel = half ? 0x7362 : 0x5140;
-                        uint32_t lo = __byte_perm(w[0][i], w[1][i], sel), hi = __byte_perm(w[2][i], w[3][i], sel);
-                        const int j = c * (St::kVBytes / 2) + 2 * i + half;
-                        if (nan) {
-                            const uint32_t nl = __vcmpeq4(lo & 0x7f7f7f7fu, 0x7f7f7f7fu), nh = __vcmpeq4(hi & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                            lo &= ~nl;
-                            hi &= ~nh;
-                            const uint32_t a[4] = {f16x2_of(nl & 0x38383838u), f16x2_of((nl & 0x38383838u) >> 16),
-                                                   f16x2_of(nh & 0x38383838u), f16x2_of((nh & 0x38383838u) >> 16)};
-#pragma unroll
-                            for (int nt = 0; nt < NT; nt++) {
-                                const uint32_t one = 0x3c00u;
-                                const uint32_t s01 = ((seen[nt] & 1) ? one : 0) | ((seen[nt] & 2) ? one << 16 : 0);
-                                const uint32_t s23 = ((seen[nt] & 4) ? one : 0) | ((seen[nt] & 8) ? one << 16 : 0);
-                                float hit[4] = {0.f, 0.f, 0.f, 0.f};
-                                mma_f16(hit, a, transpose8x8(s01), transpose8x8(s23));
-#pragma unroll
-                                for (int k = 0; k < 4; k++)
-                                    if (hit[k] > 0.f) o[nt][j][k] = NAN;
-                            }
+                    for (int h = 0; h < 4; h++) {
+                        if constexpr (St::kVBytes == 16) {
+                            const uint4 y = *reinterpret_cast<const uint4 *>(&st.v[q][h][c][lane * 16]);
+                            w[h][0] = y.x;
+                            w[h][1] = y.y;
+                            w[h][2] = y.z;
+                            w[h][3] = y.w;
+                        } else {
+                            const uint2 y = *reinterpret_cast<const uint2 *>(&st.v[q][h][c][lane * 8]);
+                            w[h][0] = y.x;
+                            w[h][1] = y.y;
                         }
-                        const uint32_t a[4] = {f16x2_of(lo), f16x2_of(lo >> 16), f16x2_of(hi), f16x2_of(hi >> 16)};
-#pragma unroll
-                        for (int nt = 0; nt < NT; nt++) mma_f16(o[nt][j], a, pb[nt][0], pb[nt][1]);
                     }
+                    if (!whole && r.count > 1) keep_nan_apart(w, q, c, seen);
+#pragma unroll
+                    for (int i = 0; i < St::kVBytes / 4; i++)
+#pragma unroll
+                        for (int half = 0; half < 2; half++) {
+                            // dimensions 4 i + 2 half (row g) and + 1 (row g + 8), tokens (2t, 2t+1) and (2t+8, 2t+9)
+                            const uint32_t sel = half ? 0x7362 : 0x5140;
+                            const uint32_t lo = __byte_perm(w[0][i], w[1][i], sel), hi = __byte_perm(w[2][i], w[3][i], sel);
+                            const int j = c * (St::kVBytes / 2) + 2 * i + half;
+                            const uint32_t a[4] = {f16x2_of(lo), f16x2_of(lo >> 16), f16x2_of(hi), f16x2_of(hi >> 16)};
+#pragma unroll
+                            for (int nt = 0; nt < NT; nt++) mma_f16(o[nt][j], a, pb[q][nt][0], pb[q][nt][1]);
+                        }
                 }
-            }
         }
         cp_wait<0>();
 #pragma unroll
@@ -306,6 +360,43 @@ struct Tile {
                 l += __shfl_xor_sync(~0u, l, 16);
                 sum[nt][col] = l;
             }
+    }
+
+    // Where rows differ in the tokens they see, a row must not meet a NaN code of a token that only
+    // other rows see (0 * NaN): such codes leave the product, and the accumulators of the rows that do
+    // see them become NaN.
+    __device__ __forceinline__ void keep_nan_apart(uint32_t (&w)[4][Stage<D>::kVBytes / 4], int q, int c, const uint32_t (&seen)[NT]) {
+        constexpr int kWords = Stage<D>::kVBytes / 4;
+        bool nan = false;
+#pragma unroll
+        for (int h = 0; h < 4; h++)
+#pragma unroll
+            for (int i = 0; i < kWords; i++) nan |= (((w[h][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+        if (!__any_sync(~0u, nan)) return;
+#pragma unroll
+        for (int i = 0; i < kWords; i++)
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                const uint32_t sel = half ? 0x7362 : 0x5140;
+                const uint32_t nl = __vcmpeq4(__byte_perm(w[0][i], w[1][i], sel) & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0x38383838u;
+                const uint32_t nh = __vcmpeq4(__byte_perm(w[2][i], w[3][i], sel) & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0x38383838u;
+                const uint32_t a[4] = {f16x2_of(nl), f16x2_of(nl >> 16), f16x2_of(nh), f16x2_of(nh >> 16)};   // ones
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    const uint32_t one = 0x3c00u, m = seen[nt] >> (4 * q);
+                    const uint32_t s01 = ((m & 1) ? one : 0) | ((m & 2) ? one << 16 : 0);
+                    const uint32_t s23 = ((m & 4) ? one : 0) | ((m & 8) ? one << 16 : 0);
+                    float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_f16(hit, a, transpose8x8(s01), transpose8x8(s23));
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        if (hit[k] > 0.f) o[nt][c * (2 * kWords) + 2 * i + half][k] = NAN;
+                }
+            }
+#pragma unroll
+        for (int h = 0; h < 4; h++)
+#pragma unroll
+            for (int i = 0; i < kWords; i++) w[h][i] &= ~__vcmpeq4(w[h][i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
     }
 
     // Dimensions of this lane's accumulators: piece c covers 128 c + kVBytes g .., pairs in order.
@@ -369,7 +460,7 @@ struct Tile {
     }
 };
 
-template <int D, int NT>
+template <int D, int NT, bool kGrouped>
 __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(const AttnParams p) {
     constexpr int kWarps = warps_of<D, NT>(), kThreads = 32 * kWarps;
     constexpr int kPart = 8 * NT * (D + 2);
@@ -412,7 +503,7 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
             const int64_t tile = first + static_cast<int64_t>(rt) * per;      // the tile's first unit
             const int ua = static_cast<int>(u - tile);
             const int ub = static_cast<int>(end - tile < per ? end - tile : per);
-            Tile<D, NT> x;
+            Tile<D, NT, kGrouped> x;
             x.run(p, r, p.tables + static_cast<int64_t>(i) * p.W, head, rt, ua, ub, ring, s_valid[warp]);
             if (ua == 0 && ub == per) {
                 x.write(p, r, head, rt);
@@ -483,25 +574,21 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
         p.lse[static_cast<int64_t>(r.start + j) * p.Hkv * p.G + hq] = none ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool kGrouped>
 int launch(const AttnParams &p, int sms, cudaStream_t s) {
     constexpr int kWarps = warps_of<D, NT>();
     constexpr size_t smem = sizeof(Stage<D>) * kStages * kWarps;
-    static bool set[64] = {false};
-    int dev = 0;
-    PKV_CUDA_TRY(cudaGetDevice(&dev));
-    if (dev < 0 || dev >= 64 || !set[dev]) {
-        PKV_CUDA_TRY(cudaFuncSetAttribute(kv8_decode_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          static_cast<int>(smem)));
-        if (dev >= 0 && dev < 64) set[dev] = true;
-    }
-    PKV_CUDA_TRY(launch_pdl(kv8_decode_kernel<D, NT>, dim3(sms), dim3(32 * kWarps), smem, s, p));
+    static_assert(smem <= 220 * 1024, "shared memory");
+    PKV_CUDA_TRY(cudaFuncSetAttribute(kv8_decode_kernel<D, NT, kGrouped>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(smem)));
+    PKV_CUDA_TRY(launch_pdl(kv8_decode_kernel<D, NT, kGrouped>, dim3(sms), dim3(32 * kWarps), smem, s, p));
     return kv8_launch_merge(p, D, 8 * NT, sms * kWarps, p.Hkv, s);
 }
 
 template <int D>
 int launch_rows(const AttnParams &p, bool one_tile, int sms, cudaStream_t s) {
-    return one_tile ? launch<D, 1>(p, sms, s) : launch<D, 2>(p, sms, s);
+    if (p.bs % 16 == 0) return one_tile ? launch<D, 1, true>(p, sms, s) : launch<D, 2, true>(p, sms, s);
+    return one_tile ? launch<D, 1, false>(p, sms, s) : launch<D, 2, false>(p, sms, s);
 }
 
 }  // namespace
