@@ -14,10 +14,9 @@
 // of 32-token units of the batch; the warps of the KV heads of one range are
 // neighbours, so a token's line is read by one CTA at one time.  Keys are the
 // M side of the products (S^T = K Q^T, O^T = V^T P^T), so eight rows fill the
-// N side.  Each lane copies with cp.async exactly the codes that its own
-// fragments need into its own slots of a ring, so the ring needs no barrier
-// and no transpose: K by token rows, V as pairs of tokens merged with a byte
-// permute; e4m3 turns into f16 exactly on the way into the fragments, and P
+// N side.  A warp copies its unit's rows with cp.async into a stage of its own, whose
+// halves (keys, values) it refills as soon as it has taken them out; V comes
+// out as pairs of tokens merged with a byte permute, no transpose; e4m3 turns into f16 exactly on the way into the fragments, and P
 // moves from accumulator to operand layout with movmatrix.
 // A range that ends inside a request leaves a partial result (R, sum, O) that
 // a second kernel merges in a fixed order.
@@ -27,21 +26,29 @@ namespace pkv {
 namespace {
 
 constexpr int kUnit = 32;          // tokens per unit, two groups of 16
-constexpr int kStages = 2;
+constexpr int kDepth = 1;           // units whose codes are held or on their way; two measured no faster
 constexpr float kSlack = 14.f;     // growth of a row's maximum (log2) that R does not follow
 
+// A unit's codes, a row of D bytes per token, and its scales.  A row's 16-byte pieces are permuted
+// by f(token) = (token & 6) ^ ((token & 1) << 2) (pairs of 64-byte rows: by token >> 1), which makes
+// the fragment reads below free of bank conflicts: K rows g and g + 1 fall into different halves of
+// the banks, V tokens 2t into different quarters.
 template <int D>
 struct Stage {
     static constexpr int kKPieces = D / 64;                   // 16-byte pieces per lane and token row
     static constexpr int kVBytes = D / 8 < 16 ? D / 8 : 16;   // bytes per piece
     static constexpr int kVPieces = D / 8 / kVBytes;
-    uint4 k[2][2][kKPieces][32];
-    char v[2][4][kVPieces][32 * kVBytes];
+    static constexpr int kRowLanes = D / 16;                  // lanes that copy a token's row
+    static constexpr int kRows = 32 / kRowLanes;              // rows of one copy instruction
+    char k[kUnit * D], v[kUnit * D];
     float ks[kUnit], vs[kUnit];                               // by token, or by group
+    __device__ static __forceinline__ int swizzle(int piece, int token) {
+        return D == 64 ? piece ^ ((token >> 1) & 3) : piece ^ (token & 6) ^ ((token & 1) << 2);
+    }
 };
 
 template <int D, int NT>
-constexpr int warps_of() { return D > 128 ? 6 : NT == 1 ? 12 : 8; }
+constexpr int warps_of() { return D == 256 ? 6 : NT == 2 ? 8 : D == 128 ? 12 : 16; }
 
 // Units of a request: 32-token units of its visible range, once per tile of 8 * NT rows.
 template <int NT>
@@ -63,7 +70,7 @@ struct Tile {
     float top[NT][2], sum[NT][2];          // of columns 2t, 2t + 1
 
     __device__ __forceinline__ void run(const AttnParams &p, const Req &r, const int32_t *table, int head,
-                                        int rt, int ua, int ub, Stage<D> *ring, uint32_t *valid) {
+                                        int rt, int ua, int ub, Stage<D> *ring) {
         constexpr int S = D / 16;
         using St = Stage<D>;
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -105,107 +112,104 @@ struct Tile {
         if (ua >= ub) return;
 
         const int64_t line = static_cast<int64_t>(p.Hkv) * D;
-        // this lane's place in a group: rows g and g + 8 of K, tokens 2t, 2t + 1, 2t + 8, 2t + 9 of V
-        const uint8_t *kh = p.kc + head * D + 16 * t + (kGrouped ? g * line : 0);
-        const uint8_t *vh = p.vc + head * D + St::kVBytes * g + (kGrouped ? 2 * t * line : 0);
+        // copying: this lane moves 16 bytes of every kRows-th row, so that eight lanes ask for 128 (or
+        // 64) consecutive bytes
+        const int crow = lane / St::kRowLanes, cpiece = lane % St::kRowLanes;
+        const uint8_t *kh = p.kc + head * D + 16 * cpiece + (kGrouped ? crow * line : 0);
+        const uint8_t *vh = p.vc + head * D + 16 * cpiece + (kGrouped ? crow * line : 0);
 
-        // slot of token `lane` of unit u, kNone where it is not read; an id that is asked for one unit
-        // ahead is looked at here
+        // Block id of token `lane`'s (group of) unit u: asked for one unit ahead, looked at by place().
         auto ask = [&](int u) {
             const int s = base + u * kUnit + (kGrouped ? lane & 16 : lane);
             return u < ub && s < some_hi ? p.table_at(table, s) : -1;
         };
-        auto issue = [&](int u, int block) {
-            if (u < ub) {
-                St &st = ring[u % kStages];
-                const int s0 = base + u * kUnit, s = s0 + lane;
-                if (block >= p.num_blocks) {
-                    if (p.err && s >= some_lo && s < some_hi) atomicOr(p.err, PKV_DEVERR_BLOCK);
-                    block = -1;
+        // Where a unit's lines are: a bit for each token that is read; the offset of each group's first
+        // line (kGrouped) or this lane's token's slot.
+        struct Place {
+            uint32_t mask, slot;
+            int64_t at[2];
+            int32_t block;
+        };
+        auto place = [&](int u, int block) {
+            Place y;
+            const int s = base + u * kUnit + lane;
+            if (block >= p.num_blocks) {
+                if (p.err && s >= some_lo && s < some_hi) atomicOr(p.err, PKV_DEVERR_BLOCK);
+                block = -1;
+            }
+            y.block = block;
+            y.mask = __ballot_sync(~0u, u < ub && block >= 0 && s >= some_lo && s < some_hi);
+            y.slot = static_cast<uint32_t>(block) * static_cast<uint32_t>(p.bs) + static_cast<uint32_t>(s) % static_cast<uint32_t>(p.bs);
+            if constexpr (kGrouped) {
+                y.at[0] = static_cast<int64_t>(__shfl_sync(~0u, y.slot, 0)) * line;
+                y.at[1] = static_cast<int64_t>(__shfl_sync(~0u, y.slot, 16)) * line;
+            }
+            return y;
+        };
+        auto fetch = [&](const Place &y, const uint8_t *from, char *to) {
+            if (kGrouped && y.mask == ~0u) {
+#pragma unroll
+                for (int i = 0; i < kUnit; i += St::kRows) {
+                    const int r = i + crow;
+                    cp_async_full<16>(smem_addr(to + r * D + 16 * St::swizzle(cpiece, r)), from + y.at[i >> 4] + (i & 15) * line);
                 }
-                const bool live = block >= 0 && s >= some_lo && s < some_hi;
-                const uint32_t slot = static_cast<uint32_t>(block) * static_cast<uint32_t>(p.bs) + static_cast<uint32_t>(s) % static_cast<uint32_t>(p.bs);
-                const uint32_t mask = __ballot_sync(~0u, live);
-                if (lane == 0) valid[u % kStages] = mask;
-                if constexpr (kGrouped) {
-                    // lanes 0, 16: K scales; lanes 1, 17: V scales
-                    if ((lane & 15) < 2) {
-                        const float *sc = lane & 1 ? p.vs : p.ks;
-                        float *to = lane & 1 ? st.vs : st.ks;
-                        cp_async<4>(smem_addr(&to[lane >> 4]), sc + (block >= 0 ? static_cast<int64_t>(block) * p.Hkv + head : 0),
-                                    block >= 0);
-                    }
+            } else {
 #pragma unroll
-                    for (int q = 0; q < 2; q++) {
-                        const int64_t at = static_cast<int64_t>(__shfl_sync(~0u, slot, 16 * q)) * line;
-                        const uint32_t m = mask >> (16 * q);
-#pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const bool on = (m >> (g + 8 * h)) & 1;
-                            const uint8_t *src = kh + (on ? at + 8 * h * line : 0);
-#pragma unroll
-                            for (int c = 0; c < St::kKPieces; c++) cp_async<16>(smem_addr(&st.k[q][h][c][lane]), src + 64 * c, on);
-                        }
-#pragma unroll
-                        for (int h = 0; h < 4; h++) {
-                            const int tok = (h & 1) + 8 * (h >> 1);
-                            const bool on = (m >> (2 * t + tok)) & 1;
-                            const uint8_t *src = vh + (on ? at + tok * line : 0);
-#pragma unroll
-                            for (int c = 0; c < St::kVPieces; c++)
-                                cp_async<St::kVBytes>(smem_addr(&st.v[q][h][c][lane * St::kVBytes]), src + 128 * c, on);
-                        }
-                    }
-                } else {
-                    const int64_t sc = live ? static_cast<int64_t>(block) * p.Hkv + head : 0;
-                    cp_async<4>(smem_addr(&st.ks[lane]), p.ks + sc, live);
-                    cp_async<4>(smem_addr(&st.vs[lane]), p.vs + sc, live);
-#pragma unroll
-                    for (int q = 0; q < 2; q++) {
-#pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const int tok = 16 * q + g + 8 * h;
-                            const uint32_t x = __shfl_sync(~0u, slot, tok);
-                            const bool on = (mask >> tok) & 1;
-                            const uint8_t *src = kh + (on ? x * line : 0);
-#pragma unroll
-                            for (int c = 0; c < St::kKPieces; c++) cp_async<16>(smem_addr(&st.k[q][h][c][lane]), src + 64 * c, on);
-                        }
-#pragma unroll
-                        for (int h = 0; h < 4; h++) {
-                            const int tok = 16 * q + 2 * t + (h & 1) + 8 * (h >> 1);
-                            const uint32_t x = __shfl_sync(~0u, slot, tok);
-                            const bool on = (mask >> tok) & 1;
-                            const uint8_t *src = vh + (on ? x * line : 0);
-#pragma unroll
-                            for (int c = 0; c < St::kVPieces; c++)
-                                cp_async<St::kVBytes>(smem_addr(&st.v[q][h][c][lane * St::kVBytes]), src + 128 * c, on);
-                        }
-                    }
+                for (int i = 0; i < kUnit; i += St::kRows) {
+                    const int r = i + crow;
+                    const bool on = (y.mask >> r) & 1;
+                    const int64_t x = kGrouped ? y.at[i >> 4] + (i & 15) * line
+                                               : static_cast<int64_t>(__shfl_sync(~0u, y.slot, r)) * line;
+                    cp_async<16>(smem_addr(to + r * D + 16 * St::swizzle(cpiece, r)), from + (on ? x : 0), on);
                 }
             }
+        };
+        // A stage's keys are refilled when every lane has taken them out, then its values.
+        auto fetch_k = [&](const Place &y, Stage<D> &st) {
+            const bool on = kGrouped ? y.block >= 0 : (y.mask >> lane) & 1;
+            const int64_t sc = on ? static_cast<int64_t>(y.block) * p.Hkv + head : 0;
+            if constexpr (kGrouped) {
+                // lanes 0, 16: K scales; lanes 1, 17: V scales
+                if ((lane & 15) < 2) cp_async<4>(smem_addr(&(lane & 1 ? st.vs : st.ks)[lane >> 4]), (lane & 1 ? p.vs : p.ks) + sc, on);
+            } else {
+                cp_async<4>(smem_addr(&st.ks[lane]), p.ks + sc, on);
+                cp_async<4>(smem_addr(&st.vs[lane]), p.vs + sc, on);
+            }
+            fetch(y, kh, st.k);
+            cp_commit();
+        };
+        auto fetch_v = [&](const Place &y, Stage<D> &st) {
+            fetch(y, vh, st.v);
             cp_commit();
         };
 
         __syncwarp();
-        {
-            const int b = ask(ua);
-            issue(ua, b);
+        uint32_t masks[kDepth];                // of units u, u + 1, ..
+#pragma unroll
+        for (int k = 0; k < kDepth; k++) {
+            const Place y = place(ua + k, ask(ua + k));
+            masks[k] = y.mask;
+            fetch_k(y, ring[(ua + k) % kDepth]);
+            fetch_v(y, ring[(ua + k) % kDepth]);
         }
-        int ahead = ask(ua + 1);
+        int ahead = ask(ua + kDepth);
         for (int u = ua; u < ub; u++) {
-            __syncwarp();                      // everyone has left the stage that is filled next
-            {
-                const int b = ahead;
-                ahead = ask(u + 2);
-                issue(u + 1, b);
-            }
-            cp_wait<1>();
-            __syncwarp();
-            const St &st = ring[u % kStages];
-            const uint32_t mask = valid[u % kStages];
+            Stage<D> &st = ring[u % kDepth];
+            const Place next = place(u + kDepth, ahead);
+            ahead = ask(u + kDepth + 1);
+            const uint32_t mask = masks[0];
             const int s0 = base + u * kUnit;
-
+            cp_wait<2 * kDepth - 1>();         // the keys are here, all later copies may be on their way
+            __syncwarp();
+            float ks[2][2], vs[2][2];
+#pragma unroll
+            for (int q = 0; q < 2; q++)
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int at = kGrouped ? q : 16 * q + g + 8 * h;
+                    ks[q][h] = st.ks[at];
+                    vs[q][h] = value_scale(st.vs[at]);
+                }
             float x[2][NT][4];
 #pragma unroll
             for (int q = 0; q < 2; q++) {
@@ -219,8 +223,9 @@ struct Tile {
                 uint4 ka[2], kb[2];
 #pragma unroll
                 for (int q = 0; q < 2; q++) {
-                    ka[q] = st.k[q][0][c][lane];
-                    kb[q] = st.k[q][1][c][lane];
+                    const char *row = st.k + (16 * q + g) * D + 16 * St::swizzle(4 * c + t, g);
+                    ka[q] = *reinterpret_cast<const uint4 *>(row);
+                    kb[q] = *reinterpret_cast<const uint4 *>(row + 8 * D);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; i++)
@@ -233,6 +238,8 @@ struct Tile {
                         for (int nt = 0; nt < NT; nt++) mma_f16(x[q][nt], a, qb[nt][4 * c + i][0], qb[nt][4 * c + i][1]);
                     }
             }
+            __syncwarp();
+            fetch_k(next, st);
             const bool whole = mask == ~0u && s0 >= all_lo && s0 + kUnit <= all_hi;
             float iv[2][2];                    // of the lane's tokens g, g + 8 of both groups
             uint32_t seen[NT];                 // bit 4 q + c: the lane's value is visible
@@ -242,15 +249,14 @@ struct Tile {
             for (int q = 0; q < 2; q++)
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
-                    const int at = kGrouped ? q : 16 * q + g + 8 * h;
-                    const float ks = st.ks[at], vs = value_scale(st.vs[at]), lv = __log2f(vs);
-                    iv[q][h] = __frcp_rn(vs);
+                    const float lv = __log2f(vs[q][h]);
+                    iv[q][h] = __frcp_rn(vs[q][h]);
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                         for (int col = 0; col < 2; col++) {
                             float &y = x[q][nt][2 * h + col];
-                            y = fmaf(y, cf[nt][col] * ks, lv);
+                            y = fmaf(y, cf[nt][col] * ks[q][h], lv);
                         }
                 }
             if (!whole) {
@@ -315,6 +321,8 @@ struct Tile {
                     pb[q][nt][1] = transpose8x8(pack_f16(w[2], w[3]));
                 }
             }
+            cp_wait<2 * kDepth - 1>();         // the values are here
+            __syncwarp();
 #pragma unroll
             for (int q = 0; q < 2; q++)
 #pragma unroll
@@ -322,14 +330,15 @@ struct Tile {
                     uint32_t w[4][St::kVBytes / 4];
 #pragma unroll
                     for (int h = 0; h < 4; h++) {
+                        const int r = 16 * q + 2 * t + (h & 1) + 8 * (h >> 1);
                         if constexpr (St::kVBytes == 16) {
-                            const uint4 y = *reinterpret_cast<const uint4 *>(&st.v[q][h][c][lane * 16]);
+                            const uint4 y = *reinterpret_cast<const uint4 *>(st.v + r * D + 16 * St::swizzle(8 * c + g, r));
                             w[h][0] = y.x;
                             w[h][1] = y.y;
                             w[h][2] = y.z;
                             w[h][3] = y.w;
                         } else {
-                            const uint2 y = *reinterpret_cast<const uint2 *>(&st.v[q][h][c][lane * 8]);
+                            const uint2 y = *reinterpret_cast<const uint2 *>(st.v + r * D + 16 * St::swizzle(g >> 1, r) + 8 * (g & 1));
                             w[h][0] = y.x;
                             w[h][1] = y.y;
                         }
@@ -348,6 +357,11 @@ struct Tile {
                             for (int nt = 0; nt < NT; nt++) mma_f16(o[nt][j], a, pb[q][nt][0], pb[q][nt][1]);
                         }
                 }
+            __syncwarp();
+            fetch_v(next, st);
+#pragma unroll
+            for (int k = 0; k + 1 < kDepth; k++) masks[k] = masks[k + 1];
+            masks[kDepth - 1] = next.mask;
         }
         cp_wait<0>();
 #pragma unroll
@@ -467,7 +481,6 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
     extern __shared__ __align__(16) char s_ring[];
     __shared__ int64_t s_prefix[kThreads + 1];
     __shared__ int64_t s_warp[kWarps];
-    __shared__ uint32_t s_valid[kWarps][kStages];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -487,7 +500,7 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
     if (range < ranges) {
         int64_t u = range * total / ranges;
         const int64_t end = (range + 1) * total / ranges;
-        Stage<D> *ring = reinterpret_cast<Stage<D> *>(s_ring) + warp * kStages;
+        Stage<D> *ring = reinterpret_cast<Stage<D> *>(s_ring) + warp * kDepth;
         int64_t first;
         int i = plan_find<kThreads>(s_prefix, p.n, u, units, &first);
         while (u < end) {
@@ -504,7 +517,7 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
             const int ua = static_cast<int>(u - tile);
             const int ub = static_cast<int>(end - tile < per ? end - tile : per);
             Tile<D, NT, kGrouped> x;
-            x.run(p, r, p.tables + static_cast<int64_t>(i) * p.W, head, rt, ua, ub, ring, s_valid[warp]);
+            x.run(p, r, p.tables + static_cast<int64_t>(i) * p.W, head, rt, ua, ub, ring);
             if (ua == 0 && ub == per) {
                 x.write(p, r, head, rt);
             } else {
@@ -548,21 +561,42 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
     float sum = 0.f, acc[kPer];
 #pragma unroll
     for (int c = 0; c < kPer; c++) acc[c] = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < pieces; k++) {
-        const float *a = part(k);
-        const float m = a[row], l = a[rows + row];
-        // a piece without a top adds nothing, unless its logits were NaN
-        const float f2 = m == -INFINITY ? (l == 0.f ? 0.f : NAN) : exp2_fast(m - top);
-        sum += f2 * l;
-        const float *o = a + 2 * rows + row * D + lane * kPer;
+    for (int k0 = 0; k0 < pieces; k0 += 32) {
+        // a piece's factor, in the lane of its number; a piece without a top adds nothing, unless its
+        // logits were NaN
+        float fac = 0.f;
+        if (k0 + lane < pieces) {
+            const float *a = part(k0 + lane);
+            const float m = a[row], l = a[rows + row];
+            fac = m == -INFINITY ? (l == 0.f ? 0.f : NAN) : exp2_fast(m - top);
+            sum += fac * l;
+        }
+        // sixteen rows on their way at a time
+        const int n = min(32, pieces - k0);
+        for (int k1 = 0; k1 < n; k1 += 16) {
+            float y[16][kPer];
 #pragma unroll
-        for (int c = 0; c < kPer; c += 2) {
-            const float2 y = *reinterpret_cast<const float2 *>(o + c);
-            acc[c] += f2 == 0.f ? 0.f : f2 * y.x;
-            acc[c + 1] += f2 == 0.f ? 0.f : f2 * y.y;
+            for (int k = 0; k < 16; k++) {
+                const float *o = part(k0 + min(k1 + k, n - 1)) + 2 * rows + row * D + lane * kPer;
+#pragma unroll
+                for (int c = 0; c < kPer; c += 2) {
+                    const float2 z = *reinterpret_cast<const float2 *>(o + c);
+                    y[k][c] = z.x;
+                    y[k][c + 1] = z.y;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 16; k++) {
+                const float f2 = __shfl_sync(~0u, fac, k1 + k);
+                if (k1 + k < n && f2 != 0.f) {
+#pragma unroll
+                    for (int c = 0; c < kPer; c++) acc[c] = fmaf(f2, y[k][c], acc[c]);
+                }
+            }
         }
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     const bool none = top == -INFINITY && sum == 0.f;
     const int j = f / p.G, hq = head * p.G + f - j * p.G;
     const float inv = none ? 0.f : 1.f / sum;
@@ -577,7 +611,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
 template <int D, int NT, bool kGrouped>
 int launch(const AttnParams &p, int sms, cudaStream_t s) {
     constexpr int kWarps = warps_of<D, NT>();
-    constexpr size_t smem = sizeof(Stage<D>) * kStages * kWarps;
+    constexpr size_t smem = sizeof(Stage<D>) * kDepth * kWarps;
     static_assert(smem <= 220 * 1024, "shared memory");
     PKV_CUDA_TRY(cudaFuncSetAttribute(kv8_decode_kernel<D, NT, kGrouped>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                       static_cast<int>(smem)));
