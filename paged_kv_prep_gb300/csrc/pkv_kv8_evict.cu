@@ -10,11 +10,16 @@
 // blocks changes, so they may be shared.
 //
 // Selection: the r-th largest weight by a radix select over order-preserving
-// integer keys, eight bits a pass, then one ordered pass in which a token's
-// place follows from two running counts (larger ones, equal ones).  A CTA per
-// request; bound by the passes' latency.
+// integer keys in three passes of 11, 11 and 10 bits, then one ordered pass in
+// which a token's place follows from two running counts (larger ones, equal
+// ones).  A request is one CTA's, or a cluster's of eight where tables are
+// long; the keys stay in shared memory after the first pass, and the clusters'
+// histograms and counts meet through distributed shared memory.  Bound by the
+// passes' latency.
 //
-// Copy: a CTA per new block; bound by HBM (4 * line bytes per kept token).
+// Copy: a CTA per new block moves its K and V lines; the lines are on their way
+// before the new scales are known.  Bound by HBM (4 * line bytes per kept
+// token).
 #include "pkv_async.cuh"
 #include "pkv_kv8.cuh"
 
@@ -46,188 +51,317 @@ __device__ __forceinline__ uint32_t key_of(float w) {
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictParams p) {
-    __shared__ uint32_t s_hist[256];
+// Distributed shared memory: a value of CTA `rank` of this cluster.
+template <typename T>
+__device__ __forceinline__ T of_rank(const T *at, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(pkv::smem_addr(at)), "r"(rank));
+    uint32_t v;
+    static_assert(sizeof(T) == 4, "32-bit values");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return static_cast<T>(v);
+}
+template <int kCluster>
+__device__ __forceinline__ void sync_all() {
+    if constexpr (kCluster == 1) {
+        __syncthreads();
+    } else {
+        asm volatile("barrier.cluster.arrive;" ::: "memory");
+        asm volatile("barrier.cluster.wait;" ::: "memory");
+    }
+}
+
+// One cluster of kCluster CTAs per request; `cap` keys fit the dynamic shared memory.
+template <int kCluster>
+__global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictParams p, int cap) {
+    constexpr int kBins = 2048, kWarps = kSelThreads / 32;
+    extern __shared__ uint32_t s_key[];
+    __shared__ uint32_t s_hist[2][kBins];              // two, so that a pass clears while others still read
     __shared__ uint32_t s_bad;
-    __shared__ uint32_t s_prefix, s_need;
-    __shared__ uint64_t s_warp[kSelThreads / 32];
+    __shared__ uint32_t s_digit, s_before;
+    __shared__ uint32_t s_gt[kWarps + 1], s_eq[kWarps + 1];   // by warp; the last: the CTA's totals
+    __shared__ uint32_t s_sum[kWarps];
     pkv::pdl_wait();
     pkv::pdl_trigger();
-    const int req = blockIdx.x, tid = threadIdx.x;
-    const int lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int req = blockIdx.x / kCluster, rank = blockIdx.x % kCluster, all = rank * kSelThreads + tid;
+    constexpr int kAll = kCluster * kSelThreads;
     const int32_t *table = p.tables + static_cast<int64_t>(req) * p.W;
     const int32_t *fresh = p.new_tables + static_cast<int64_t>(req) * p.W2;
     int32_t *kept = p.kept + static_cast<int64_t>(req) * p.budget;
     const int64_t L64 = p.lens[req];
     const int bs = p.bs;
     if (tid == 0) s_bad = 0;
+    for (int i = tid; i < 2 * kBins; i += kSelThreads) (&s_hist[0][0])[i] = 0;
     __syncthreads();
     const int64_t n64 = L64 < p.budget ? L64 : p.budget;
     uint32_t bad = 0;
     if (L64 < 0 || L64 > static_cast<int64_t>(p.W) * bs || n64 > static_cast<int64_t>(p.W2) * bs)
         bad = PKV_DEVERR_POSITION;
     if (!bad) {
-        for (int64_t j = tid; j * bs < L64; j += kSelThreads)
+        for (int64_t j = all; j * bs < L64; j += kAll)
             if (table[j] < 0 || table[j] >= p.num_blocks) bad = PKV_DEVERR_BLOCK;
-        for (int64_t j = tid; j * bs < n64; j += kSelThreads)
+        for (int64_t j = all; j * bs < n64; j += kAll)
             if (fresh[j] < 0 || fresh[j] >= p.num_blocks) bad = PKV_DEVERR_BLOCK;
     }
     if (bad) atomicOr(&s_bad, bad);
-    __syncthreads();
-    if (s_bad) {
-        if (tid == 0) {
+    sync_all<kCluster>();
+    bad = 0;
+#pragma unroll
+    for (int c = 0; c < kCluster; c++) bad |= of_rank(&s_bad, c);
+    if (bad) {
+        if (all == 0) {
             p.new_lens[req] = -1;
-            if (p.err) atomicOr(p.err, static_cast<int32_t>(s_bad));
+            if (p.err) atomicOr(p.err, static_cast<int32_t>(bad));
         }
-        for (int j = tid; j < p.budget; j += kSelThreads) kept[j] = -1;
+        for (int j = all; j < p.budget; j += kAll) kept[j] = -1;
+        sync_all<kCluster>();                          // nobody leaves while its memory is read
         return;
     }
     const int L = static_cast<int>(L64), n = static_cast<int>(n64);
-    if (tid == 0) p.new_lens[req] = n;
-    for (int j = n + tid; j < p.budget; j += kSelThreads) kept[j] = -1;
-    if (L <= p.budget) {
-        for (int j = tid; j < n; j += kSelThreads) kept[j] = j;
-        return;
-    }
-    auto weight_key = [&](int pos) {
-        const int b = pos / bs;
-        return key_of(p.weights[static_cast<int64_t>(table[b]) * bs + (pos - b * bs)]);
-    };
+    if (all == 0) p.new_lens[req] = n;
+    for (int j = n + all; j < p.budget; j += kAll) kept[j] = -1;
     const int lo = p.first, hi = L - p.last;           // candidates lo..hi-1
     const int r = p.budget - p.first - p.last;
-    for (int j = tid; j < p.first; j += kSelThreads) kept[j] = j;
-    for (int j = tid; j < p.last; j += kSelThreads) kept[p.budget - p.last + j] = hi + j;
-    if (r == 0) return;
+    if (L <= p.budget) {
+        for (int j = all; j < n; j += kAll) kept[j] = j;
+    } else {
+        for (int j = all; j < p.first; j += kAll) kept[j] = j;
+        for (int j = all; j < p.last; j += kAll) kept[p.budget - p.last + j] = hi + j;
+    }
+    if (L <= p.budget || r == 0) {
+        sync_all<kCluster>();
+        return;
+    }
+    // this CTA's candidates, a stretch per warp
+    const int stretch = 32 * ((hi - lo + kAll - 1) / kAll);
+    const int begin = lo + (rank * kWarps + warp) * stretch;
+    const int mine = min(max(hi - begin, 0), stretch);
+    const bool hold = stretch * kWarps <= cap;
+    uint32_t *keys = s_key + warp * stretch;
+    auto weight_key = [&](int i) {
+        const int pos = begin + i, b = pos / bs;
+        return key_of(p.weights[static_cast<int64_t>(table[b]) * bs + (pos - b * bs)]);
+    };
+    uint32_t prefix = 0, need = static_cast<uint32_t>(r);
+    // the r-th largest key, from the top digit down
+#pragma unroll 1
+    for (int pass = 0; pass < 3; pass++) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+        uint32_t *hist = s_hist[pass & 1];
+        const uint32_t above = pass == 0 ? 0u : 0xffffffffu << (pass == 1 ? 21 : 10);
+        for (int i = lane; i < mine; i += 32) {
+            uint32_t k;
+            if (pass > 0 && hold) {
+                k = keys[i];
+            } else {
+                k = weight_key(i);
+                if (hold) keys[i] = k;
+            }
+            if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+        }
+        sync_all<kCluster>();
+        // thread t holds digits bins-1 - 2t and the one below it, largest first
+        uint32_t c0 = 0, c1 = 0;
+        const int d0 = bins - 1 - 2 * tid;
+        if (d0 > 0) {
+#pragma unroll
+            for (int c = 0; c < kCluster; c++) {
+                c0 += of_rank(&hist[d0], c);
+                c1 += of_rank(&hist[d0 - 1], c);
+            }
+        }
+        uint32_t incl = c0 + c1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o) incl += u;
+        }
+        if (lane == 31) s_sum[warp] = incl;
+        __syncthreads();
+        uint32_t base = lane < warp ? s_sum[lane] : 0;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) base += __shfl_xor_sync(~0u, base, o);
+        incl += base;
+        const uint32_t before = incl - c0 - c1;
+        if (before < need && need <= incl) {           // one thread
+            const bool second = before + c0 < need;
+            s_digit = static_cast<uint32_t>(d0 - second);
+            s_before = before + (second ? c0 : 0);
+        }
+        // the other histogram is free: everyone is past its last reading
+        for (int i = tid; i < kBins; i += kSelThreads) s_hist[(pass & 1) ^ 1][i] = 0;
+        __syncthreads();
+        prefix |= s_digit << shift;
+        need -= s_before;
+    }
+    const uint32_t pivot = prefix, ties = need;        // keep every key > pivot and the first `ties` equal ones
+    // places in order: counts of larger and equal keys before each stretch
+    uint32_t gt = 0, eq = 0;
+    for (int i = lane; i < mine; i += 32) {
+        const uint32_t k = hold ? keys[i] : weight_key(i);
+        gt += k > pivot;
+        eq += k == pivot;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        gt += __shfl_xor_sync(~0u, gt, o);
+        eq += __shfl_xor_sync(~0u, eq, o);
+    }
+    if (lane == 0) {
+        s_gt[warp] = gt;
+        s_eq[warp] = eq;
+    }
+    __syncthreads();
+    uint32_t g = lane < warp ? s_gt[lane] : 0, e = lane < warp ? s_eq[lane] : 0, ag = s_gt[lane], ae = s_eq[lane];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        g += __shfl_xor_sync(~0u, g, o);
+        e += __shfl_xor_sync(~0u, e, o);
+        ag += __shfl_xor_sync(~0u, ag, o);
+        ae += __shfl_xor_sync(~0u, ae, o);
+    }
     if (tid == 0) {
-        s_prefix = 0;
-        s_need = static_cast<uint32_t>(r);
+        s_gt[kWarps] = ag;
+        s_eq[kWarps] = ae;
     }
-    // the r-th largest key, eight bits at a time from the top
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        for (int i = tid; i < 256; i += kSelThreads) s_hist[i] = 0;
-        __syncthreads();
-        const uint32_t prefix = s_prefix;
-        const uint32_t above = shift == 24 ? 0 : 0xffffffffu << (shift + 8);
-        for (int pos = lo + tid; pos < hi; pos += kSelThreads) {
-            const uint32_t k = weight_key(pos);
-            if ((k & above) == prefix) atomicAdd(&s_hist[(k >> shift) & 255], 1u);
+    sync_all<kCluster>();
+#pragma unroll
+    for (int c = 0; c + 1 < kCluster; c++)
+        if (c < rank) {
+            g += of_rank(&s_gt[kWarps], c);
+            e += of_rank(&s_eq[kWarps], c);
         }
-        __syncthreads();
-        if (warp == 0) {
-            // lane l holds digits 255 - 8l .. 248 - 8l, largest first
-            uint32_t c[8], sum = 0;
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                c[i] = s_hist[255 - 8 * lane - i];
-                sum += c[i];
-            }
-            uint32_t incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t u = __shfl_up_sync(~0u, incl, o);
-                if (lane >= o) incl += u;
-            }
-            const uint32_t need = s_need;
-            uint32_t seen = incl - sum;
-            if (seen < need && need <= incl) {
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    if (seen < need && need <= seen + c[i]) {
-                        s_prefix = prefix | (static_cast<uint32_t>(255 - 8 * lane - i) << shift);
-                        s_need = need - seen;
-                        seen = need;               // found: no later digit matches
-                    } else {
-                        seen += c[i];
-                    }
-                }
-            }
-        }
-        __syncthreads();
-    }
-    const uint32_t pivot = s_prefix, ties = s_need;    // keep every key > pivot and the first `ties` equal ones
-    // places in order: larger ones in the low word of the count, equal ones in the high word
-    uint64_t base = 0;
-    for (int at = lo; at < hi; at += kSelThreads) {
-        const int pos = at + tid;
+    const uint32_t below = (1u << lane) - 1;
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+        const int i = i0 + lane;
         uint32_t k = 0;
-        bool in = pos < hi;
-        if (in) k = weight_key(pos);
-        const bool gt = in && k > pivot, eq = in && k == pivot;
-        const uint32_t bg = __ballot_sync(~0u, gt), be = __ballot_sync(~0u, eq);
-        if (lane == 0) s_warp[warp] = static_cast<uint64_t>(__popc(bg)) | (static_cast<uint64_t>(__popc(be)) << 32);
-        __syncthreads();
-        uint64_t mine = lane < warp ? s_warp[lane] : 0, all = s_warp[lane];
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-            mine += __shfl_xor_sync(~0u, mine, o);
-            all += __shfl_xor_sync(~0u, all, o);
-        }
-        const uint32_t below = (1u << lane) - 1;
-        const uint64_t before = base + mine;
-        const uint32_t g = static_cast<uint32_t>(before) + __popc(bg & below);
-        const uint32_t e = static_cast<uint32_t>(before >> 32) + __popc(be & below);
-        if (gt || (eq && e < ties)) kept[lo + g + (e < ties ? e : ties)] = pos;
-        base += all;
-        __syncthreads();
+        if (i < mine) k = hold ? keys[i] : weight_key(i);
+        const uint32_t bg = __ballot_sync(~0u, i < mine && k > pivot), be = __ballot_sync(~0u, i < mine && k == pivot);
+        const uint32_t here = e + __popc(be & below);
+        const bool is_gt = (bg >> lane) & 1, is_eq = (be >> lane) & 1;
+        if (is_gt || (is_eq && here < ties)) kept[lo + g + __popc(bg & below) + (here < ties ? here : ties)] = begin + i;
+        g += __popc(bg);
+        e += __popc(be);
     }
+    sync_all<kCluster>();                              // nobody leaves while its memory is read
 }
 
-// grid (new blocks per request, requests, K and V)
-__global__ void __launch_bounds__(kCopyThreads) kv8_copy_kernel(const EvictParams p) {
-    __shared__ int64_t s_src[kCopyLines];
-    extern __shared__ float s_scale[];                 // [heads]
+// grid (new blocks per request, requests)
+constexpr int kCopyHold = 4;                           // 16-byte pieces of K (and of V) that a thread holds
+
+__global__ void __launch_bounds__(kCopyThreads, 4) kv8_copy_kernel(const EvictParams p, int chunk_shift, int head_shift) {
+    __shared__ uint32_t s_src[kCopyLines];             // slot and block that a line comes from
+    __shared__ int32_t s_block[kCopyLines];
+    extern __shared__ float s_scale[];                 // [2][heads]
     pkv::pdl_wait();
     pkv::pdl_trigger();
-    const int req = blockIdx.y, tid = threadIdx.x, bs = p.bs;
-    const bool is_v = blockIdx.z != 0;
-    const int n = p.new_lens[req];
+    const int req = blockIdx.y, tid = threadIdx.x, bs = p.bs, heads = p.heads;
     const int64_t d0 = static_cast<int64_t>(blockIdx.x) * bs;
+    // what the block is made from is asked for together: its lines' old positions, its new id
+    const int first = d0 + tid < p.budget && tid < kCopyLines ? p.kept[static_cast<int64_t>(req) * p.budget + d0 + tid] : -1;
+    const int64_t block = p.new_tables[static_cast<int64_t>(req) * p.W2 + blockIdx.x];
+    const int n = p.new_lens[req];
     if (d0 >= n) return;                               // also a refused request (-1)
     const int lines = n - d0 < bs ? static_cast<int>(n - d0) : bs;
     const int32_t *table = p.tables + static_cast<int64_t>(req) * p.W;
     const int32_t *kept = p.kept + static_cast<int64_t>(req) * p.budget + d0;
-    const int64_t block = p.new_tables[static_cast<int64_t>(req) * p.W2 + blockIdx.x];
-    const uint8_t *from = is_v ? p.vc : p.kc;
-    uint8_t *to = is_v ? p.vd : p.kd;
-    float *scale = is_v ? p.vs : p.ks;
-    const int heads = p.heads;
+    const int chunks = p.line / 16;                    // a head has 2^head_shift of them
 
-    for (int h = tid; h < heads; h += kCopyThreads) s_scale[h] = 0.f;
-    __syncthreads();
-    for (int i = tid; i < lines * heads; i += kCopyThreads) {
-        const int l = i / heads, h = i - l * heads;
-        const int64_t b = table[kept[l] / bs];
-        // positive floats order as integers
-        atomicMax(reinterpret_cast<int *>(&s_scale[h]), __float_as_int(scale[b * heads + h]));
-    }
-    __syncthreads();
-    for (int h = tid; h < heads; h += kCopyThreads) scale[block * heads + h] = s_scale[h];
-    const int chunks = p.line / 16, per_head = chunks / heads;
+    for (int h = tid; h < 2 * heads; h += kCopyThreads) s_scale[h] = 0.f;
     for (int l0 = 0; l0 < lines; l0 += kCopyLines) {
         const int m = lines - l0 < kCopyLines ? lines - l0 : kCopyLines;
         __syncthreads();
         if (tid < m) {
-            const int pos = kept[l0 + tid], b = pos / bs;
-            const int64_t src = static_cast<int64_t>(table[b]) * bs + (pos - b * bs);
+            const int pos = l0 == 0 ? first : kept[l0 + tid], b = pos / bs;
+            const int32_t id = table[b];
+            const uint32_t src = static_cast<uint32_t>(id) * static_cast<uint32_t>(bs) + static_cast<uint32_t>(pos - b * bs);
             s_src[tid] = src;
-            if (!is_v) p.weights[block * bs + l0 + tid] = p.weights[src];
+            s_block[tid] = id;
+            p.weights[block * bs + l0 + tid] = p.weights[src];
         }
         __syncthreads();
-        for (int i = tid; i < m * chunks; i += kCopyThreads) {
-            const int l = i / chunks, c = i - l * chunks, h = c / per_head;
-            const int64_t src = s_src[l];
-            uint4 v = *reinterpret_cast<const uint4 *>(from + src * p.line + c * 16);
-            const float old = scale[src / bs * heads + h];
-            if (old != s_scale[h]) {
-                const float ratio = __fdiv_rn(old, s_scale[h]);
-                v.x = pkv::requantise4(v.x, ratio);
-                v.y = pkv::requantise4(v.y, ratio);
-                v.z = pkv::requantise4(v.z, ratio);
-                v.w = pkv::requantise4(v.w, ratio);
+        // the first round's pieces and their scales are on their way before the new scales are known
+        const int count = m * chunks;
+        for (int i0 = 0; i0 < count; i0 += kCopyThreads * kCopyHold) {
+            uint4 kv[kCopyHold][2];
+            float old[kCopyHold][2];
+#pragma unroll
+            for (int u = 0; u < kCopyHold; u++) {
+                const int i = i0 + u * kCopyThreads + tid;
+                if (i < count) {
+                    const int l = chunk_shift >= 0 ? i >> chunk_shift : i / chunks, c = i - l * chunks;
+                    const int64_t from = static_cast<int64_t>(s_src[l]) * p.line + c * 16;
+                    const int64_t at = static_cast<int64_t>(s_block[l]) * heads + (c >> head_shift);
+                    kv[u][0] = __ldg(reinterpret_cast<const uint4 *>(p.kc + from));
+                    kv[u][1] = __ldg(reinterpret_cast<const uint4 *>(p.vc + from));
+                    old[u][0] = p.ks[at];
+                    old[u][1] = p.vs[at];
+                }
             }
-            *reinterpret_cast<uint4 *>(to + (block * bs + l0 + l) * p.line + c * 16) = v;
+            if (l0 == 0 && i0 == 0) {
+                // positive floats order as integers
+                for (int i = tid; i < lines * heads; i += kCopyThreads) {
+                    const int l = i / heads, h = i - l * heads;
+                    const int64_t b = l < kCopyLines ? s_block[l] : table[kept[l] / bs], at = b * heads + h;
+                    atomicMax(reinterpret_cast<int *>(&s_scale[h]), __float_as_int(p.ks[at]));
+                    atomicMax(reinterpret_cast<int *>(&s_scale[heads + h]), __float_as_int(p.vs[at]));
+                }
+                __syncthreads();
+                for (int h = tid; h < heads; h += kCopyThreads) {
+                    p.ks[block * heads + h] = s_scale[h];
+                    p.vs[block * heads + h] = s_scale[heads + h];
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < kCopyHold; u++) {
+                const int i = i0 + u * kCopyThreads + tid;
+                if (i < count) {
+                    const int l = chunk_shift >= 0 ? i >> chunk_shift : i / chunks, c = i - l * chunks, h = c >> head_shift;
+                    const int64_t to = (block * bs + l0 + l) * p.line + c * 16;
+#pragma unroll
+                    for (int w = 0; w < 2; w++) {
+                        const float now = s_scale[w * heads + h];
+                        uint4 v = kv[u][w];
+                        if (old[u][w] != now) {
+                            const float ratio = old[u][w] * __frcp_rn(now);    // exact between powers of two
+                            v.x = pkv::requantise4(v.x, ratio);
+                            v.y = pkv::requantise4(v.y, ratio);
+                            v.z = pkv::requantise4(v.z, ratio);
+                            v.w = pkv::requantise4(v.w, ratio);
+                        }
+                        *reinterpret_cast<uint4 *>((w ? p.vd : p.kd) + to) = v;
+                    }
+                }
+            }
         }
     }
+}
+
+constexpr int kSelCap = 16384;                         // keys held per CTA: 64 KB
+
+template <int kCluster>
+cudaError_t launch_select(const EvictParams &p, int n, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(kv8_select_kernel<kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCap * 4);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(n) * kCluster);
+    cfg.blockDim = dim3(kSelThreads);
+    // a CTA holds what its share of the longest table row needs, kSelCap at most
+    const int64_t share = (static_cast<int64_t>(p.W) * p.bs + kCluster * kSelThreads - 1) / (kCluster * kSelThreads) * kSelThreads;
+    const int cap = share < kSelCap ? static_cast<int>(share) : kSelCap;
+    cfg.dynamicSmemBytes = static_cast<size_t>(cap) * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kCluster == 1 ? 1 : 2;
+    return cudaLaunchKernelEx(&cfg, kv8_select_kernel<kCluster>, p, cap);
 }
 
 }  // namespace
@@ -269,9 +403,17 @@ extern "C" int pkv_kv8_evict(const pkv_kv8_cache *cache, float *weights,
     p.kept = kept;
     p.err = d_error;
     cudaStream_t s = pkv::as_stream(stream);
-    PKV_CUDA_TRY(pkv::launch_pdl(kv8_select_kernel, dim3(n), dim3(kSelThreads), 0, s, p));
+    // Eight CTAs share a request where tables reach past 16384 tokens (one CTA holds that many keys):
+    // four requests of 131072 tokens MEASURE.
+    if (static_cast<int64_t>(p.W) * p.bs > kSelCap)
+        PKV_CUDA_TRY(launch_select<8>(p, n, s));
+    else
+        PKV_CUDA_TRY(launch_select<1>(p, n, s));
     const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(budget) + p.bs - 1) / p.bs);
-    PKV_CUDA_TRY(pkv::launch_pdl(kv8_copy_kernel, dim3(blocks, n, 2), dim3(kCopyThreads),
-                                 p.heads * sizeof(float), s, p));
+    const int chunks = p.line / 16;
+    const int chunk_shift = (chunks & (chunks - 1)) ? -1 : 31 - __builtin_clz(static_cast<unsigned>(chunks));
+    const int head_shift = cache->head_dim == 64 ? 2 : cache->head_dim == 128 ? 3 : 4;
+    PKV_CUDA_TRY(pkv::launch_pdl(kv8_copy_kernel, dim3(blocks, n), dim3(kCopyThreads), 2 * p.heads * sizeof(float), s, p,
+                                 chunk_shift, head_shift));
     return PKV_OK;
 }
