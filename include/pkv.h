@@ -613,10 +613,11 @@ int pkv_kv8_store(const pkv_kv8_cache *cache, const void *k, const void *v,
                   const int64_t *slot_mapping, int32_t num_tokens, int32_t *d_error,
                   pkv_stream_t stream);
 
-/* Bytes of device workspace that pkv_kv8_attention takes (the same for every
-   batch); its contents need no initialisation and may be reused by the next
-   call on the same stream. */
-int pkv_kv8_attention_workspace(int32_t num_heads, int32_t head_dim, int64_t *bytes);
+/* Bytes of device workspace that pkv_kv8_attention takes for up to num_tokens
+   tokens (with_weights: when weights are added up too).  Its contents need no
+   initialisation and it may be reused by the next call on the same stream. */
+int pkv_kv8_attention_workspace(int32_t num_tokens, int32_t num_q_heads, int32_t head_dim,
+                                int32_t with_weights, int64_t *bytes);
 
 /*
  * Attention of a prepared batch's queries over the cache.  Request i's tokens

@@ -149,7 +149,7 @@ def _declare(lib):
         "pkv_version": [],
         "pkv_selftest_wait_timeout": [_VP, C.c_uint32, _VP],
         "pkv_kv8_store": [C.POINTER(Kv8CacheArgs), _VP, _VP, i64, i64, i32, _VP, i32, _VP, _VP],
-        "pkv_kv8_attention_workspace": [i32, i32, C.POINTER(i64)],
+        "pkv_kv8_attention_workspace": [i32, i32, i32, i32, C.POINTER(i64)],
         "pkv_kv8_attention": [C.POINTER(Kv8CacheArgs), _VP, i64, i32, i32, _VP, i32, _VP, _VP, i32,
                               i32, C.c_float, i32, _VP, i64, _VP, _VP, _VP, i64, _VP, _VP],
         "pkv_kv8_evict": [C.POINTER(Kv8CacheArgs), _VP, _VP, i32, _VP, i32, _VP, i32, i32, i32, i32,
@@ -877,10 +877,11 @@ def kv8_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, d_error=No
     return rc
 
 
-def kv8_attention_workspace(num_heads, head_dim):
+def kv8_attention_workspace(num_tokens, num_q_heads, head_dim, with_weights=False):
     """Bytes of device workspace an attention call takes (``pkv_kv8_attention_workspace``)."""
     n = C.c_int64(0)
-    _check(lib().pkv_kv8_attention_workspace(int(num_heads), int(head_dim), C.byref(n)),
+    _check(lib().pkv_kv8_attention_workspace(int(num_tokens), int(num_q_heads), int(head_dim),
+                                             int(bool(with_weights)), C.byref(n)),
            "pkv_kv8_attention_workspace")
     return n.value
 
@@ -921,7 +922,7 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     _need(lse.shape == (T, hq) and lse.is_contiguous() and str(lse.dtype) == "torch.float32",
           "lse is contiguous float32 [tokens, q_heads]")
     if workspace is None:
-        workspace = torch.empty(kv8_attention_workspace(cache.num_heads, cache.head_dim),
+        workspace = torch.empty(kv8_attention_workspace(T, hq, cache.head_dim, weights is not None),
                                 dtype=torch.uint8, device=q.device)
         made.append(workspace)
     if stream is not None and made and q.is_cuda:

@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <string.h>
 
 #include "pkv_common.cuh"
 
@@ -45,6 +46,29 @@ __device__ __forceinline__ float scale_for(float amax) {
 __device__ __forceinline__ uint32_t requantise4(uint32_t c, float ratio) {
     const float2 a = floats_of(c & 0xffffu), b = floats_of(c >> 16);
     return e4m3x2(a.x * ratio, a.y * ratio) | (e4m3x2(b.x * ratio, b.y * ratio) << 16);
+}
+
+// Thread-block clusters: CTAs in this one, a barrier over them, a value of CTA `rank`.
+__device__ __forceinline__ int cluster_size() {
+    uint32_t n;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+    return static_cast<int>(n);
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive;" ::: "memory");
+    asm volatile("barrier.cluster.wait;" ::: "memory");
+}
+template <typename T>
+__device__ __forceinline__ T cluster_read(const T *at, uint32_t rank) {
+    static_assert(sizeof(T) == 4, "32-bit values");
+    uint32_t a, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(a)
+                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(at))), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    T r;
+    memcpy(&r, &v, 4);
+    return r;
 }
 
 inline bool kv8_head_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }

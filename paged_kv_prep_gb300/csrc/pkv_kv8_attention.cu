@@ -3,15 +3,24 @@
 //
 // weights[slot] += sum over the step's queries and heads of exp(x - lse): the
 // row's lse is known once the attention has run, so a token's weight is a sum
-// over rows that one CTA can own.  A CTA takes 64 tokens of a request; its
-// warps share out the KV heads, each recomputes K Q^T of its head for all rows
-// of the request, and the warps' sums meet in a fixed order.  No atomics unless
-// requests share a block: the addition to global memory itself is atomic, so
-// that shared blocks lose nothing.
+// over rows that one CTA can own.  No atomics unless requests share a block:
+// the addition to global memory itself is atomic, so that shared blocks lose
+// nothing.
+//
+// Layout.  A first kernel packs the rows (f16, scaled by a power of two, in the
+// order of the fragments) with their factors, so that rows of one KV head lie
+// behind one another.  A CTA owns kT token groups of 32 of a request and walks
+// the KV heads: a head's codes come by cp.async while the head before is worked
+// on, become f16 fragments in registers once, and meet the request's rows in
+// chunks of 64 that bulk copies bring two chunks ahead.  With kT = 8 (single tokens: few rows) a warp per group; with kT = 1
+// (chunks: many rows) the warps share a group's rows and a cluster shares the
+// KV heads, so that the tokens that thousands of rows see do not hold the
+// launch up; the sums meet in a fixed order.
 //
 // Bound: for single tokens HBM (D bytes of K per token and KV head, the second
-// read of K), for chunks the tensor pipe (mma.sync).
+// read of K), for chunks the tensor pipe (mma.sync) and the exponentials.
 #include "pkv_kv8_attention.cuh"
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 
@@ -24,157 +33,428 @@ namespace {
 
 constexpr int kPrefillRows = 32;
 
-constexpr int kWTokens = 64;
-constexpr int kWWarps = 8;
+constexpr int kWWarps = 8, kWThreads = 32 * kWWarps, kWStages = 3;
+template <int D>
+constexpr int kWRows = D <= 128 ? 64 : 32;                    // rows of a chunk
 
-__device__ __forceinline__ int64_t weight_units(const AttnParams &p, const Req &r) {
-    if (r.count <= 0) return 0;
-    const int lo = r.lo & ~(kWTokens - 1);
-    return r.keys > lo ? (r.keys - lo + kWTokens - 1) / kWTokens : 0;
+template <int D, int kT>
+struct WeightsShape {
+    static constexpr int kSubs = D <= 128 ? 2 : 1;            // 16-token fragments per warp
+    static constexpr int kGroup = 16 * kSubs, kTokens = kGroup * kT;
+    static constexpr int kTeams = kWWarps / kT;               // warps that share a group's rows
+};
+
+template <int D, int kT>
+struct WeightsSmem {
+    static constexpr int kTokens = WeightsShape<D, kT>::kTokens;
+    alignas(16) char k[kTokens * D];
+    alignas(16) char q[kWStages][kWRows<D> * D * 2];                         // packed rows
+    alignas(16) float2 fac[kWStages][kWRows<D> + 2];                            // factor of S, -lse (both for base 2)
+    uint64_t full[kWStages];
+    int32_t block[2][kTokens];                                // by unit parity; -1: not read
+    float ks[kTokens];
+    float sum[kWWarps][WeightsShape<D, kT>::kGroup];
+    float total[2][kTokens];                                  // by unit parity: this CTA's heads
+    int64_t prefix[kWThreads + 1];
+    int64_t warp_sum[kWWarps];
+};
+
+// Wait for a bulk copy; gives up after half a second or more.
+__device__ __forceinline__ bool wait_rows(uint64_t *bar, uint32_t parity) {
+    for (uint32_t k = 0; k < (1u << 22); k++)
+        if (mbar_try(bar, parity)) return true;
+    return false;
 }
 
+// Packed rows of a call: [KV head][token * G + head of the group], a row of D f16 values whose
+// 16-byte pieces stand as (step pair, lane t), the odd rows' with the halves of 128 bytes swapped (so
+// that two neighbouring rows fall into different banks); and their factors.
+struct Packed {
+    char *rows;
+    float2 *fac;
+};
+
+// A warp per token, D / 8 lanes per row.
 template <int D>
-__global__ void __launch_bounds__(32 * kWWarps) kv8_weights_kernel(const AttnParams p) {
-    constexpr int kThreads = 32 * kWWarps, S = D / 16, kSub = kWTokens / 16, kPieces = D / 64;
-    __shared__ int64_t s_prefix[kThreads + 1];
-    __shared__ int64_t s_warp[kWWarps];
-    __shared__ float s_sum[kWWarps][kWTokens];
-    __shared__ int32_t s_block[kWTokens];
+__global__ void __launch_bounds__(256) kv8_pack_kernel(const AttnParams p, const Packed out) {
+    constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, piece = lane % kPieces;
+    const bool fp16 = p.fp16 != 0;
+    const int hq = p.Hkv * p.G;
+    for (int64_t tok = (blockIdx.x * 256LL + threadIdx.x) >> 5; tok < p.T; tok += gridDim.x * 8LL) {
+        for (int h0 = 0; h0 < hq; h0 += kAtOnce) {
+            const int h = h0 + lane / kPieces;
+            uint4 y = make_uint4(0, 0, 0, 0);
+            float lse = -INFINITY;
+            if (h < hq) {
+                y = __ldg(reinterpret_cast<const uint4 *>(p.q + tok * p.q_stride + 2 * (static_cast<int64_t>(h) * D + 8 * piece)));
+                lse = p.lse[tok * hq + h];
+            }
+            const float2 a = widen2(y.x, fp16), b = widen2(y.y, fp16), c = widen2(y.z, fp16), d = widen2(y.w, fp16);
+            float m = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))),
+                            fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
+#pragma unroll
+            for (int o = kPieces / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+            const int e = row_exponent(m);
+            const float s = power2(14 - e);
+            if (h < hq) {
+                const int head = h / p.G;
+                const int64_t row = (static_cast<int64_t>(head) * p.T + tok) * p.G + h - head * p.G;
+                // dimensions 8 piece ..: fragment steps 4 u + i and the one after it, lane t
+                const int dim = 8 * piece, pair = (4 * (dim / 64) + (dim % 16) / 4) >> 1, t = (dim % 64) / 16;
+                const int at = (4 * pair + t) ^ (static_cast<int>(row & 1) << 2);
+                *reinterpret_cast<uint4 *>(out.rows + row * (2 * D) + 16 * at) =
+                    make_uint4(pack_f16(a.x * s, a.y * s), pack_f16(b.x * s, b.y * s), pack_f16(c.x * s, c.y * s),
+                               pack_f16(d.x * s, d.y * s));
+                if (piece == 0) out.fac[row] = make_float2(p.scale_log2 * power2(e - 14), -lse * kLog2e);
+            }
+        }
+    }
+}
+
+template <int D, int kT>
+__global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnParams p, const Packed packed) {
+    using Shape = WeightsShape<D, kT>;
+    constexpr int S = D / 16, kSubs = Shape::kSubs, kGroup = Shape::kGroup, kTokens = Shape::kTokens, kTeams = Shape::kTeams;
+    extern __shared__ __align__(16) char s_raw[];
+    auto &sm = *reinterpret_cast<WeightsSmem<D, kT> *>(s_raw);
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    auto units = [&](int i) { return weight_units(p, request_of(p, i)); };
-    const int64_t total = plan_prefix<kThreads>(s_prefix, s_warp, p.n, units);
+    const int group = warp % kT, team = warp / kT;
     const int64_t line = static_cast<int64_t>(p.Hkv) * D;
-    const bool fp16 = p.fp16 != 0;
-    for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
-        int64_t first;
-        const int i = plan_find<kThreads>(s_prefix, p.n, u, units, &first);
+    if (tid == 0) {
+        for (int k = 0; k < kWStages; k++) mbar_init(&sm.full[k], 1);
+        fence_mbar_init();
+    }
+    auto units = [&](int i) -> int64_t {
         const Req r = request_of(p, i);
-        const int32_t *table = p.tables + static_cast<int64_t>(i) * p.W;
-        const int s0 = (r.lo & ~(kWTokens - 1)) + static_cast<int>(u - first) * kWTokens;
-        if (tid < kWTokens) {
-            const int s = s0 + tid;
-            s_block[tid] = s >= r.lo && s < r.len ? block_of(p, table, s) : -1;
+        const int lo = r.lo & ~(kTokens - 1);
+        return r.count > 0 && r.keys > lo ? (r.keys - lo + kTokens - 1) / kTokens : 0;
+    };
+    const int64_t total = plan_prefix<kWThreads>(sm.prefix, sm.warp_sum, p.n, units);
+    const int64_t all = gridDim.x / cluster_size(), ranges = total < all ? total : all;
+    const int mates = cluster_size(), rank = blockIdx.x % mates, range = blockIdx.x / mates;
+    if (range >= ranges) return;
+    // Single tokens: a stretch of units each, all alike.  Chunks: every ranges-th unit, since the tokens
+    // at a chunk's front are seen by more rows than those at its end.
+    constexpr bool kStretch = kT > 1;
+    const int64_t step = kStretch ? 1 : ranges, end = kStretch ? (range + 1) * total / ranges : total;
+    int64_t u = kStretch ? range * total / ranges : range;
+
+    // One unit: a request, the tokens s0 .. s0 + kTokens - 1, and the rows f0 .. f1 - 1 that see one of them.
+    struct Unit {
+        Req r;
+        int i, s0, f0, f1;
+    };
+    struct Walk {
+        int64_t first;                                        // first unit of request `at`
+        int at;
+    };
+    Walk walk;
+    walk.at = plan_find<kWThreads>(sm.prefix, p.n, u, units, &walk.first);
+    auto unit_of = [&](Walk &w, int64_t v) {
+        Unit x;
+        for (;;) {
+            const int64_t k = units(w.at);
+            if (v < w.first + k) break;
+            w.first += k;
+            w.at++;
         }
-        __syncthreads();
-        // rows that see some token of the tile: query j sees s in (pos_j - window, pos_j], pos_j = len - count + j
-        const int back = r.len - r.count;
-        const int j0 = max(0, s0 - back);
-        const int64_t j1w = p.window > 0 ? static_cast<int64_t>(s0) + kWTokens - 1 + p.window - 1 - back : r.count - 1;
-        const int j1 = static_cast<int>(j1w < r.count - 1 ? j1w : r.count - 1);
-        const int f0 = j0 * p.G, f1 = (j1 + 1) * p.G;
-        float acc[kSub][2];
+        x.i = w.at;
+        x.r = request_of(p, w.at);
+        x.s0 = (x.r.lo & ~(kTokens - 1)) + static_cast<int>(v - w.first) * kTokens;
+        const int back = x.r.len - x.r.count;
+        // query j (at position back + j) sees token s if s <= back + j < s + window
+        const int j0 = max(0, x.s0 - back);
+        const int64_t j1 = p.window > 0 ? static_cast<int64_t>(x.s0) + kTokens - 1 + p.window - 1 - back : x.r.count - 1;
+        x.f0 = j0 * p.G;
+        x.f1 = (static_cast<int>(j1 < x.r.count - 1 ? j1 : x.r.count - 1) + 1) * p.G;
+        return x;
+    };
+    auto find_blocks = [&](const Unit &x, int parity) {
+        if (tid < kTokens) {
+            const int s = x.s0 + tid;
+            sm.block[parity][tid] = s >= x.r.lo && s < x.r.keys
+                                        ? block_of(p, p.tables + static_cast<int64_t>(x.i) * p.W, s) : -1;
+        }
+    };
+    // the codes and scales of one head
+    auto fetch = [&](const Unit &x, int parity, int head) {
+        constexpr int kRowLanes = D / 16, kStep = kWThreads / kRowLanes;
+        const int piece = tid % kRowLanes;
 #pragma unroll
-        for (int k = 0; k < kSub; k++) acc[k][0] = acc[k][1] = 0.f;
-        int64_t slot[kSub][2];
-        uint32_t live = 0;
-#pragma unroll
-        for (int k = 0; k < kSub; k++)
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int x = 16 * k + g + 8 * h, b = s_block[x];
-                slot[k][h] = b >= 0 ? static_cast<int64_t>(b) * p.bs + (s0 + x) % p.bs : 0;
-                live |= (b >= 0 ? 1u : 0u) << (2 * k + h);
+        for (int i = 0; i < (kTokens + kStep - 1) / kStep; i++) {
+            const int tok = i * kStep + tid / kRowLanes;
+            if (tok < kTokens) {
+                const int b = sm.block[parity][tok];
+                const int64_t slot = static_cast<int64_t>(b) * p.bs + (x.s0 + tok) % p.bs;
+                cp_async<16>(smem_addr(sm.k + tok * D + 16 * swizzle<D>(piece, tok)),
+                             p.kc + (b >= 0 ? slot * line + head * D + 16 * piece : 0), b >= 0);
             }
-        for (int head = warp; head < p.Hkv; head += kWWarps) {
-            float ks[kSub][2];
+        }
+        if (tid < kTokens) {
+            const int b = sm.block[parity][tid];
+            cp_async<4>(smem_addr(&sm.ks[tid]), p.ks + (b >= 0 ? static_cast<int64_t>(b) * p.Hkv + head : 0), b >= 0);
+        }
+        cp_commit();
+    };
+    // The rows' chunks in the order in which they are used; thread 0 asks for them two ahead.
+    struct Feed {
+        Walk walk;
+        int64_t u;
+        Unit x;
+        int head, f;
+        uint32_t count;
+    };
+    Feed feed = {};
+    auto ask_rows = [&]() {
+        if (feed.u >= end) return;
+        const int stage = feed.count % kWStages;
+        const int rows = min(kWRows<D>, feed.x.f1 - feed.f);
+        const int64_t row = (static_cast<int64_t>(feed.head) * p.T + feed.x.r.start) * p.G + feed.f;
+        // the factors' copy starts on an even row and the two sides' offsets agree
+        const int odd = static_cast<int>(row & 1);
+        const uint32_t facs = static_cast<uint32_t>((rows + odd + 1) & ~1) * 8;
+        mbar_arrive_expect_tx(&sm.full[stage], rows * 2 * D + facs);
+        bulk_g2s(sm.q[stage], packed.rows + row * (2 * D), rows * 2 * D, &sm.full[stage]);
+        bulk_g2s(sm.fac[stage], packed.fac + row - odd, facs, &sm.full[stage]);
+        feed.count++;
+        feed.f += kWRows<D>;
+        if (feed.f >= feed.x.f1) {
+            feed.head += mates;
+            if (feed.head >= p.Hkv) {
+                feed.head = rank;
+                feed.u += step;
+                if (feed.u < end) feed.x = unit_of(feed.walk, feed.u);
+            }
+            feed.f = feed.x.f0;
+        }
+    };
+
+    feed.walk = walk;
+    feed.u = u;
+    Unit x = unit_of(walk, u);
+    feed.x = x;
+    feed.head = rank;
+    feed.f = x.f0;
+    feed.count = 0;
+    if (rank >= p.Hkv) feed.u = end;
+    int parity = 0;
+    uint32_t chunk = 0;
+    find_blocks(x, parity);
+    __syncthreads();
+    if (rank < p.Hkv) fetch(x, parity, rank);
+    if (tid == 0) {
+        ask_rows();
+        ask_rows();
+    }
+    while (true) {
+        const bool more = u + step < end;
+        Unit y = x;
+        if (more) {
+            y = unit_of(walk, u + step);
+            find_blocks(y, parity ^ 1);
+        }
+        float acc[kSubs][2];
 #pragma unroll
-            for (int k = 0; k < kSub; k++)
+        for (int k = 0; k < kSubs; k++) acc[k][0] = acc[k][1] = 0.f;
+        for (int head = rank; head < p.Hkv; head += mates) {
+            cp_wait<0>();
+            __syncthreads();
+            uint32_t kf[kSubs][S][4];
+            float ks[kSubs][2];
 #pragma unroll
-                for (int h = 0; h < 2; h++)
-                    ks[k][h] = (live >> (2 * k + h)) & 1
-                                   ? p.ks[static_cast<int64_t>(s_block[16 * k + g + 8 * h]) * p.Hkv + head] : 0.f;
-            const uint8_t *kh = p.kc + head * D + 16 * t;
-            for (int f8 = f0; f8 < f1; f8 += 8) {
-                uint32_t qb[S][2];
-                const int f = f8 + g, j = f / p.G;
-                const char *row = p.q + static_cast<int64_t>(r.start + j) * p.q_stride +
-                                  2 * static_cast<int64_t>(head * p.G + f - j * p.G) * D;
-                const int e = load_query<D>(qb, row, f < f1, t, fp16);
-                float cf[2], lse[2];
-                int pos[2];
+            for (int k = 0; k < kSubs; k++)
 #pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    const int fc = f8 + 2 * t + c, jc = fc / p.G;
-                    cf[c] = p.scale_log2 * power2(__shfl_sync(~0u, e, (2 * t + c) * 4) - 14);
-                    pos[c] = fc < f1 ? back + jc : -1;
-                    lse[c] = fc < f1 ? p.lse[static_cast<int64_t>(r.start + jc) * p.Hkv * p.G + head * p.G + fc - jc * p.G] * kLog2e
-                                     : 0.f;
-                    if (lse[c] == -INFINITY) pos[c] = -1;      // an empty row gives no weight
-                }
+                for (int h = 0; h < 2; h++) {
+                    const int tok = group * kGroup + 16 * k + g + 8 * h;
+                    ks[k][h] = sm.ks[tok];
 #pragma unroll
-                for (int k = 0; k < kSub; k++) {
-                    float x[4] = {0.f, 0.f, 0.f, 0.f};
+                    for (int c = 0; c < D / 64; c++) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(sm.k + tok * D + 16 * swizzle<D>(4 * c + t, tok));
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int c = 0; c < kPieces; c++) {
-                        uint4 ka = make_uint4(0, 0, 0, 0), kb = ka;
-                        if ((live >> (2 * k)) & 1) ka = __ldg(reinterpret_cast<const uint4 *>(kh + slot[k][0] * line + 64 * c));
-                        if ((live >> (2 * k + 1)) & 1) kb = __ldg(reinterpret_cast<const uint4 *>(kh + slot[k][1] * line + 64 * c));
-                        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-                        for (int q = 0; q < 4; q++) {
-                            const uint32_t a[4] = {f16x2_of(wa[q]), f16x2_of(wb[q]), f16x2_of(wa[q] >> 16), f16x2_of(wb[q] >> 16)};
-                            mma_f16(x, a, qb[4 * c + q][0], qb[4 * c + q][1]);
+                        for (int i = 0; i < 4; i++) {
+                            kf[k][4 * c + i][h] = f16x2_of(w[i]);
+                            kf[k][4 * c + i][2 + h] = f16x2_of(w[i] >> 16);
                         }
                     }
+                }
+            __syncthreads();
+            const bool last = head + mates >= p.Hkv;
+            if (!last) fetch(x, parity, head + mates);
+            else if (more) fetch(y, parity ^ 1, rank);
+            const int back = x.r.len - x.r.count;
+            const int64_t row0 = (static_cast<int64_t>(head) * p.T + x.r.start) * p.G;
+            for (int f = x.f0; f < x.f1; f += kWRows<D>, chunk++) {
+                if (f != x.f0) __syncthreads();               // everyone has left the stage that is filled next
+                if (tid == 0) ask_rows();
+                const int stage = chunk % kWStages;
+                if (!wait_rows(&sm.full[stage], (chunk / kWStages) & 1) && p.err) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
+                const int odd = static_cast<int>((row0 + f) & 1);
+#pragma unroll 1
+                for (int nt = team; nt < kWRows<D> / 8; nt += kTeams) {
+                    if (f + 8 * nt >= x.f1) break;
+                    float c[kSubs][4];
 #pragma unroll
-                    for (int c = 0; c < 4; c++) {
-                        const int h = c >> 1, col = c & 1, s = s0 + 16 * k + g + 8 * h;
-                        const bool ok = ((live >> (2 * k + h)) & 1) && s <= pos[col] &&
-                                        (p.window <= 0 || s > pos[col] - p.window);
-                        if (ok) acc[k][h] += exp2_fast(fmaf(x[c], cf[col] * ks[k][h], -lse[col]));
+                    for (int k = 0; k < kSubs; k++) c[k][0] = c[k][1] = c[k][2] = c[k][3] = 0.f;
+                    const char *row = sm.q[stage] + (8 * nt + g) * (2 * D);
+                    const int flip = ((g + odd) & 1) << 2;
+#pragma unroll
+                    for (int j = 0; j < S; j += 2) {
+                        const uint4 b = *reinterpret_cast<const uint4 *>(row + 16 * ((2 * j + t) ^ flip));
+#pragma unroll
+                        for (int k = 0; k < kSubs; k++) {
+                            mma_f16(c[k], kf[k][j], b.x, b.y);
+                            mma_f16(c[k], kf[k][j + 1], b.z, b.w);
+                        }
                     }
+                    const float2 fa = sm.fac[stage][odd + 8 * nt + 2 * t], fb = sm.fac[stage][odd + 8 * nt + 2 * t + 1];
+                    // rows first .. first + 7 see every token of the tile (tokens that are not read do not
+                    // count: their sums are dropped)
+                    const int first = f + 8 * nt;
+                    const int p0 = back + first / p.G, p1 = back + (first + 7) / p.G;
+                    const bool whole = first + 8 <= x.f1 && x.s0 + kTokens - 1 <= p0 && (p.window <= 0 || x.s0 > p1 - p.window);
+                    float v[kSubs][4];
+#pragma unroll
+                    for (int k = 0; k < kSubs; k++)
+#pragma unroll
+                        for (int q = 0; q < 4; q++)
+                            v[k][q] = exp2_fast(fmaf(c[k][q], (q & 1 ? fb.x : fa.x) * ks[k][q >> 1], q & 1 ? fb.y : fa.y));
+                    if (!whole) {
+                        const int r0 = first + 2 * t;
+                        const int pa = r0 < x.f1 ? back + r0 / p.G : -1, pb = r0 + 1 < x.f1 ? back + (r0 + 1) / p.G : -1;
+#pragma unroll
+                        for (int k = 0; k < kSubs; k++)
+#pragma unroll
+                            for (int q = 0; q < 4; q++) {
+                                const int pos = q & 1 ? pb : pa, s = x.s0 + group * kGroup + 16 * k + g + 8 * (q >> 1);
+                                // an empty row (-lse = inf) gives no weight
+                                const bool ok = s <= pos && s >= lo_of(p, pos) && (q & 1 ? fb.y : fa.y) != INFINITY;
+                                if (!ok) v[k][q] = 0.f;
+                            }
+                    }
+#pragma unroll
+                    for (int k = 0; k < kSubs; k++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++) acc[k][h] += v[k][2 * h] + v[k][2 * h + 1];
                 }
             }
         }
 #pragma unroll
-        for (int k = 0; k < kSub; k++)
+        for (int k = 0; k < kSubs; k++)
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 float a = acc[k][h];
                 a += __shfl_xor_sync(~0u, a, 1);
                 a += __shfl_xor_sync(~0u, a, 2);
-                if (t == 0) s_sum[warp][16 * k + g + 8 * h] = a;
+                if (t == 0) sm.sum[warp][16 * k + g + 8 * h] = a;
             }
         __syncthreads();
-        if (tid < kWTokens && s_block[tid] >= 0) {
+        if (tid < kTokens) {
             float a = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWWarps; w++) a += s_sum[w][tid];
-            atomicAdd(p.weights + static_cast<int64_t>(s_block[tid]) * p.bs + (s0 + tid) % p.bs, a);
+            for (int w = 0; w < kTeams; w++) a += sm.sum[w * kT + tid / kGroup][tid % kGroup];
+            sm.total[parity][tid] = a;
         }
+        cluster_sync();
+        if (rank == 0 && tid < kTokens && sm.block[parity][tid] >= 0) {
+            float a = sm.total[parity][tid];
+            for (int c = 1; c < mates; c++) a += cluster_read(&sm.total[parity][tid], c);
+            atomicAdd(p.weights + static_cast<int64_t>(sm.block[parity][tid]) * p.bs + (x.s0 + tid) % p.bs, a);
+        }
+        if (!more) break;
         __syncthreads();
+        x = y;
+        u += step;
+        parity ^= 1;
     }
+    cp_wait<0>();
+    cluster_sync();                                           // nobody leaves while its totals are read
 }
 
 int64_t workspace_of(int32_t head_dim, int sms) {
     const int64_t a = kv8_decode_workspace(head_dim, sms), b = kv8_prefill_workspace(head_dim, sms);
-    return a > b ? a : b;
+    return ((a > b ? a : b) + 255) & ~255LL;
 }
 
-int launch_weights(const AttnParams &p, int32_t head_dim, int sms, cudaStream_t s) {
-    const dim3 grid(2 * sms), block(32 * kWWarps);
-    if (head_dim == 64)
-        PKV_CUDA_TRY(launch_pdl(kv8_weights_kernel<64>, grid, block, 0, s, p));
-    else if (head_dim == 128)
-        PKV_CUDA_TRY(launch_pdl(kv8_weights_kernel<128>, grid, block, 0, s, p));
-    else
-        PKV_CUDA_TRY(launch_pdl(kv8_weights_kernel<256>, grid, block, 0, s, p));
+template <int D, int kT>
+int launch_weights_as(const AttnParams &p, const Packed &packed, int mates, int sms, cudaStream_t s) {
+    constexpr int smem = static_cast<int>(sizeof(WeightsSmem<D, kT>));
+    static_assert(smem <= 110 * 1024, "two CTAs an SM");
+    PKV_CUDA_TRY(cudaFuncSetAttribute(kv8_weights_kernel<D, kT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * sms / mates * mates));
+    cfg.blockDim = dim3(kWThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(mates);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    // Clusters that become resident while the packing still runs end up unevenly placed: three chunks'
+    // weights took 702 us with the early start and 500 us without it.
+    cfg.attrs = mates == 1 ? attr : attr + 1;
+    cfg.numAttrs = mates == 1 ? 2 : 1;
+    // Every cluster takes one stretch of the units, so no more of them are started than run at once
+    // (the SMs of a GPC are not a multiple of eight); asked for once per device and cluster size.
+    static int known[64][4] = {{0}};
+    int dev = 0;
+    PKV_CUDA_TRY(cudaGetDevice(&dev));
+    const int log = mates == 1 ? 0 : mates == 2 ? 1 : mates == 4 ? 2 : 3;
+    int clusters = dev < 64 ? known[dev][log] : 0;
+    if (!clusters) {
+        cudaLaunchConfig_t alone = cfg;
+        alone.attrs = attr + 1;
+        alone.numAttrs = 1;
+        PKV_CUDA_TRY(cudaOccupancyMaxActiveClusters(&clusters, kv8_weights_kernel<D, kT>, &alone));
+        if (clusters < 1) clusters = 1;
+        if (dev < 64) known[dev][log] = clusters;
+    }
+    if (clusters * mates < 2 * sms) cfg.gridDim = dim3(static_cast<unsigned>(clusters * mates));
+    PKV_CUDA_TRY(launch_pdl(kv8_pack_kernel<D>, dim3(static_cast<unsigned>(p.T < 64 * sms ? (p.T + 7) / 8 : 8 * sms)), dim3(256), 0, s, p, packed));
+    PKV_CUDA_TRY(cudaLaunchKernelEx(&cfg, kv8_weights_kernel<D, kT>, p, packed));
     return PKV_OK;
 }
+
+int launch_weights(const AttnParams &p, char *workspace, int32_t head_dim, int sms, cudaStream_t s) {
+    Packed packed;
+    packed.rows = workspace;
+    packed.fac = reinterpret_cast<float2 *>(workspace + 2LL * p.T * p.Hkv * p.G * head_dim);
+    // a step of single tokens has few rows a request: the warps share out its tokens
+    const bool single = p.T <= p.n;
+    const int mates = single || p.Hkv < 2 ? 1 : p.Hkv < 4 ? 2 : p.Hkv < 8 ? 4 : 8;
+    if (head_dim == 64)
+        return single ? launch_weights_as<64, 8>(p, packed, mates, sms, s) : launch_weights_as<64, 1>(p, packed, mates, sms, s);
+    if (head_dim == 128)
+        return single ? launch_weights_as<128, 8>(p, packed, mates, sms, s) : launch_weights_as<128, 1>(p, packed, mates, sms, s);
+    return single ? launch_weights_as<256, 8>(p, packed, mates, sms, s) : launch_weights_as<256, 1>(p, packed, mates, sms, s);
+}
+
+// Bytes of the packed rows and their factors (a pair of factors may be read past the last row).
+int64_t packed_bytes(int64_t rows, int32_t head_dim) { return rows * (2LL * head_dim + 8) + 16; }
 
 }  // namespace
 }  // namespace pkv
 
 extern "C" {
 
-int pkv_kv8_attention_workspace(int32_t num_heads, int32_t head_dim, int64_t *bytes) {
-    if (!bytes || num_heads < 1 || num_heads > 1024 || !pkv::kv8_head_dim(head_dim)) return PKV_ERR_INVALID_ARG;
+int pkv_kv8_attention_workspace(int32_t num_tokens, int32_t num_q_heads, int32_t head_dim, int32_t with_weights,
+                                int64_t *bytes) {
+    if (!bytes || num_tokens < 0 || num_tokens >= PKV_MAX_TOKENS || num_q_heads < 1 || num_q_heads > (1 << 20) ||
+        !pkv::kv8_head_dim(head_dim))
+        return PKV_ERR_INVALID_ARG;
     int sms = 0;
     const int rc = pkv::kv8_sm_count(&sms);
     if (rc != PKV_OK) return rc;
     *bytes = pkv::workspace_of(head_dim, sms);
+    if (with_weights) *bytes += pkv::packed_bytes(static_cast<int64_t>(num_tokens) * num_q_heads, head_dim);
     return PKV_OK;
 }
 
@@ -206,7 +486,9 @@ int pkv_kv8_attention(const pkv_kv8_cache *cache, const void *q, int64_t q_strid
     int sms = 0;
     rc = pkv::kv8_sm_count(&sms);
     if (rc != PKV_OK) return rc;
-    if (workspace_bytes < pkv::workspace_of(cache->head_dim, sms)) return PKV_ERR_INVALID_ARG;
+    const int64_t own = pkv::workspace_of(cache->head_dim, sms);
+    if (workspace_bytes < own + (weights ? pkv::packed_bytes(static_cast<int64_t>(num_tokens) * num_q_heads, cache->head_dim) : 0))
+        return PKV_ERR_INVALID_ARG;
     pkv::AttnParams p = {};
     p.q = static_cast<const char *>(q);
     p.q_stride = q_stride_bytes;
@@ -250,7 +532,7 @@ int pkv_kv8_attention(const pkv_kv8_cache *cache, const void *q, int64_t q_strid
     }
     rc = pkv::kv8_launch_decode(p, cache->head_dim, one_tile, sms, s);
     if (rc != PKV_OK || !weights) return rc;
-    return pkv::launch_weights(p, cache->head_dim, sms, s);
+    return pkv::launch_weights(p, static_cast<char *>(workspace) + own, cache->head_dim, sms, s);
 }
 
 }  // extern "C"

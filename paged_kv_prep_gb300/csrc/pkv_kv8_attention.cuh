@@ -214,6 +214,15 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Rows of codes in shared memory: a row's 16-byte pieces are permuted by f(token) = (token & 6) ^
+// ((token & 1) << 2) (pairs of 64-byte rows: by token >> 1), which makes the fragment reads free of
+// bank conflicts: K rows g and g + 1 fall into different halves of the banks, V tokens 2t into
+// different quarters.
+template <int D>
+__device__ __forceinline__ int swizzle(int piece, int token) {
+    return D == 64 ? piece ^ ((token >> 1) & 3) : piece ^ (token & 6) ^ ((token & 1) << 2);
+}
+
 // Loads one (query, head) row's f16 fragments of a query tile: element pairs of this lane's
 // dimensions 64 u + 16 t + 4 i .. + 3 in qb[4 u + i], scaled by 2^(14 - E); returns E.
 template <int D>

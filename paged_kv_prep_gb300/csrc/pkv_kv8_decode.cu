@@ -29,10 +29,7 @@ constexpr int kUnit = 32;          // tokens per unit, two groups of 16
 constexpr int kDepth = 1;           // units whose codes are held or on their way; two measured no faster
 constexpr float kSlack = 14.f;     // growth of a row's maximum (log2) that R does not follow
 
-// A unit's codes, a row of D bytes per token, and its scales.  A row's 16-byte pieces are permuted
-// by f(token) = (token & 6) ^ ((token & 1) << 2) (pairs of 64-byte rows: by token >> 1), which makes
-// the fragment reads below free of bank conflicts: K rows g and g + 1 fall into different halves of
-// the banks, V tokens 2t into different quarters.
+// A unit's codes, a row of D bytes per token (pieces permuted by swizzle()), and its scales.
 template <int D>
 struct Stage {
     static constexpr int kKPieces = D / 64;                   // 16-byte pieces per lane and token row
@@ -42,9 +39,6 @@ struct Stage {
     static constexpr int kRows = 32 / kRowLanes;              // rows of one copy instruction
     char k[kUnit * D], v[kUnit * D];
     float ks[kUnit], vs[kUnit];                               // by token, or by group
-    __device__ static __forceinline__ int swizzle(int piece, int token) {
-        return D == 64 ? piece ^ ((token >> 1) & 3) : piece ^ (token & 6) ^ ((token & 1) << 2);
-    }
 };
 
 template <int D, int NT>
@@ -151,7 +145,7 @@ struct Tile {
 #pragma unroll
                 for (int i = 0; i < kUnit; i += St::kRows) {
                     const int r = i + crow;
-                    cp_async_full<16>(smem_addr(to + r * D + 16 * St::swizzle(cpiece, r)), from + y.at[i >> 4] + (i & 15) * line);
+                    cp_async_full<16>(smem_addr(to + r * D + 16 * swizzle<D>(cpiece, r)), from + y.at[i >> 4] + (i & 15) * line);
                 }
             } else {
 #pragma unroll
@@ -160,7 +154,7 @@ struct Tile {
                     const bool on = (y.mask >> r) & 1;
                     const int64_t x = kGrouped ? y.at[i >> 4] + (i & 15) * line
                                                : static_cast<int64_t>(__shfl_sync(~0u, y.slot, r)) * line;
-                    cp_async<16>(smem_addr(to + r * D + 16 * St::swizzle(cpiece, r)), from + (on ? x : 0), on);
+                    cp_async<16>(smem_addr(to + r * D + 16 * swizzle<D>(cpiece, r)), from + (on ? x : 0), on);
                 }
             }
         };
@@ -223,7 +217,7 @@ struct Tile {
                 uint4 ka[2], kb[2];
 #pragma unroll
                 for (int q = 0; q < 2; q++) {
-                    const char *row = st.k + (16 * q + g) * D + 16 * St::swizzle(4 * c + t, g);
+                    const char *row = st.k + (16 * q + g) * D + 16 * swizzle<D>(4 * c + t, g);
                     ka[q] = *reinterpret_cast<const uint4 *>(row);
                     kb[q] = *reinterpret_cast<const uint4 *>(row + 8 * D);
                 }
@@ -332,13 +326,13 @@ struct Tile {
                     for (int h = 0; h < 4; h++) {
                         const int r = 16 * q + 2 * t + (h & 1) + 8 * (h >> 1);
                         if constexpr (St::kVBytes == 16) {
-                            const uint4 y = *reinterpret_cast<const uint4 *>(st.v + r * D + 16 * St::swizzle(8 * c + g, r));
+                            const uint4 y = *reinterpret_cast<const uint4 *>(st.v + r * D + 16 * swizzle<D>(8 * c + g, r));
                             w[h][0] = y.x;
                             w[h][1] = y.y;
                             w[h][2] = y.z;
                             w[h][3] = y.w;
                         } else {
-                            const uint2 y = *reinterpret_cast<const uint2 *>(st.v + r * D + 16 * St::swizzle(g >> 1, r) + 8 * (g & 1));
+                            const uint2 y = *reinterpret_cast<const uint2 *>(st.v + r * D + 16 * swizzle<D>(g >> 1, r) + 8 * (g & 1));
                             w[h][0] = y.x;
                             w[h][1] = y.y;
                         }
@@ -571,29 +565,34 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
             fac = m == -INFINITY ? (l == 0.f ? 0.f : NAN) : exp2_fast(m - top);
             sum += fac * l;
         }
-        // sixteen rows on their way at a time
+        // many pieces: sixteen rows on their way at a time; few: four
         const int n = min(32, pieces - k0);
-        for (int k1 = 0; k1 < n; k1 += 16) {
-            float y[16][kPer];
+        auto add = [&](auto batch) {
+            constexpr int kBatch = decltype(batch)::value;
+            for (int k1 = 0; k1 < n; k1 += kBatch) {
+                float y[kBatch][kPer];
 #pragma unroll
-            for (int k = 0; k < 16; k++) {
-                const float *o = part(k0 + min(k1 + k, n - 1)) + 2 * rows + row * D + lane * kPer;
+                for (int k = 0; k < kBatch; k++) {
+                    const float *o = part(k0 + min(k1 + k, n - 1)) + 2 * rows + row * D + lane * kPer;
 #pragma unroll
-                for (int c = 0; c < kPer; c += 2) {
-                    const float2 z = *reinterpret_cast<const float2 *>(o + c);
-                    y[k][c] = z.x;
-                    y[k][c + 1] = z.y;
+                    for (int c = 0; c < kPer; c += 2) {
+                        const float2 z = *reinterpret_cast<const float2 *>(o + c);
+                        y[k][c] = z.x;
+                        y[k][c + 1] = z.y;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; k++) {
+                    const float f2 = __shfl_sync(~0u, fac, k1 + k);
+                    if (k1 + k < n && f2 != 0.f) {
+#pragma unroll
+                        for (int c = 0; c < kPer; c++) acc[c] = fmaf(f2, y[k][c], acc[c]);
+                    }
                 }
             }
-#pragma unroll
-            for (int k = 0; k < 16; k++) {
-                const float f2 = __shfl_sync(~0u, fac, k1 + k);
-                if (k1 + k < n && f2 != 0.f) {
-#pragma unroll
-                    for (int c = 0; c < kPer; c++) acc[c] = fmaf(f2, y[k][c], acc[c]);
-                }
-            }
-        }
+        };
+        if (n > 8) add(std::integral_constant<int, 16>());
+        else add(std::integral_constant<int, 4>());
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);

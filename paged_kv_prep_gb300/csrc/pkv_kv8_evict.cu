@@ -51,23 +51,12 @@ __device__ __forceinline__ uint32_t key_of(float w) {
     return (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// Distributed shared memory: a value of CTA `rank` of this cluster.
-template <typename T>
-__device__ __forceinline__ T of_rank(const T *at, uint32_t rank) {
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(pkv::smem_addr(at)), "r"(rank));
-    uint32_t v;
-    static_assert(sizeof(T) == 4, "32-bit values");
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    return static_cast<T>(v);
-}
 template <int kCluster>
 __device__ __forceinline__ void sync_all() {
     if constexpr (kCluster == 1) {
         __syncthreads();
     } else {
-        asm volatile("barrier.cluster.arrive;" ::: "memory");
-        asm volatile("barrier.cluster.wait;" ::: "memory");
+        pkv::cluster_sync();
     }
 }
 
@@ -108,7 +97,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
     sync_all<kCluster>();
     bad = 0;
 #pragma unroll
-    for (int c = 0; c < kCluster; c++) bad |= of_rank(&s_bad, c);
+    for (int c = 0; c < kCluster; c++) bad |= pkv::cluster_read(&s_bad, c);
     if (bad) {
         if (all == 0) {
             p.new_lens[req] = -1;
@@ -167,8 +156,8 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
         if (d0 > 0) {
 #pragma unroll
             for (int c = 0; c < kCluster; c++) {
-                c0 += of_rank(&hist[d0], c);
-                c1 += of_rank(&hist[d0 - 1], c);
+                c0 += pkv::cluster_read(&hist[d0], c);
+                c1 += pkv::cluster_read(&hist[d0 - 1], c);
             }
         }
         uint32_t incl = c0 + c1;
@@ -229,8 +218,8 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
 #pragma unroll
     for (int c = 0; c + 1 < kCluster; c++)
         if (c < rank) {
-            g += of_rank(&s_gt[kWarps], c);
-            e += of_rank(&s_eq[kWarps], c);
+            g += pkv::cluster_read(&s_gt[kWarps], c);
+            e += pkv::cluster_read(&s_eq[kWarps], c);
         }
     const uint32_t below = (1u << lane) - 1;
     for (int i0 = 0; i0 < mine; i0 += 32) {

@@ -235,7 +235,7 @@ def test_strided_rows_and_given_buffers():
     wide = torch.full((a[0].shape[0], 8 * 128 + 64), 5.0, dtype=torch.bfloat16, device="cuda")
     out = wide[:, :8 * 128].unflatten(1, (8, 128))
     lse = torch.empty(a[0].shape[0], 8, device="cuda")
-    ws = torch.full((pkv.kv8_attention_workspace(2, 128),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((pkv.kv8_attention_workspace(a[0].shape[0], 8, 128),), 255, dtype=torch.uint8, device="cuda")
     want = case.reference(case.d ** -0.5, 0)
     for _ in range(2):
         pkv.kv8_attention(*a, out=out, lse=lse, workspace=ws)
