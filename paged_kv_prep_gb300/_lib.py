@@ -808,7 +808,16 @@ class PrefixCache:
 
 # -- the cache held in 8 bits -------------------------------------------------
 
-_KV8_DTYPES = {"torch.bfloat16": 0, "torch.float16": 1}
+_KV8 = None          # torch's types by what they are here (set on first use: torch loads late)
+
+
+def _kv8_types():
+    global _KV8
+    if _KV8 is None:
+        import torch
+
+        _KV8 = (torch, {torch.bfloat16: 0, torch.float16: 1}, torch.float32, torch.int32, torch.int64)
+    return _KV8
 
 
 def _need(ok, what):
@@ -819,42 +828,62 @@ def _need(ok, what):
 def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
     """The C view of an 8-bit cache: lines [num_slots, heads * head_dim] of one byte per element
     and scales [num_blocks, heads]."""
-    _need(k_scale.dim() == 2 and k_scale.shape == v_scale.shape and k_cache.shape == v_cache.shape,
-          "k_cache and v_cache, k_scale and v_scale have the same shapes; scales are [num_blocks, heads]")
-    blocks, heads = k_scale.shape
-    _need(blocks > 0 and heads > 0 and k_cache.dim() >= 1 and k_cache.shape[0] % blocks == 0
-          and k_cache.numel() % max(k_cache.shape[0] * heads, 1) == 0 and k_cache.shape[0] > 0,
-          "the caches hold num_blocks * block_size lines of heads * head_dim bytes")
-    for t in (k_cache, v_cache):
-        _need(t.element_size() == 1 and t.is_contiguous(), "the caches are contiguous, one byte an element")
-    for t in (k_scale, v_scale):
-        _need(str(t.dtype) == "torch.float32" and t.is_contiguous(), "the scales are contiguous float32")
-    slots = k_cache.shape[0]
+    f32 = _kv8_types()[2]
+    shape, scales = k_cache.shape, k_scale.shape
+    if not (len(scales) == 2 and v_scale.shape == scales and v_cache.shape == shape and len(shape) >= 1):
+        raise ValueError("k_cache and v_cache, k_scale and v_scale have the same shapes; scales are [num_blocks, heads]")
+    blocks, heads = scales
+    slots, size = shape[0], k_cache.numel()
+    if not (blocks > 0 and heads > 0 and slots > 0 and slots % blocks == 0 and size % (slots * heads) == 0):
+        raise ValueError("the caches hold num_blocks * block_size lines of heads * head_dim bytes")
+    if not (k_cache.itemsize == 1 and v_cache.itemsize == 1 and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("the caches are contiguous, one byte an element")
+    if not (k_scale.dtype is f32 and v_scale.dtype is f32 and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        raise ValueError("the scales are contiguous float32")
     return Kv8CacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                        blocks, slots // blocks, heads, k_cache.numel() // (slots * heads))
+                        blocks, slots // blocks, heads, size // (slots * heads))
 
 
 def _kv8_int32(*tensors):
+    i32 = _kv8_types()[3]
     for t in tensors:
-        _need(str(t.dtype) == "torch.int32" and t.is_contiguous(), "tables, lengths and locations are contiguous int32")
+        if not (t.dtype is i32 and t.is_contiguous()):
+            raise ValueError("tables, lengths and locations are contiguous int32")
 
 
 def _kv8_rows(x, width, what):
-    """Bytes between the tokens of x: [tokens, width] or [tokens, heads, head_dim], each token's
-    elements contiguous."""
+    """Bytes between the tokens of x (two-byte elements): [tokens, width] or [tokens, heads,
+    head_dim], each token's elements contiguous."""
+    shape, stride = x.shape, x.stride()
     inner = 1
-    for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
-        _need(size == 1 or stride == inner, f"{what}: a token's elements are contiguous")
-        inner *= size
-    _need(x.dim() >= 2 and inner == width, f"{what}: [tokens, heads, head_dim] of the cache's sizes")
-    return x.stride(0) * x.element_size() if x.shape[0] > 1 else width * x.element_size()
+    for i in range(len(shape) - 1, 0, -1):
+        if stride[i] != inner and shape[i] != 1:
+            raise ValueError(f"{what}: a token's elements are contiguous")
+        inner *= shape[i]
+    if len(shape) < 2 or inner != width:
+        raise ValueError(f"{what}: [tokens, heads, head_dim] of the cache's sizes")
+    return stride[0] * 2 if shape[0] > 1 else width * 2
 
 
-def _kv8_dtype(*tensors):
-    kind = _KV8_DTYPES.get(str(tensors[0].dtype))
-    _need(kind is not None and all(t.dtype == tensors[0].dtype for t in tensors),
-          "bfloat16 or float16, the same for all")
+def _kv8_dtype(x):
+    kind = _kv8_types()[1].get(x.dtype)
+    if kind is None:
+        raise ValueError("bfloat16 or float16")
     return kind
+
+
+def _kv8_weights(weights, slots):
+    if not (weights.dtype is _kv8_types()[2] and weights.is_contiguous() and weights.numel() == slots):
+        raise ValueError("weights is contiguous float32, one for each slot")
+
+
+def _kv8_made(made, stream, handle):
+    """Tensors made for a call were allocated on the current stream; the work runs on another."""
+    made = [t for t in made if t.is_cuda]
+    if made:
+        other = _kv8_types()[0].cuda.ExternalStream(handle) if isinstance(stream, int) else stream
+        for t in made:
+            t.record_stream(other)
 
 
 def kv8_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, d_error=None, stream=None,
@@ -866,23 +895,26 @@ def kv8_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, d_error=No
     head_dim]; k_scale, v_scale: float32 [num_blocks, heads]; slot_mapping: int64."""
     cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     T = slot_mapping.numel()
-    _need(str(slot_mapping.dtype) == "torch.int64" and slot_mapping.is_contiguous(), "slot_mapping is contiguous int64")
-    _need(k.shape == v.shape and k.shape[0] >= T, "k and v have the same shape, a row for each slot")
+    if not (slot_mapping.dtype is _kv8_types()[4] and slot_mapping.is_contiguous()):
+        raise ValueError("slot_mapping is contiguous int64")
+    if not (k.dtype is v.dtype and k.shape == v.shape and k.shape[0] >= T):
+        raise ValueError("k and v have the same shape and type, a row for each slot")
     width = cache.num_heads * cache.head_dim
-    rc = lib().pkv_kv8_store(C.byref(cache), _ptr(k), _ptr(v), _kv8_rows(k, width, "k"),
-                             _kv8_rows(v, width, "v"), _kv8_dtype(k, v), _ptr(slot_mapping), T,
-                             C.c_void_p(d_error) if d_error else None, _stream(stream))
-    if check:
-        _check(rc, "pkv_kv8_store")
+    rc = lib().pkv_kv8_store(C.byref(cache), k.data_ptr(), v.data_ptr(), _kv8_rows(k, width, "k"),
+                             _kv8_rows(v, width, "v"), _kv8_dtype(k), slot_mapping.data_ptr(), T,
+                             d_error or None, _stream(stream))
+    if check and rc != OK:
+        raise PkvError(rc, "pkv_kv8_store")
     return rc
 
 
 def kv8_attention_workspace(num_tokens, num_q_heads, head_dim, with_weights=False):
     """Bytes of device workspace an attention call takes (``pkv_kv8_attention_workspace``)."""
     n = C.c_int64(0)
-    _check(lib().pkv_kv8_attention_workspace(int(num_tokens), int(num_q_heads), int(head_dim),
-                                             int(bool(with_weights)), C.byref(n)),
-           "pkv_kv8_attention_workspace")
+    rc = lib().pkv_kv8_attention_workspace(int(num_tokens), int(num_q_heads), int(head_dim),
+                                           int(bool(with_weights)), C.byref(n))
+    if rc != OK:
+        raise PkvError(rc, "pkv_kv8_attention_workspace")
     return n.value
 
 
@@ -896,51 +928,50 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     that many positions, its own among them (0: all).  weights: float32 [num_slots], each token's
     softmax weight is added to it.  out, lse, workspace (uint8, kv8_attention_workspace bytes) are
     allocated when not given.  Returns (out, lse); lse is float32 [tokens, q_heads]."""
-    import torch
-
+    torch, _, f32, _, _ = _kv8_types()
     cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     _kv8_int32(block_tables, query_start_loc, seq_lens)
-    n = seq_lens.numel()
-    _need(block_tables.dim() == 2 and block_tables.shape[0] >= n and query_start_loc.numel() >= n + 1,
-          "block_tables [n, W], query_start_loc [n + 1], seq_lens [n]")
-    _need(q.dim() == 3 and q.shape[2] == cache.head_dim, "q is [tokens, q_heads, head_dim]")
-    T, hq = q.shape[0], q.shape[1]
-    kind, q_stride = _kv8_dtype(q), _kv8_rows(q, hq * cache.head_dim, "q")
+    n, table = seq_lens.numel(), block_tables.shape
+    if not (len(table) == 2 and table[0] >= n and query_start_loc.numel() >= n + 1):
+        raise ValueError("block_tables [n, W], query_start_loc [n + 1], seq_lens [n]")
+    shape = q.shape
+    if not (len(shape) == 3 and shape[2] == cache.head_dim):
+        raise ValueError("q is [tokens, q_heads, head_dim]")
+    T, hq, d = shape
+    kind, q_stride = _kv8_dtype(q), _kv8_rows(q, hq * d, "q")
     if weights is not None:
-        _need(str(weights.dtype) == "torch.float32" and weights.is_contiguous()
-              and weights.numel() == k_cache.shape[0], "weights is contiguous float32, one for each slot")
+        _kv8_weights(weights, k_cache.shape[0])
     handle = _stream(stream)
     made = []
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        out = q.new_empty(shape)
         made.append(out)
-    _need(out.shape == q.shape and out.dtype == q.dtype, "out has q's shape and type")
-    out_stride = _kv8_rows(out, hq * cache.head_dim, "out")
+        out_stride = hq * d * 2
+    else:
+        if not (out.shape == shape and out.dtype is q.dtype):
+            raise ValueError("out has q's shape and type")
+        out_stride = _kv8_rows(out, hq * d, "out")
     if lse is None:
-        lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((T, hq), dtype=f32)
         made.append(lse)
-    _need(lse.shape == (T, hq) and lse.is_contiguous() and str(lse.dtype) == "torch.float32",
-          "lse is contiguous float32 [tokens, q_heads]")
+    elif not (lse.shape == (T, hq) and lse.dtype is f32 and lse.is_contiguous()):
+        raise ValueError("lse is contiguous float32 [tokens, q_heads]")
     if workspace is None:
-        workspace = torch.empty(kv8_attention_workspace(T, hq, cache.head_dim, weights is not None),
-                                dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty(kv8_attention_workspace(T, hq, d, weights is not None), dtype=torch.uint8)
         made.append(workspace)
-    if stream is not None and made and q.is_cuda:
-        # tensors made here were allocated on the current stream, the work runs on another
-        other = torch.cuda.ExternalStream(handle) if isinstance(stream, int) else stream
-        for t in made:
-            t.record_stream(other)
-    if softmax_scale is None:
-        softmax_scale = cache.head_dim ** -0.5
-    rc = lib().pkv_kv8_attention(C.byref(cache), _ptr(q), q_stride, kind, hq, _ptr(block_tables),
-                                 block_tables.shape[1], _ptr(query_start_loc), _ptr(seq_lens), n, T,
-                                 float(softmax_scale), int(window), _ptr(out), out_stride, _ptr(lse),
-                                 _ptr(weights), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                 C.c_void_p(d_error) if d_error else None, handle)
-    if check:
-        _check(rc, "pkv_kv8_attention")
-        return out, lse
-    return (out, lse) if rc == OK else rc
+    if stream is not None:
+        _kv8_made(made, stream, handle)
+    rc = lib().pkv_kv8_attention(C.byref(cache), q.data_ptr(), q_stride, kind, hq, block_tables.data_ptr(),
+                                 table[1], query_start_loc.data_ptr(), seq_lens.data_ptr(), n, T,
+                                 d ** -0.5 if softmax_scale is None else float(softmax_scale), int(window),
+                                 out.data_ptr(), out_stride, lse.data_ptr(),
+                                 None if weights is None else weights.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel() * workspace.itemsize, d_error or None, handle)
+    if rc != OK:
+        if check:
+            raise PkvError(rc, "pkv_kv8_attention")
+        return rc
+    return out, lse
 
 
 def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_lens,
@@ -948,34 +979,32 @@ def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_len
               d_error=None, stream=None, check=True):
     """Shrink requests to ``budget`` tokens by accumulated weight, into new blocks
     (``pkv_kv8_evict``).  Returns (new_seq_lens [n], kept [n, budget])."""
-    import torch
-
     cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     _kv8_int32(block_tables, new_block_tables, seq_lens)
-    n = seq_lens.numel()
-    _need(block_tables.dim() == 2 and new_block_tables.dim() == 2 and block_tables.shape[0] >= n
-          and new_block_tables.shape[0] >= n, "block_tables and new_block_tables are [n, width]")
-    _need(str(weights.dtype) == "torch.float32" and weights.is_contiguous()
-          and weights.numel() == k_cache.shape[0], "weights is contiguous float32, one for each slot")
+    n, budget = seq_lens.numel(), int(budget)
+    old, new = block_tables.shape, new_block_tables.shape
+    if not (len(old) == 2 and len(new) == 2 and old[0] >= n and new[0] >= n):
+        raise ValueError("block_tables and new_block_tables are [n, width]")
+    _kv8_weights(weights, k_cache.shape[0])
     handle = _stream(stream)
     made = []
     if new_seq_lens is None:
-        new_seq_lens = torch.empty(n, dtype=torch.int32, device=k_cache.device)
+        new_seq_lens = seq_lens.new_empty(n)
         made.append(new_seq_lens)
     if kept is None:
-        kept = torch.empty((n, max(int(budget), 0)), dtype=torch.int32, device=k_cache.device)
+        kept = seq_lens.new_empty((n, max(budget, 0)))
         made.append(kept)
     _kv8_int32(new_seq_lens, kept)
-    _need(new_seq_lens.numel() == n and kept.numel() == n * max(int(budget), 0), "new_seq_lens [n], kept [n, budget]")
-    if stream is not None and made and k_cache.is_cuda:
-        other = torch.cuda.ExternalStream(handle) if isinstance(stream, int) else stream
-        for t in made:
-            t.record_stream(other)
-    rc = lib().pkv_kv8_evict(C.byref(cache), _ptr(weights), _ptr(block_tables), block_tables.shape[1],
-                             _ptr(seq_lens), n, _ptr(new_block_tables), new_block_tables.shape[1],
-                             int(budget), int(keep_first), int(keep_last), _ptr(new_seq_lens),
-                             _ptr(kept), C.c_void_p(d_error) if d_error else None, handle)
-    if check:
-        _check(rc, "pkv_kv8_evict")
-        return new_seq_lens, kept
-    return (new_seq_lens, kept) if rc == OK else rc
+    if not (new_seq_lens.numel() == n and kept.numel() == n * max(budget, 0)):
+        raise ValueError("new_seq_lens [n], kept [n, budget]")
+    if stream is not None:
+        _kv8_made(made, stream, handle)
+    rc = lib().pkv_kv8_evict(C.byref(cache), weights.data_ptr(), block_tables.data_ptr(), old[1],
+                             seq_lens.data_ptr(), n, new_block_tables.data_ptr(), new[1], budget,
+                             int(keep_first), int(keep_last), new_seq_lens.data_ptr(), kept.data_ptr(),
+                             d_error or None, handle)
+    if rc != OK:
+        if check:
+            raise PkvError(rc, "pkv_kv8_evict")
+        return rc
+    return new_seq_lens, kept

@@ -12,7 +12,7 @@
 // behind one another.  A CTA owns kT token groups of 32 of a request and walks
 // the KV heads: a head's codes come by cp.async while the head before is worked
 // on, become f16 fragments in registers once, and meet the request's rows in
-// chunks of 64 that bulk copies bring two chunks ahead.  With kT = 8 (single tokens: few rows) a warp per group; with kT = 1
+// chunks that bulk copies bring two chunks ahead.  With kT = 8 (single tokens: few rows) a warp per group; with kT = 1
 // (chunks: many rows) the warps share a group's rows and a cluster shares the
 // KV heads, so that the tokens that thousands of rows see do not hold the
 // launch up; the sums meet in a fixed order.
@@ -34,8 +34,9 @@ namespace {
 constexpr int kPrefillRows = 32;
 
 constexpr int kWWarps = 8, kWThreads = 32 * kWWarps, kWStages = 3;
-template <int D>
-constexpr int kWRows = D <= 128 ? 64 : 32;                    // rows of a chunk
+constexpr uint32_t kNone = 0xffffffffu;                       // no slot: slots fit 32 bits with room
+template <int D, int kT>
+constexpr int kWRows = D > 128 ? 32 : kT == 1 ? 128 : 64;     // rows of a chunk
 
 template <int D, int kT>
 struct WeightsShape {
@@ -48,10 +49,11 @@ template <int D, int kT>
 struct WeightsSmem {
     static constexpr int kTokens = WeightsShape<D, kT>::kTokens;
     alignas(16) char k[kTokens * D];
-    alignas(16) char q[kWStages][kWRows<D> * D * 2];                         // packed rows
-    alignas(16) float2 fac[kWStages][kWRows<D> + 2];                            // factor of S, -lse (both for base 2)
+    alignas(16) char q[kWStages][kWRows<D, kT> * D * 2];                         // packed rows
+    alignas(16) float2 fac[kWStages][kWRows<D, kT> + 2];                            // factor of S, -lse (both for base 2)
     uint64_t full[kWStages];
     int32_t block[2][kTokens];                                // by unit parity; -1: not read
+    uint32_t slot[2][kTokens];
     float ks[kTokens];
     float sum[kWWarps][WeightsShape<D, kT>::kGroup];
     float total[2][kTokens];                                  // by unit parity: this CTA's heads
@@ -74,7 +76,7 @@ struct Packed {
     float2 *fac;
 };
 
-// A warp per token, D / 8 lanes per row.
+// A warp per 32 * 8 / D rows of a token, D / 8 lanes per row.
 template <int D>
 __global__ void __launch_bounds__(256) kv8_pack_kernel(const AttnParams p, const Packed out) {
     constexpr int kPieces = D / 8, kAtOnce = 32 / kPieces;
@@ -82,34 +84,34 @@ __global__ void __launch_bounds__(256) kv8_pack_kernel(const AttnParams p, const
     pdl_trigger();
     const int lane = threadIdx.x & 31, piece = lane % kPieces;
     const bool fp16 = p.fp16 != 0;
-    const int hq = p.Hkv * p.G;
-    for (int64_t tok = (blockIdx.x * 256LL + threadIdx.x) >> 5; tok < p.T; tok += gridDim.x * 8LL) {
-        for (int h0 = 0; h0 < hq; h0 += kAtOnce) {
-            const int h = h0 + lane / kPieces;
-            uint4 y = make_uint4(0, 0, 0, 0);
-            float lse = -INFINITY;
-            if (h < hq) {
-                y = __ldg(reinterpret_cast<const uint4 *>(p.q + tok * p.q_stride + 2 * (static_cast<int64_t>(h) * D + 8 * piece)));
-                lse = p.lse[tok * hq + h];
-            }
-            const float2 a = widen2(y.x, fp16), b = widen2(y.y, fp16), c = widen2(y.z, fp16), d = widen2(y.w, fp16);
-            float m = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))),
-                            fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
+    const int hq = p.Hkv * p.G, per = (hq + kAtOnce - 1) / kAtOnce;
+    const int64_t jobs = static_cast<int64_t>(p.T) * per;
+    for (int64_t job = (blockIdx.x * 256LL + threadIdx.x) >> 5; job < jobs; job += gridDim.x * 8LL) {
+        const int64_t tok = job / per;
+        const int h = static_cast<int>(job - tok * per) * kAtOnce + lane / kPieces;
+        uint4 y = make_uint4(0, 0, 0, 0);
+        float lse = -INFINITY;
+        if (h < hq) {
+            y = __ldg(reinterpret_cast<const uint4 *>(p.q + tok * p.q_stride + 2 * (static_cast<int64_t>(h) * D + 8 * piece)));
+            lse = p.lse[tok * hq + h];
+        }
+        const float2 a = widen2(y.x, fp16), b = widen2(y.y, fp16), c = widen2(y.z, fp16), d = widen2(y.w, fp16);
+        float m = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))),
+                        fmaxf(fmaxf(fabsf(c.x), fabsf(c.y)), fmaxf(fabsf(d.x), fabsf(d.y))));
 #pragma unroll
-            for (int o = kPieces / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-            const int e = row_exponent(m);
-            const float s = power2(14 - e);
-            if (h < hq) {
-                const int head = h / p.G;
-                const int64_t row = (static_cast<int64_t>(head) * p.T + tok) * p.G + h - head * p.G;
-                // dimensions 8 piece ..: fragment steps 4 u + i and the one after it, lane t
-                const int dim = 8 * piece, pair = (4 * (dim / 64) + (dim % 16) / 4) >> 1, t = (dim % 64) / 16;
-                const int at = (4 * pair + t) ^ (static_cast<int>(row & 1) << 2);
-                *reinterpret_cast<uint4 *>(out.rows + row * (2 * D) + 16 * at) =
-                    make_uint4(pack_f16(a.x * s, a.y * s), pack_f16(b.x * s, b.y * s), pack_f16(c.x * s, c.y * s),
-                               pack_f16(d.x * s, d.y * s));
-                if (piece == 0) out.fac[row] = make_float2(p.scale_log2 * power2(e - 14), -lse * kLog2e);
-            }
+        for (int o = kPieces / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        const int e = row_exponent(m);
+        const float s = power2(14 - e);
+        if (h < hq) {
+            const int head = h / p.G;
+            const int64_t row = (static_cast<int64_t>(head) * p.T + tok) * p.G + h - head * p.G;
+            // dimensions 8 piece ..: fragment steps 4 u + i and the one after it, lane t
+            const int dim = 8 * piece, pair = (4 * (dim / 64) + (dim % 16) / 4) >> 1, t = (dim % 64) / 16;
+            const int at = (4 * pair + t) ^ (static_cast<int>(row & 1) << 2);
+            *reinterpret_cast<uint4 *>(out.rows + row * (2 * D) + 16 * at) =
+                make_uint4(pack_f16(a.x * s, a.y * s), pack_f16(b.x * s, b.y * s), pack_f16(c.x * s, c.y * s),
+                           pack_f16(d.x * s, d.y * s));
+            if (piece == 0) out.fac[row] = make_float2(p.scale_log2 * power2(e - 14), -lse * kLog2e);
         }
     }
 }
@@ -177,8 +179,9 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
     auto find_blocks = [&](const Unit &x, int parity) {
         if (tid < kTokens) {
             const int s = x.s0 + tid;
-            sm.block[parity][tid] = s >= x.r.lo && s < x.r.keys
-                                        ? block_of(p, p.tables + static_cast<int64_t>(x.i) * p.W, s) : -1;
+            const int b = s >= x.r.lo && s < x.r.keys ? block_of(p, p.tables + static_cast<int64_t>(x.i) * p.W, s) : -1;
+            sm.block[parity][tid] = b;
+            sm.slot[parity][tid] = b < 0 ? kNone : static_cast<uint32_t>(b) * static_cast<uint32_t>(p.bs) + static_cast<uint32_t>(s % p.bs);
         }
     };
     // the codes and scales of one head
@@ -189,10 +192,9 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
         for (int i = 0; i < (kTokens + kStep - 1) / kStep; i++) {
             const int tok = i * kStep + tid / kRowLanes;
             if (tok < kTokens) {
-                const int b = sm.block[parity][tok];
-                const int64_t slot = static_cast<int64_t>(b) * p.bs + (x.s0 + tok) % p.bs;
+                const uint32_t slot = sm.slot[parity][tok];
                 cp_async<16>(smem_addr(sm.k + tok * D + 16 * swizzle<D>(piece, tok)),
-                             p.kc + (b >= 0 ? slot * line + head * D + 16 * piece : 0), b >= 0);
+                             p.kc + (slot != kNone ? slot * line + head * D + 16 * piece : 0), slot != kNone);
             }
         }
         if (tid < kTokens) {
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
     auto ask_rows = [&]() {
         if (feed.u >= end) return;
         const int stage = feed.count % kWStages;
-        const int rows = min(kWRows<D>, feed.x.f1 - feed.f);
+        const int rows = min(kWRows<D, kT>, feed.x.f1 - feed.f);
         const int64_t row = (static_cast<int64_t>(feed.head) * p.T + feed.x.r.start) * p.G + feed.f;
         // the factors' copy starts on an even row and the two sides' offsets agree
         const int odd = static_cast<int>(row & 1);
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
         bulk_g2s(sm.q[stage], packed.rows + row * (2 * D), rows * 2 * D, &sm.full[stage]);
         bulk_g2s(sm.fac[stage], packed.fac + row - odd, facs, &sm.full[stage]);
         feed.count++;
-        feed.f += kWRows<D>;
+        feed.f += kWRows<D, kT>;
         if (feed.f >= feed.x.f1) {
             feed.head += mates;
             if (feed.head >= p.Hkv) {
@@ -289,14 +291,14 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
             else if (more) fetch(y, parity ^ 1, rank);
             const int back = x.r.len - x.r.count;
             const int64_t row0 = (static_cast<int64_t>(head) * p.T + x.r.start) * p.G;
-            for (int f = x.f0; f < x.f1; f += kWRows<D>, chunk++) {
+            for (int f = x.f0; f < x.f1; f += kWRows<D, kT>, chunk++) {
                 if (f != x.f0) __syncthreads();               // everyone has left the stage that is filled next
                 if (tid == 0) ask_rows();
                 const int stage = chunk % kWStages;
                 if (!wait_rows(&sm.full[stage], (chunk / kWStages) & 1) && p.err) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
                 const int odd = static_cast<int>((row0 + f) & 1);
 #pragma unroll 1
-                for (int nt = team; nt < kWRows<D> / 8; nt += kTeams) {
+                for (int nt = team; nt < kWRows<D, kT> / 8; nt += kTeams) {
                     if (f + 8 * nt >= x.f1) break;
                     float c[kSubs][4];
 #pragma unroll
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
         if (rank == 0 && tid < kTokens && sm.block[parity][tid] >= 0) {
             float a = sm.total[parity][tid];
             for (int c = 1; c < mates; c++) a += cluster_read(&sm.total[parity][tid], c);
-            atomicAdd(p.weights + static_cast<int64_t>(sm.block[parity][tid]) * p.bs + (x.s0 + tid) % p.bs, a);
+            atomicAdd(p.weights + sm.slot[parity][tid], a);
         }
         if (!more) break;
         __syncthreads();
@@ -418,7 +420,8 @@ int launch_weights_as(const AttnParams &p, const Packed &packed, int mates, int 
         if (dev < 64) known[dev][log] = clusters;
     }
     if (clusters * mates < 2 * sms) cfg.gridDim = dim3(static_cast<unsigned>(clusters * mates));
-    PKV_CUDA_TRY(launch_pdl(kv8_pack_kernel<D>, dim3(static_cast<unsigned>(p.T < 64 * sms ? (p.T + 7) / 8 : 8 * sms)), dim3(256), 0, s, p, packed));
+    const int64_t pack = (static_cast<int64_t>(p.T) * p.Hkv * p.G * D + 2047) / 2048;   // CTAs that hold all rows
+    PKV_CUDA_TRY(launch_pdl(kv8_pack_kernel<D>, dim3(static_cast<unsigned>(pack < 8 * sms ? pack : 8 * sms)), dim3(256), 0, s, p, packed));
     PKV_CUDA_TRY(cudaLaunchKernelEx(&cfg, kv8_weights_kernel<D, kT>, p, packed));
     return PKV_OK;
 }
