@@ -816,7 +816,8 @@ def _kv8_types():
     if _KV8 is None:
         import torch
 
-        _KV8 = (torch, {torch.bfloat16: 0, torch.float16: 1}, torch.float32, torch.int32, torch.int64)
+        _KV8 = (torch, {torch.bfloat16: 0, torch.float16: 1}, torch.float32, torch.int32, torch.int64,
+                getattr(torch._C, "_cuda_getCurrentRawStream", None))
     return _KV8
 
 
@@ -877,6 +878,17 @@ def _kv8_weights(weights, slots):
         raise ValueError("weights is contiguous float32, one for each slot")
 
 
+def _kv8_stream(stream, tensor):
+    """The stream's handle; without one the current stream of the tensor's device (its raw handle
+    where torch gives it: the stream object costs more than the rest of the marshalling)."""
+    if stream is None:
+        raw = _kv8_types()[5]
+        if raw is not None and tensor.is_cuda:
+            return raw(tensor.get_device())
+        return _stream(None)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
 def _kv8_made(made, stream, handle):
     """Tensors made for a call were allocated on the current stream; the work runs on another."""
     made = [t for t in made if t.is_cuda]
@@ -902,7 +914,7 @@ def kv8_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, d_error=No
     width = cache.num_heads * cache.head_dim
     rc = lib().pkv_kv8_store(C.byref(cache), k.data_ptr(), v.data_ptr(), _kv8_rows(k, width, "k"),
                              _kv8_rows(v, width, "v"), _kv8_dtype(k), slot_mapping.data_ptr(), T,
-                             d_error or None, _stream(stream))
+                             d_error or None, _kv8_stream(stream, k_cache))
     if check and rc != OK:
         raise PkvError(rc, "pkv_kv8_store")
     return rc
@@ -928,7 +940,7 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     that many positions, its own among them (0: all).  weights: float32 [num_slots], each token's
     softmax weight is added to it.  out, lse, workspace (uint8, kv8_attention_workspace bytes) are
     allocated when not given.  Returns (out, lse); lse is float32 [tokens, q_heads]."""
-    torch, _, f32, _, _ = _kv8_types()
+    torch, _, f32 = _kv8_types()[:3]
     cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     _kv8_int32(block_tables, query_start_loc, seq_lens)
     n, table = seq_lens.numel(), block_tables.shape
@@ -941,10 +953,10 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     kind, q_stride = _kv8_dtype(q), _kv8_rows(q, hq * d, "q")
     if weights is not None:
         _kv8_weights(weights, k_cache.shape[0])
-    handle = _stream(stream)
+    handle = _kv8_stream(stream, k_cache)
     made = []
     if out is None:
-        out = q.new_empty(shape)
+        out = torch.empty(shape, dtype=q.dtype, device=q.device)
         made.append(out)
         out_stride = hq * d * 2
     else:
@@ -952,12 +964,13 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
             raise ValueError("out has q's shape and type")
         out_stride = _kv8_rows(out, hq * d, "out")
     if lse is None:
-        lse = q.new_empty((T, hq), dtype=f32)
+        lse = torch.empty((T, hq), dtype=f32, device=q.device)
         made.append(lse)
     elif not (lse.shape == (T, hq) and lse.dtype is f32 and lse.is_contiguous()):
         raise ValueError("lse is contiguous float32 [tokens, q_heads]")
     if workspace is None:
-        workspace = q.new_empty(kv8_attention_workspace(T, hq, d, weights is not None), dtype=torch.uint8)
+        workspace = torch.empty(kv8_attention_workspace(T, hq, d, weights is not None), dtype=torch.uint8,
+                                device=q.device)
         made.append(workspace)
     if stream is not None:
         _kv8_made(made, stream, handle)
@@ -979,6 +992,7 @@ def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_len
               d_error=None, stream=None, check=True):
     """Shrink requests to ``budget`` tokens by accumulated weight, into new blocks
     (``pkv_kv8_evict``).  Returns (new_seq_lens [n], kept [n, budget])."""
+    torch = _kv8_types()[0]
     cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     _kv8_int32(block_tables, new_block_tables, seq_lens)
     n, budget = seq_lens.numel(), int(budget)
@@ -986,13 +1000,13 @@ def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_len
     if not (len(old) == 2 and len(new) == 2 and old[0] >= n and new[0] >= n):
         raise ValueError("block_tables and new_block_tables are [n, width]")
     _kv8_weights(weights, k_cache.shape[0])
-    handle = _stream(stream)
+    handle = _kv8_stream(stream, k_cache)
     made = []
     if new_seq_lens is None:
-        new_seq_lens = seq_lens.new_empty(n)
+        new_seq_lens = torch.empty(n, dtype=torch.int32, device=seq_lens.device)
         made.append(new_seq_lens)
     if kept is None:
-        kept = seq_lens.new_empty((n, max(budget, 0)))
+        kept = torch.empty((n, max(budget, 0)), dtype=torch.int32, device=seq_lens.device)
         made.append(kept)
     _kv8_int32(new_seq_lens, kept)
     if not (new_seq_lens.numel() == n and kept.numel() == n * max(budget, 0)):

@@ -88,6 +88,17 @@ inline int kv8_check_cache(const pkv_kv8_cache *c) {
     return PKV_OK;
 }
 
+// Lets a kernel take `bytes` of dynamic shared memory; asked for once per device (`set` is the
+// kernel's own record).
+inline int kv8_allow_smem(const void *kernel, int bytes, bool (&set)[64]) {
+    int dev = 0;
+    PKV_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev < 64 && set[dev]) return PKV_OK;
+    PKV_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    if (dev < 64) set[dev] = true;
+    return PKV_OK;
+}
+
 // SMs of the current device (asked once per device).
 inline int kv8_sm_count(int *out) {
     int dev = 0;

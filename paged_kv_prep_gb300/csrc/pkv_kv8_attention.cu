@@ -387,7 +387,9 @@ template <int D, int kT>
 int launch_weights_as(const AttnParams &p, const Packed &packed, int mates, int sms, cudaStream_t s) {
     constexpr int smem = static_cast<int>(sizeof(WeightsSmem<D, kT>));
     static_assert(smem <= 110 * 1024, "two CTAs an SM");
-    PKV_CUDA_TRY(cudaFuncSetAttribute(kv8_weights_kernel<D, kT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    static bool set[64] = {false};
+    const int rc = kv8_allow_smem(reinterpret_cast<const void *>(kv8_weights_kernel<D, kT>), smem, set);
+    if (rc != PKV_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * sms / mates * mates));
     cfg.blockDim = dim3(kWThreads);

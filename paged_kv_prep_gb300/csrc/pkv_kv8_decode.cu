@@ -612,10 +612,15 @@ int launch(const AttnParams &p, int sms, cudaStream_t s) {
     constexpr int kWarps = warps_of<D, NT>();
     constexpr size_t smem = sizeof(Stage<D>) * kDepth * kWarps;
     static_assert(smem <= 220 * 1024, "shared memory");
-    PKV_CUDA_TRY(cudaFuncSetAttribute(kv8_decode_kernel<D, NT, kGrouped>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(smem)));
-    PKV_CUDA_TRY(launch_pdl(kv8_decode_kernel<D, NT, kGrouped>, dim3(sms), dim3(32 * kWarps), smem, s, p));
-    return kv8_launch_merge(p, D, 8 * NT, sms * kWarps, p.Hkv, s);
+    static bool set[64] = {false};
+    const int rc = kv8_allow_smem(reinterpret_cast<const void *>(kv8_decode_kernel<D, NT, kGrouped>), static_cast<int>(smem), set);
+    if (rc != PKV_OK) return rc;
+    // one CTA an SM, or as many as the longest requests the tables can name would give a unit a warp
+    const int64_t tiles = static_cast<int64_t>(p.T) * p.G / (8 * NT) + p.n;
+    const int64_t most = tiles * (static_cast<int64_t>(p.W) * p.bs / kUnit + 2) * p.Hkv;
+    const int grid = most < static_cast<int64_t>(sms) * kWarps ? static_cast<int>((most + kWarps - 1) / kWarps) : sms;
+    PKV_CUDA_TRY(launch_pdl(kv8_decode_kernel<D, NT, kGrouped>, dim3(grid), dim3(32 * kWarps), smem, s, p));
+    return kv8_launch_merge(p, D, 8 * NT, grid * kWarps, p.Hkv, s);
 }
 
 template <int D>

@@ -330,9 +330,10 @@ __global__ void __launch_bounds__(kCopyThreads, 4) kv8_copy_kernel(const EvictPa
 constexpr int kSelCap = 16384;                         // keys held per CTA: 64 KB
 
 template <int kCluster>
-cudaError_t launch_select(const EvictParams &p, int n, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(kv8_select_kernel<kCluster>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCap * 4);
-    if (e != cudaSuccess) return e;
+int launch_select(const EvictParams &p, int n, cudaStream_t s) {
+    static bool set[64] = {false};
+    const int rc = pkv::kv8_allow_smem(reinterpret_cast<const void *>(kv8_select_kernel<kCluster>), kSelCap * 4, set);
+    if (rc != PKV_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(n) * kCluster);
     cfg.blockDim = dim3(kSelThreads);
@@ -350,7 +351,8 @@ cudaError_t launch_select(const EvictParams &p, int n, cudaStream_t s) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = kCluster == 1 ? 1 : 2;
-    return cudaLaunchKernelEx(&cfg, kv8_select_kernel<kCluster>, p, cap);
+    PKV_CUDA_TRY(cudaLaunchKernelEx(&cfg, kv8_select_kernel<kCluster>, p, cap));
+    return PKV_OK;
 }
 
 }  // namespace
@@ -394,10 +396,8 @@ extern "C" int pkv_kv8_evict(const pkv_kv8_cache *cache, float *weights,
     cudaStream_t s = pkv::as_stream(stream);
     // Eight CTAs share a request where tables reach past 16384 tokens (one CTA holds that many keys):
     // four requests of 131072 tokens MEASURE.
-    if (static_cast<int64_t>(p.W) * p.bs > kSelCap)
-        PKV_CUDA_TRY(launch_select<8>(p, n, s));
-    else
-        PKV_CUDA_TRY(launch_select<1>(p, n, s));
+    rc = static_cast<int64_t>(p.W) * p.bs > kSelCap ? launch_select<8>(p, n, s) : launch_select<1>(p, n, s);
+    if (rc != PKV_OK) return rc;
     const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(budget) + p.bs - 1) / p.bs);
     const int chunks = p.line / 16;
     const int chunk_shift = (chunks & (chunks - 1)) ? -1 : 31 - __builtin_clz(static_cast<unsigned>(chunks));

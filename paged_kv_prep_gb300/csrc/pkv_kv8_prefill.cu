@@ -758,8 +758,9 @@ template <int D>
 int launch(const AttnParams &p, int sms, cudaStream_t s) {
     constexpr size_t smem = sizeof(Smem<D>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
-    PKV_CUDA_TRY(cudaFuncSetAttribute(kv8_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(smem)));
+    static bool set[64] = {false};
+    const int rc = kv8_allow_smem(reinterpret_cast<const void *>(kv8_prefill_kernel<D>), static_cast<int>(smem), set);
+    if (rc != PKV_OK) return rc;
     PKV_CUDA_TRY(launch_pdl(kv8_prefill_kernel<D>, dim3(sms), dim3(kThreads), smem, s, p));
     return kv8_launch_merge(p, D, kRows, sms, 1, s);
 }
