@@ -531,7 +531,9 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
 // Merge the partial results of the tiles that were cut, a warp per (worker, row).
 constexpr int kMergeThreads = 256;
 
-template <int D>
+// kBatch: partial rows on their way at a time (sixteen for the long chains of a few decodes; two
+// pieces are the rule for row tiles of chunks, whose thousands of rows want more warps resident).
+template <int D, int kBatch>
 __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnParams p, int rows, int workers, int stride) {
     constexpr int kPer = D / 32;
     pdl_wait();
@@ -565,34 +567,28 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
             fac = m == -INFINITY ? (l == 0.f ? 0.f : NAN) : exp2_fast(m - top);
             sum += fac * l;
         }
-        // many pieces: sixteen rows on their way at a time; few: four
         const int n = min(32, pieces - k0);
-        auto add = [&](auto batch) {
-            constexpr int kBatch = decltype(batch)::value;
-            for (int k1 = 0; k1 < n; k1 += kBatch) {
-                float y[kBatch][kPer];
+        for (int k1 = 0; k1 < n; k1 += kBatch) {
+            float y[kBatch][kPer];
 #pragma unroll
-                for (int k = 0; k < kBatch; k++) {
-                    const float *o = part(k0 + min(k1 + k, n - 1)) + 2 * rows + row * D + lane * kPer;
+            for (int k = 0; k < kBatch; k++) {
+                const float *o = part(k0 + min(k1 + k, n - 1)) + 2 * rows + row * D + lane * kPer;
 #pragma unroll
-                    for (int c = 0; c < kPer; c += 2) {
-                        const float2 z = *reinterpret_cast<const float2 *>(o + c);
-                        y[k][c] = z.x;
-                        y[k][c + 1] = z.y;
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; k++) {
-                    const float f2 = __shfl_sync(~0u, fac, k1 + k);
-                    if (k1 + k < n && f2 != 0.f) {
-#pragma unroll
-                        for (int c = 0; c < kPer; c++) acc[c] = fmaf(f2, y[k][c], acc[c]);
-                    }
+                for (int c = 0; c < kPer; c += 2) {
+                    const float2 z = *reinterpret_cast<const float2 *>(o + c);
+                    y[k][c] = z.x;
+                    y[k][c + 1] = z.y;
                 }
             }
-        };
-        if (n > 8) add(std::integral_constant<int, 16>());
-        else add(std::integral_constant<int, 4>());
+#pragma unroll
+            for (int k = 0; k < kBatch; k++) {
+                const float f2 = __shfl_sync(~0u, fac, k1 + k);
+                if (k1 + k < n && f2 != 0.f) {
+#pragma unroll
+                    for (int c = 0; c < kPer; c++) acc[c] = fmaf(f2, y[k][c], acc[c]);
+                }
+            }
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
@@ -633,12 +629,11 @@ int launch_rows(const AttnParams &p, bool one_tile, int sms, cudaStream_t s) {
 
 int kv8_launch_merge(const AttnParams &p, int32_t head_dim, int rows, int workers, int stride, cudaStream_t s) {
     const dim3 grid((static_cast<unsigned>(workers) * rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32)), block(kMergeThreads);
-    if (head_dim == 64)
-        PKV_CUDA_TRY(launch_pdl(kv8_merge_kernel<64>, grid, block, 0, s, p, rows, workers, stride));
-    else if (head_dim == 128)
-        PKV_CUDA_TRY(launch_pdl(kv8_merge_kernel<128>, grid, block, 0, s, p, rows, workers, stride));
-    else
-        PKV_CUDA_TRY(launch_pdl(kv8_merge_kernel<256>, grid, block, 0, s, p, rows, workers, stride));
+    const bool tile = rows > 16;
+    auto kernel = head_dim == 64 ? (tile ? kv8_merge_kernel<64, 2> : kv8_merge_kernel<64, 16>)
+                  : head_dim == 128 ? (tile ? kv8_merge_kernel<128, 2> : kv8_merge_kernel<128, 16>)
+                                    : kv8_merge_kernel<256, 16>;
+    PKV_CUDA_TRY(launch_pdl(kernel, grid, block, 0, s, p, rows, workers, stride));
     return PKV_OK;
 }
 

@@ -664,18 +664,16 @@ __device__ void issue_role(Smem<D> *sm, Walk<D> &walk) {
         for (int t = 0; t < nu && ok; t++, unit++) {
             const int stage = unit & 1, next = stage ^ 1;
             for (int m = 0; m < tiles && ok; m++) {
-                if (m == 0) ok = all(&sm->v_full[stage], (unit >> 1) & 1);
+                if (m == 0) {
+                    // the operands are usually there before the weights are: off the weights' path
+                    ok = all(&sm->v_full[stage], (unit >> 1) & 1) && (t + 1 == nu || all(&sm->k_full[next], ((unit + 1) >> 1) & 1));
+                }
                 ok = ok && all(&sm->p_full[m], p_phase[m]);
                 p_phase[m] ^= 1;
                 if (!ok) break;
                 tc_fence_after();
                 pv(m, stage, t > 0);
                 if (t + 1 < nu) {
-                    if (m == 0) {
-                        ok = all(&sm->k_full[next], ((unit + 1) >> 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                    }
                     qk(m, next);
                 } else {
                     commit(&sm->o_full[m]);
