@@ -362,7 +362,8 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk, in
 
         const int f0 = x.rt * kRows + m * 128, f1 = min(rows, f0 + 128) - 1;
         const int pos0 = back + f0 / p.G, pos1 = back + f1 / p.G;
-        float top = -INFINITY, sum = 0.f;
+        // a row past the tile's last sees nothing and needs no reference to be looked for
+        float top = live ? -INFINITY : 0.f, sum = 0.f;
         bool ok = true;
         for (int t = 0; t < nu && ok; t++, unit++) {
             ok = wait(sm, &sm->s_full[m], s_phase);
