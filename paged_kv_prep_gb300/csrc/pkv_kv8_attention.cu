@@ -51,7 +51,7 @@ struct WeightsSmem {
     alignas(16) char k[kTokens * D];
     alignas(16) char q[kWStages][kWRows<D, kT> * D * 2];                         // packed rows
     alignas(16) float2 fac[kWStages][kWRows<D, kT> + 2];                            // factor of S, -lse (both for base 2)
-    uint64_t full[kWStages];
+    uint64_t full[kWStages], free[kWStages];
     int32_t block[2][kTokens];                                // by unit parity; -1: not read
     uint32_t slot[2][kTokens];
     float ks[kTokens];
@@ -128,7 +128,10 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
     const int group = warp % kT, team = warp / kT;
     const int64_t line = static_cast<int64_t>(p.Hkv) * D;
     if (tid == 0) {
-        for (int k = 0; k < kWStages; k++) mbar_init(&sm.full[k], 1);
+        for (int k = 0; k < kWStages; k++) {
+            mbar_init(&sm.full[k], 1);
+            mbar_init(&sm.free[k], kWWarps);
+        }
         fence_mbar_init();
     }
     auto units = [&](int i) -> int64_t {
@@ -203,7 +206,8 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
         }
         cp_commit();
     };
-    // The rows' chunks in the order in which they are used; thread 0 asks for them two ahead.
+    // The rows' chunks in the order in which they are used; thread 0 asks for them two ahead, into the
+    // place of the chunk before.
     struct Feed {
         Walk walk;
         int64_t u;
@@ -215,6 +219,9 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
     auto ask_rows = [&]() {
         if (feed.u >= end) return;
         const int stage = feed.count % kWStages;
+        // every warp has left the chunk that had this place before
+        if (feed.count >= kWStages && !wait_rows(&sm.free[stage], (feed.count / kWStages - 1) & 1) && p.err)
+            atomicOr(p.err, PKV_DEVERR_TIMEOUT);
         const int rows = min(kWRows<D, kT>, feed.x.f1 - feed.f);
         const int64_t row = (static_cast<int64_t>(feed.head) * p.T + feed.x.r.start) * p.G + feed.f;
         // the factors' copy starts on an even row and the two sides' offsets agree
@@ -292,11 +299,14 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
             const int back = x.r.len - x.r.count;
             const int64_t row0 = (static_cast<int64_t>(head) * p.T + x.r.start) * p.G;
             for (int f = x.f0; f < x.f1; f += kWRows<D, kT>, chunk++) {
-                if (f != x.f0) __syncthreads();               // everyone has left the stage that is filled next
                 if (tid == 0) ask_rows();
                 const int stage = chunk % kWStages;
                 if (!wait_rows(&sm.full[stage], (chunk / kWStages) & 1) && p.err) atomicOr(p.err, PKV_DEVERR_TIMEOUT);
                 const int odd = static_cast<int>((row0 + f) & 1);
+                // every row of the chunk sees every token of the tile (tokens that are not read do not count:
+                // their sums are dropped)
+                const int p0 = back + f / p.G, p1 = back + (min(f + kWRows<D, kT>, x.f1) - 1) / p.G;
+                const bool chunk_whole = x.s0 + kTokens - 1 <= p0 && (p.window <= 0 || x.s0 > p1 - p.window);
 #pragma unroll 1
                 for (int nt = team; nt < kWRows<D, kT> / 8; nt += kTeams) {
                     if (f + 8 * nt >= x.f1) break;
@@ -315,11 +325,8 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
                         }
                     }
                     const float2 fa = sm.fac[stage][odd + 8 * nt + 2 * t], fb = sm.fac[stage][odd + 8 * nt + 2 * t + 1];
-                    // rows first .. first + 7 see every token of the tile (tokens that are not read do not
-                    // count: their sums are dropped)
                     const int first = f + 8 * nt;
-                    const int p0 = back + first / p.G, p1 = back + (first + 7) / p.G;
-                    const bool whole = first + 8 <= x.f1 && x.s0 + kTokens - 1 <= p0 && (p.window <= 0 || x.s0 > p1 - p.window);
+                    const bool whole = chunk_whole && first + 8 <= x.f1;
                     float v[kSubs][4];
 #pragma unroll
                     for (int k = 0; k < kSubs; k++)
@@ -344,6 +351,8 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
 #pragma unroll
                         for (int h = 0; h < 2; h++) acc[k][h] += v[k][2 * h] + v[k][2 * h + 1];
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.free[stage]);
             }
         }
 #pragma unroll

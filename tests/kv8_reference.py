@@ -83,28 +83,38 @@ def attention(q, kc, vc, ks, vs, tables, starts, lens, scale, window, weights=No
     lse = torch.full((T, hq), -math.inf, dtype=torch.float64)
     for i, length in enumerate(lens):
         a, b = starts[i], starts[i + 1]
-        for t in range(a, b):
-            pos = length - (b - t)
-            keys = range(max(0, pos - window + 1) if window else 0, pos + 1)
-            keys = [s for s in keys if s // bs < tables.shape[1] and 0 <= tables[i, s // bs] < blocks]
-            if not keys:
-                continue
-            at = torch.tensor(keys)
-            block = tables[i].long()[at // bs]
-            slot = block * bs + at % bs
-            for h in range(heads):
-                k = decode(kc[slot, h]) * ks[block, h].double()[:, None]
-                v = decode(vc[slot, h]) * vs[block, h].double()[:, None]
-                x = q[t, h * group:(h + 1) * group].double()
-                logits = (x @ k.T) * scale
-                top = torch.logsumexp(logits, -1)
-                p = torch.exp(logits - top[:, None])
-                out[t, h * group:(h + 1) * group] = p @ v
-                size[t, h * group:(h + 1) * group] = p @ v.abs()
-                reach[t, h * group:(h + 1) * group] = ((x.abs() @ k.abs().T) * abs(scale)).amax(-1)
-                lse[t, h * group:(h + 1) * group] = top
-                if weights is not None:
-                    weights.index_add_(0, slot, p.sum(0))
+        keys = [s for s in range(max(length, 0)) if s // bs < tables.shape[1] and 0 <= tables[i, s // bs] < blocks]
+        if a == b or not keys:
+            continue
+        at = torch.tensor(keys)
+        block = tables[i].long()[at // bs]
+        slot = block * bs + at % bs
+        pos = length - b + torch.arange(a, b)                              # of the queries
+        seen = at[None, :] <= pos[:, None]
+        if window:
+            seen &= at[None, :] > pos[:, None] - window
+        some = seen.any(1)
+        for h in range(heads):
+            k = decode(kc[slot, h]) * ks[block, h].double()[:, None]
+            v = decode(vc[slot, h]) * vs[block, h].double()[:, None]
+            x = q[a:b, h * group:(h + 1) * group].double()
+            logits = (x @ k.T * scale).masked_fill(~seen[:, None], -math.inf)
+            top = torch.logsumexp(logits, -1)
+            p = torch.exp(logits - top[..., None]).masked_fill(~seen[:, None], 0.0)
+            hs = slice(h * group, (h + 1) * group)
+            # a value that is NaN reaches the rows that see it and no other
+            plain = torch.where(v.isnan(), 0.0, v)
+            out[a:b, hs] = p @ plain
+            hit = (seen.double() @ v.isnan().double()) > 0
+            out[a:b, hs] = out[a:b, hs].masked_fill(hit[:, None, :], math.nan)
+            size[a:b, hs] = p @ plain.abs()
+            far = (x.abs() @ torch.where(k.isnan(), 0.0, k).abs().T * abs(scale)).masked_fill(~seen[:, None], 0.0)
+            reach[a:b, hs] = far.amax(-1)
+            lse[a:b, hs] = top
+            if weights is not None:
+                weights.index_add_(0, slot, p.sum((0, 1)))
+            none = torch.arange(a, b)[~some]
+            out[none, hs], lse[none, hs] = 0.0, -math.inf
     return out, lse, size, reach
 
 
