@@ -634,6 +634,7 @@ int pkv_kv8_attention_workspace(int32_t num_tokens, int32_t num_q_heads, int32_t
  *         weight, summed over the step's queries and heads, is added to its
  *         slot (needs lse; where requests of one call share a block their
  *         sums are added in any order).
+ *   workspace: device, 16-byte aligned, at least pkv_kv8_attention_workspace bytes.
  * A row that sees nothing gives 0 and -inf.  Tokens past query_start_loc[n] are
  * not written.  Device errors: PKV_DEVERR_COUNT (query_start_loc descends or
  * leaves the batch: the request is skipped), PKV_DEVERR_BLOCK (a block id past

@@ -19,6 +19,9 @@
 //
 // Bound: for single tokens HBM (D bytes of K per token and KV head, the second
 // read of K), for chunks the tensor pipe (mma.sync) and the exponentials.
+// Measured: 32 single tokens on 8192 cached (271 MB) 98 us, 2.7 TB/s, held by the
+// barriers and row copies of each (256 tokens, head) step; three chunks (145 GFLOP
+// of attention) 368 us with the tensor pipe active a third of the time.
 #include "pkv_kv8_attention.cuh"
 #include "pkv_tcgen05.cuh"
 

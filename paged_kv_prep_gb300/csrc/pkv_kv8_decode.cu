@@ -18,8 +18,14 @@
 // halves (keys, values) it refills as soon as it has taken them out; V comes
 // out as pairs of tokens merged with a byte permute, no transpose; e4m3 turns into f16 exactly on the way into the fragments, and P
 // moves from accumulator to operand layout with movmatrix.
+// The copies go by whole 128-byte pieces of a line: fetched as the fragments
+// want them (16 bytes of four to eight lines an instruction) the kernel stood at
+// 4.3 TB/s with or without its arithmetic.
 // A range that ends inside a request leaves a partial result (R, sum, O) that
 // a second kernel merges in a fixed order.
+// Measured: 256 single tokens on contexts up to 8192 (2.1 GB, floor 312 us) 381 to
+// 399 us with the merge, 5.3 to 5.5 TB/s; the kernel alone 5.45 TB/s, 80 % of the
+// measured copy rate.  Without its arithmetic it reaches 5.7 TB/s.
 #include "pkv_kv8_attention.cuh"
 
 namespace pkv {

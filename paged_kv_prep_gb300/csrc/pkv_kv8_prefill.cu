@@ -23,6 +23,14 @@
 // split evenly over the CTAs; a row tile that is cut leaves partial results
 // for a merge in a fixed order.
 //
+// Measured: 913 GFLOP of chunks (2 x 2048 tokens, 4 heads a group, contexts up to
+// 16384) 810 us, 1.13 PFLOP/s, 59 % of the measured rate, the tensor pipe active
+// 47 % of the time.  A unit takes about 4150 cycles against 2048 of products: the
+// way from a tile's scores through its softmax (2100 cycles at two warps a
+// scheduler) and back into its next scores is longer than the other tile's
+// products.  Not kept: a second issuing warp (1020 us), eight converting warps
+// (990 us, registers), bodies unrolled over a unit (instruction cache, 2 x slower).
+//
 // Every wait has a limit; one that runs out sets PKV_DEVERR_TIMEOUT, the other
 // waits give up after it, and the CTA drains its products and frees its TMEM.
 #include "pkv_kv8_attention.cuh"

@@ -328,6 +328,15 @@ def test_cache_past_32_bits():
     assert float(w.sum()) == pytest.approx(4 * heads * group, rel=1e-4)
 
 
+def test_thousands_of_requests():
+    """More requests than a CTA has threads: the plan's chunks hold several."""
+    gen = torch.Generator().manual_seed(2)
+    lens = torch.randint(0, 8, (3000,), generator=gen).tolist()
+    reqs = [(int(torch.randint(0, x + 1, (1,), generator=gen)) if x else 0, x) for x in lens]
+    check(Case(reqs, 16, 1, 3, 64, seed=15))
+    check(Case([(1, max(x, 1)) for x in lens] + [(40, 50)], 16, 1, 2, 64, seed=16))
+
+
 def test_no_tokens():
     case = Case([(1, 5)], 16, 1, 1, 64)
     q, kc, vc, ks, vs, tab, qsl, lens = case.args()
