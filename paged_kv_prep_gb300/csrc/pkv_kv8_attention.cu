@@ -39,7 +39,7 @@ constexpr int kPrefillRows = 32;
 constexpr int kWWarps = 8, kWThreads = 32 * kWWarps, kWStages = 3;
 constexpr uint32_t kNone = 0xffffffffu;                       // no slot: slots fit 32 bits with room
 template <int D, int kT>
-constexpr int kWRows = D > 128 ? 32 : kT == 1 ? 128 : 64;     // rows of a chunk
+constexpr int kWRows = kT == 1 ? (D > 128 ? 32 : 128) : (D > 128 ? 16 : 32);   // rows of a chunk
 
 template <int D, int kT>
 struct WeightsShape {
@@ -51,13 +51,13 @@ struct WeightsShape {
 template <int D, int kT>
 struct WeightsSmem {
     static constexpr int kTokens = WeightsShape<D, kT>::kTokens;
-    alignas(16) char k[kTokens * D];
+    alignas(16) char k[2][kTokens * D];                       // this head's codes, the next one's
     alignas(16) char q[kWStages][kWRows<D, kT> * D * 2];                         // packed rows
     alignas(16) float2 fac[kWStages][kWRows<D, kT> + 2];                            // factor of S, -lse (both for base 2)
     uint64_t full[kWStages], free[kWStages];
     int32_t block[2][kTokens];                                // by unit parity; -1: not read
     uint32_t slot[2][kTokens];
-    float ks[kTokens];
+    float ks[2][kTokens];
     float sum[kWWarps][WeightsShape<D, kT>::kGroup];
     float total[2][kTokens];                                  // by unit parity: this CTA's heads
     int64_t prefix[kWThreads + 1];
@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
         }
     };
     // the codes and scales of one head
-    auto fetch = [&](const Unit &x, int parity, int head) {
+    auto fetch = [&](const Unit &x, int parity, int head, int place) {
         constexpr int kRowLanes = D / 16, kStep = kWThreads / kRowLanes;
         const int piece = tid % kRowLanes;
 #pragma unroll
@@ -199,13 +199,13 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
             const int tok = i * kStep + tid / kRowLanes;
             if (tok < kTokens) {
                 const uint32_t slot = sm.slot[parity][tok];
-                cp_async<16>(smem_addr(sm.k + tok * D + 16 * swizzle<D>(piece, tok)),
+                cp_async<16>(smem_addr(sm.k[place] + tok * D + 16 * swizzle<D>(piece, tok)),
                              p.kc + (slot != kNone ? slot * line + head * D + 16 * piece : 0), slot != kNone);
             }
         }
         if (tid < kTokens) {
             const int b = sm.block[parity][tid];
-            cp_async<4>(smem_addr(&sm.ks[tid]), p.ks + (b >= 0 ? static_cast<int64_t>(b) * p.Hkv + head : 0), b >= 0);
+            cp_async<4>(smem_addr(&sm.ks[place][tid]), p.ks + (b >= 0 ? static_cast<int64_t>(b) * p.Hkv + head : 0), b >= 0);
         }
         cp_commit();
     };
@@ -255,10 +255,10 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
     feed.count = 0;
     if (rank >= p.Hkv) feed.u = end;
     int parity = 0;
-    uint32_t chunk = 0;
+    uint32_t chunk = 0, step_no = 0;
     find_blocks(x, parity);
     __syncthreads();
-    if (rank < p.Hkv) fetch(x, parity, rank);
+    if (rank < p.Hkv) fetch(x, parity, rank, 0);
     if (tid == 0) {
         ask_rows();
         ask_rows();
@@ -274,8 +274,14 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
 #pragma unroll
         for (int k = 0; k < kSubs; k++) acc[k][0] = acc[k][1] = 0.f;
         for (int head = rank; head < p.Hkv; head += mates) {
+            // this head's codes are here, and everyone has left the place of the head before: the next
+            // head's are on their way for a whole step
             cp_wait<0>();
             __syncthreads();
+            const int place = step_no++ & 1;
+            const bool last = head + mates >= p.Hkv;
+            if (!last) fetch(x, parity, head + mates, place ^ 1);
+            else if (more) fetch(y, parity ^ 1, rank, place ^ 1);
             uint32_t kf[kSubs][S][4];
             float ks[kSubs][2];
 #pragma unroll
@@ -283,10 +289,10 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
 #pragma unroll
                 for (int h = 0; h < 2; h++) {
                     const int tok = group * kGroup + 16 * k + g + 8 * h;
-                    ks[k][h] = sm.ks[tok];
+                    ks[k][h] = sm.ks[place][tok];
 #pragma unroll
                     for (int c = 0; c < D / 64; c++) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(sm.k + tok * D + 16 * swizzle<D>(4 * c + t, tok));
+                        const uint4 v = *reinterpret_cast<const uint4 *>(sm.k[place] + tok * D + 16 * swizzle<D>(4 * c + t, tok));
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
@@ -295,10 +301,6 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
                         }
                     }
                 }
-            __syncthreads();
-            const bool last = head + mates >= p.Hkv;
-            if (!last) fetch(x, parity, head + mates);
-            else if (more) fetch(y, parity ^ 1, rank);
             const int back = x.r.len - x.r.count;
             const int64_t row0 = (static_cast<int64_t>(head) * p.T + x.r.start) * p.G;
             for (int f = x.f0; f < x.f1; f += kWRows<D, kT>, chunk++) {
@@ -329,14 +331,13 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
                     }
                     const float2 fa = sm.fac[stage][odd + 8 * nt + 2 * t], fb = sm.fac[stage][odd + 8 * nt + 2 * t + 1];
                     const int first = f + 8 * nt;
-                    const bool whole = chunk_whole && first + 8 <= x.f1;
                     float v[kSubs][4];
 #pragma unroll
                     for (int k = 0; k < kSubs; k++)
 #pragma unroll
                         for (int q = 0; q < 4; q++)
                             v[k][q] = exp2_fast(fmaf(c[k][q], (q & 1 ? fb.x : fa.x) * ks[k][q >> 1], q & 1 ? fb.y : fa.y));
-                    if (!whole) {
+                    if (!chunk_whole) {
                         const int r0 = first + 2 * t;
                         const int pa = r0 < x.f1 ? back + r0 / p.G : -1, pb = r0 + 1 < x.f1 ? back + (r0 + 1) / p.G : -1;
 #pragma unroll
@@ -348,6 +349,12 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
                                 const bool ok = s <= pos && s >= lo_of(p, pos) && (q & 1 ? fb.y : fa.y) != INFINITY;
                                 if (!ok) v[k][q] = 0.f;
                             }
+                    } else if (first + 8 > x.f1) {
+#pragma unroll
+                        for (int k = 0; k < kSubs; k++)
+#pragma unroll
+                            for (int q = 0; q < 4; q++)
+                                if (first + 2 * t + (q & 1) >= x.f1) v[k][q] = 0.f;
                     }
 #pragma unroll
                     for (int k = 0; k < kSubs; k++)
@@ -398,7 +405,7 @@ int64_t workspace_of(int32_t head_dim, int sms) {
 template <int D, int kT>
 int launch_weights_as(const AttnParams &p, const Packed &packed, int mates, int sms, cudaStream_t s) {
     constexpr int smem = static_cast<int>(sizeof(WeightsSmem<D, kT>));
-    static_assert(smem <= 110 * 1024, "two CTAs an SM");
+    static_assert(smem <= 113 * 1024, "two CTAs an SM");
     static bool set[64] = {false};
     const int rc = kv8_allow_smem(reinterpret_cast<const void *>(kv8_weights_kernel<D, kT>), smem, set);
     if (rc != PKV_OK) return rc;
