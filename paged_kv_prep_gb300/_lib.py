@@ -920,13 +920,23 @@ def kv8_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, d_error=No
     return rc
 
 
+_KV8_WORKSPACE = {}      # bytes by the sizes they depend on
+
+
 def kv8_attention_workspace(num_tokens, num_q_heads, head_dim, with_weights=False):
     """Bytes of device workspace an attention call takes (``pkv_kv8_attention_workspace``)."""
+    # without weights the size does not depend on the number of tokens
+    key = (num_tokens if with_weights else 0, num_q_heads, head_dim, bool(with_weights))
+    found = _KV8_WORKSPACE.get(key)
+    if found is not None:
+        return found
     n = C.c_int64(0)
     rc = lib().pkv_kv8_attention_workspace(int(num_tokens), int(num_q_heads), int(head_dim),
                                            int(bool(with_weights)), C.byref(n))
     if rc != OK:
         raise PkvError(rc, "pkv_kv8_attention_workspace")
+    if not with_weights:
+        _KV8_WORKSPACE[key] = n.value
     return n.value
 
 

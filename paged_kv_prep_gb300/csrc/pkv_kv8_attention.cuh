@@ -27,6 +27,7 @@ struct AttnParams {
     int32_t window;
     int32_t fp16;
     float scale_log2;              // softmax_scale * log2(e)
+    int32_t whole;                 // decode kernel: row tiles are not cut (no merge follows)
     int32_t short_rows;            // requests with more (query, head) rows than this take the prefill kernel
     float *part;                   // partial results, see pkv_kv8_decode.cu
     int4 *meta;

@@ -484,14 +484,14 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto units = [&](int i) {
+    // what the ranges are cut from: a request's units, or its row tiles
+    auto share = [&](const Req &r) {
         int per;
-        return units_of_request<NT>(p, request_of(p, i), &per);
+        const int64_t k = units_of_request<NT>(p, r, &per);
+        return p.whole ? k / per : k;
     };
-    const int64_t total = plan_prefix<kThreads>(s_prefix, s_warp, p.n, [&](int i) {
-        int per;
-        return units_of_request<NT>(p, request_of(p, i, blockIdx.x == 0), &per);
-    });
+    auto units = [&](int i) { return share(request_of(p, i)); };
+    const int64_t total = plan_prefix<kThreads>(s_prefix, s_warp, p.n, [&](int i) { return share(request_of(p, i, blockIdx.x == 0)); });
     const int worker = blockIdx.x * kWarps + warp;
     const int64_t all = static_cast<int64_t>(gridDim.x) * kWarps / p.Hkv;     // ranges the batch is cut into
     const int64_t ranges = total < all ? total : all;
@@ -506,16 +506,18 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
         while (u < end) {
             const Req r = request_of(p, i);
             int per;
-            const int64_t k = units_of_request<NT>(p, r, &per);
+            const int64_t all_units = units_of_request<NT>(p, r, &per);
+            const int64_t k = p.whole ? all_units / per : all_units;
             if (u >= first + k) {
                 first += k;
                 i++;
                 continue;
             }
-            const int rt = static_cast<int>((u - first) / per);
-            const int64_t tile = first + static_cast<int64_t>(rt) * per;      // the tile's first unit
-            const int ua = static_cast<int>(u - tile);
-            const int ub = static_cast<int>(end - tile < per ? end - tile : per);
+            const int cut = p.whole ? 1 : per;                                // shares of a row tile
+            const int rt = static_cast<int>((u - first) / cut);
+            const int64_t tile = first + static_cast<int64_t>(rt) * cut;      // the tile's first share
+            const int ua = p.whole ? 0 : static_cast<int>(u - tile);
+            const int ub = p.whole ? per : static_cast<int>(end - tile < per ? end - tile : per);
             Tile<D, NT, kGrouped> x;
             x.run(p, r, p.tables + static_cast<int64_t>(i) * p.W, head, rt, ua, ub, ring);
             if (ua == 0 && ub == per) {
@@ -528,7 +530,7 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
                     note = make_int4(i, rt, static_cast<int>(last - range) + 1, head);
                 }
             }
-            u = tile + ub;
+            u = p.whole ? u + 1 : tile + ub;
         }
     }
     if (lane == 0) p.meta[worker] = note;
@@ -622,7 +624,7 @@ int launch(const AttnParams &p, int sms, cudaStream_t s) {
     const int64_t most = tiles * (static_cast<int64_t>(p.W) * p.bs / kUnit + 2) * p.Hkv;
     const int grid = most < static_cast<int64_t>(sms) * kWarps ? static_cast<int>((most + kWarps - 1) / kWarps) : sms;
     PKV_CUDA_TRY(launch_pdl(kv8_decode_kernel<D, NT, kGrouped>, dim3(grid), dim3(32 * kWarps), smem, s, p));
-    return kv8_launch_merge(p, D, 8 * NT, grid * kWarps, p.Hkv, s);
+    return p.whole ? PKV_OK : kv8_launch_merge(p, D, 8 * NT, grid * kWarps, p.Hkv, s);
 }
 
 template <int D>

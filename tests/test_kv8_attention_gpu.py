@@ -337,6 +337,15 @@ def test_thousands_of_requests():
     check(Case([(1, max(x, 1)) for x in lens] + [(40, 50)], 16, 1, 2, 64, seed=16))
 
 
+def test_many_short_requests_are_not_cut():
+    """Short tables and many tiles: a warp takes a whole row tile."""
+    gen = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 250, (60,), generator=gen).tolist()
+    check(Case([(1, x) for x in lens], 16, 8, 4, 64, seed=17))
+    check(Case([(1 + x % 3, x) for x in lens] + [(30, 100)], 16, 8, 4, 64, seed=18), window=100)
+    check(Case([(1, x) for x in lens[:20]], 24, 16, 1, 64, seed=19))
+
+
 def test_no_tokens():
     case = Case([(1, 5)], 16, 1, 1, 64)
     q, kc, vc, ks, vs, tab, qsl, lens = case.args()
