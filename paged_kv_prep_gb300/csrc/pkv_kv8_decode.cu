@@ -539,8 +539,9 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
 // Merge the partial results of the tiles that were cut, a warp per (worker, row).
 constexpr int kMergeThreads = 256;
 
-// kBatch: partial rows on their way at a time (sixteen for the long chains of a few decodes; two
-// pieces are the rule for row tiles of chunks, whose thousands of rows want more warps resident).
+// kBatch: partial rows on their way at a time.  Sixteen for the long chains of a few decodes (four long
+// ones 135 us, with eight 140), eight for a full batch (256 decodes 372 us, with sixteen 382: fewer
+// warps resident), two for the thousands of rows of row tiles, mostly of two pieces.
 template <int D, int kBatch>
 __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnParams p, int rows, int workers, int stride) {
     constexpr int kPer = D / 32;
@@ -637,10 +638,11 @@ int launch_rows(const AttnParams &p, bool one_tile, int sms, cudaStream_t s) {
 
 int kv8_launch_merge(const AttnParams &p, int32_t head_dim, int rows, int workers, int stride, cudaStream_t s) {
     const dim3 grid((static_cast<unsigned>(workers) * rows + kMergeThreads / 32 - 1) / (kMergeThreads / 32)), block(kMergeThreads);
-    const bool tile = rows > 16;
-    auto kernel = head_dim == 64 ? (tile ? kv8_merge_kernel<64, 2> : kv8_merge_kernel<64, 16>)
-                  : head_dim == 128 ? (tile ? kv8_merge_kernel<128, 2> : kv8_merge_kernel<128, 16>)
-                                    : kv8_merge_kernel<256, 16>;
+    const int64_t tiles = (static_cast<int64_t>(p.T) * p.G / rows + p.n) * p.Hkv;
+    const bool tile = rows > 16, chains = tiles * 8 <= workers;
+    auto kernel = head_dim == 64    ? (tile ? kv8_merge_kernel<64, 2> : chains ? kv8_merge_kernel<64, 16> : kv8_merge_kernel<64, 8>)
+                  : head_dim == 128 ? (tile ? kv8_merge_kernel<128, 2> : chains ? kv8_merge_kernel<128, 16> : kv8_merge_kernel<128, 8>)
+                                    : kv8_merge_kernel<256, 8>;
     PKV_CUDA_TRY(launch_pdl(kernel, grid, block, 0, s, p, rows, workers, stride));
     return PKV_OK;
 }
