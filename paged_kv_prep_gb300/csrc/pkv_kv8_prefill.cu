@@ -6,7 +6,7 @@
 // log2(v_scale), both constant over 16 tokens; w = 2^(x - R) goes into the
 // second product as f16, the softmax sum adds w / v_scale in fp32.  R is the
 // row's maximum over its first unit and then follows lazily: it moves only
-// when the sum of 32 w, which is needed anyway, exceeds 2^14.  So later units
+// when the sum of 64 w, which is needed anyway, exceeds 2^14.  So later units
 // take no pass for the maximum, the accumulator is hardly ever rescaled, and w
 // stays inside f16's range with all its bits.
 //
@@ -49,7 +49,7 @@ constexpr int kSoftRegs = 176, kConvRegs = 104, kIssueRegs = 56;
 static_assert(32 * (kSoftWarps * kSoftRegs + kConvWarps * kConvRegs + 4 * kIssueRegs) <= 65536, "registers");
 static_assert((kThreads + 1 + kThreads / 32) * 8 <= 2 * kKeys * 64, "the plan's sums lie in the raw codes' place");
 constexpr uint32_t kTries = 1u << 22;   // polls before a wait gives up (half a second or more)
-constexpr float kMostSum = 16384.f;     // sum of 32 w that makes R follow the row's maximum
+constexpr float kMostSum = 16384.f;     // sum of 64 w that makes R follow the row's maximum
 
 template <int D>
 struct Smem {
@@ -57,7 +57,7 @@ struct Smem {
     char k[2][kKeys * D * 2];
     char v[2][kKeys * D * 2];
     char raw[2][kKeys * D];             // codes of the unit that is converted next: keys, values
-    float ks[4][kSub], lv[4][kSub], iv[4][kSub];   // per 16 tokens: k_scale, log2(v_scale), 1 / v_scale
+    alignas(16) float ks[4][kSub], lv[4][kSub], iv[4][kSub];   // per 16 tokens: k_scale, log2(v_scale), 1 / v_scale
     uint64_t q_full[2], k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2], o_full[2], done;
     uint32_t tmem;
     int32_t failed;
@@ -262,49 +262,38 @@ __device__ __forceinline__ void grow_rows(const Smem<D> *sm, int c, uint32_t ts,
     }
 }
 
-// Columns 32 c .. + 31 of a unit: weights in the place of S (32 columns of scores become 16 of packed
-// f16).  False, with nothing written, where a row's weights outgrow its reference.
-template <int D>
-__device__ __forceinline__ bool columns32(const Smem<D> *sm, uint32_t (&s)[32], int c, uint32_t ts, int ring, float cf, float ref,
-                                          float &sum, bool whole, int lo, int hi) {
-    uint32_t w[16];
-    const float2 a = factors(cf, *reinterpret_cast<const float2 *>(&sm->ks[ring][2 * c]));
-    const float2 lv = *reinterpret_cast<const float2 *>(&sm->lv[ring][2 * c]);
-    const float2 iv = *reinterpret_cast<const float2 *>(&sm->iv[ring][2 * c]);
-    if (!whole) hide(s, lo - 32 * c, hi - 32 * c);
-    const float2 part = weights32(s, w, a, make_float2(lv.x - ref, lv.y - ref));
-    if (__any_sync(~0u, part.x + part.y > kMostSum)) return false;
-    sum = fmaf(part.x, iv.x, fmaf(part.y, iv.y, sum));
-    tmem_st16(ts + 16 * c, w);
-    return true;
-}
-
-// All of a unit's columns; the next 32 are on their way while 32 are worked on.  The loop is not
-// unrolled further: the body of a whole unit would not stay in the instruction cache beside the
-// other warps' code.
+// All of a unit's columns, 64 at a time: their exponentials, sums and packing are one block of
+// independent work, which hides its own latencies (a call of chunks and decodes 1704 us, one under a
+// window 771; 32 columns at a time, the next on their way, 1711 and 776).  Weights stand in the place
+// of S (32 columns of scores become 16 of packed f16).  The loop is not unrolled: the body of a whole
+// unit would not stay in the instruction cache beside the other warps' code.
 template <int D>
 __device__ __forceinline__ void row_weights(const Smem<D> *sm, uint32_t ts, uint32_t to, int o_cols, int ring, float cf,
                                             float &top, float &sum, bool whole, int lo, int hi) {
     const float ref = top == -INFINITY ? 0.f : top;
-    uint32_t s0[32], s1[32];
-    tmem_ld32(s0, ts);
     int c = 0;
 #pragma unroll 1
     for (; c < 4; c += 2) {
-        tc_wait_ld();
+        uint32_t s0[32], s1[32], w0[16], w1[16];
+        tmem_ld32(s0, ts + 32 * c);
         tmem_ld32(s1, ts + 32 * (c + 1));
-        if (!columns32<D>(sm, s0, c, ts, ring, cf, ref, sum, whole, lo, hi)) break;
+        const float4 ks = *reinterpret_cast<const float4 *>(&sm->ks[ring][2 * c]);
+        const float4 lv = *reinterpret_cast<const float4 *>(&sm->lv[ring][2 * c]);
+        const float4 iv = *reinterpret_cast<const float4 *>(&sm->iv[ring][2 * c]);
+        const float2 a0 = factors(cf, make_float2(ks.x, ks.y)), a1 = factors(cf, make_float2(ks.z, ks.w));
         tc_wait_ld();
-        if (c == 0) tmem_ld32(s0, ts + 64);
-        if (!columns32<D>(sm, s1, c + 1, ts, ring, cf, ref, sum, whole, lo, hi)) {
-            c++;
-            break;
+        if (!whole) {
+            hide(s0, lo - 32 * c, hi - 32 * c);
+            hide(s1, lo - 32 * c - 32, hi - 32 * c - 32);
         }
+        const float2 p0 = weights32(s0, w0, a0, make_float2(lv.x - ref, lv.y - ref));
+        const float2 p1 = weights32(s1, w1, a1, make_float2(lv.z - ref, lv.w - ref));
+        if (__any_sync(~0u, (p0.x + p0.y) + (p1.x + p1.y) > kMostSum)) break;
+        sum += fmaf(p0.x, iv.x, p0.y * iv.y) + fmaf(p1.x, iv.z, p1.y * iv.w);
+        tmem_st16(ts + 16 * c, w0);
+        tmem_st16(ts + 16 * (c + 1), w1);
     }
-    if (c < 4) {
-        tc_wait_ld();
-        grow_rows<D>(sm, c, ts, to, o_cols, ring, cf, top, sum, lo, hi);
-    }
+    if (c < 4) grow_rows<D>(sm, c, ts, to, o_cols, ring, cf, top, sum, lo, hi);
 }
 
 // ---- softmax warps: a thread per row ----------------------------------------------------------
