@@ -12,16 +12,18 @@
 // behind one another.  A CTA owns kT token groups of 32 of a request and walks
 // the KV heads: a head's codes come by cp.async while the head before is worked
 // on, become f16 fragments in registers once, and meet the request's rows in
-// chunks that bulk copies bring two chunks ahead.  With kT = 8 (single tokens: few rows) a warp per group; with kT = 1
-// (chunks: many rows) the warps share a group's rows and a cluster shares the
-// KV heads, so that the tokens that thousands of rows see do not hold the
-// launch up; the sums meet in a fixed order.
+// chunks that bulk copies bring two chunks ahead.  With kT = 8 (single tokens: few
+// rows) a warp per group; with kT = 4 (chunks: many rows) two warps share a group's
+// rows and a cluster shares the KV heads, so that the tokens that thousands of rows
+// see do not hold the launch up; the sums meet in a fixed order.
 //
 // Bound: for single tokens HBM (D bytes of K per token and KV head, the second
 // read of K), for chunks the tensor pipe (mma.sync) and the exponentials.
-// Measured: 32 single tokens on 8192 cached (271 MB) 98 us, 2.7 TB/s, held by the
+// Measured: 32 single tokens on 8192 cached (271 MB) 76 us, 3.6 TB/s, held by the
 // barriers and row copies of each (256 tokens, head) step; three chunks (145 GFLOP
-// of attention) 368 us with the tensor pipe active a third of the time.
+// of attention) 267 us with the tensor pipe active 46 % of the time.  Chunks with
+// kT = 1 and 128 rows a chunk 291 us, kT = 2 and 96 rows 286 (a row is fetched by
+// four or two times as many CTAs); rows shared out over the cluster as well 278.
 #include "pkv_kv8_attention.cuh"
 #include "pkv_tcgen05.cuh"
 
@@ -39,7 +41,7 @@ constexpr int kPrefillRows = 32;
 constexpr int kWWarps = 8, kWThreads = 32 * kWWarps, kWStages = 3;
 constexpr uint32_t kNone = 0xffffffffu;                       // no slot: slots fit 32 bits with room
 template <int D, int kT>
-constexpr int kWRows = kT == 1 ? (D > 128 ? 32 : 128) : (D > 128 ? 16 : 32);   // rows of a chunk
+constexpr int kWRows = kT < 8 ? (D > 128 ? 32 : 64) : (D > 128 ? 16 : 32);   // rows of a chunk
 
 template <int D, int kT>
 struct WeightsShape {
@@ -148,7 +150,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
     if (range >= ranges) return;
     // Single tokens: a stretch of units each, all alike.  Chunks: every ranges-th unit, since the tokens
     // at a chunk's front are seen by more rows than those at its end.
-    constexpr bool kStretch = kT > 1;
+    constexpr bool kStretch = kT == 8;
     const int64_t step = kStretch ? 1 : ranges, end = kStretch ? (range + 1) * total / ranges : total;
     int64_t u = kStretch ? range * total / ranges : range;
 
@@ -302,6 +304,10 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
                     }
                 }
             const int back = x.r.len - x.r.count;
+            // rows whose position is at least the tile's last token and whose window reaches its first
+            const auto rows_to = [&](int64_t j) { return static_cast<int>(min(max(j, int64_t{0}) * p.G, int64_t{0x7fffffff})); };
+            const int whole0 = rows_to(static_cast<int64_t>(x.s0) + kTokens - 1 - back);
+            const int whole1 = p.window > 0 ? rows_to(static_cast<int64_t>(x.s0) + p.window - back) : 0x7fffffff;
             const int64_t row0 = (static_cast<int64_t>(head) * p.T + x.r.start) * p.G;
             for (int f = x.f0; f < x.f1; f += kWRows<D, kT>, chunk++) {
                 if (tid == 0) ask_rows();
@@ -310,10 +316,46 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
                 const int odd = static_cast<int>((row0 + f) & 1);
                 // every row of the chunk sees every token of the tile (tokens that are not read do not count:
                 // their sums are dropped)
-                const int p0 = back + f / p.G, p1 = back + (min(f + kWRows<D, kT>, x.f1) - 1) / p.G;
-                const bool chunk_whole = x.s0 + kTokens - 1 <= p0 && (p.window <= 0 || x.s0 > p1 - p.window);
+                const bool chunk_whole = f >= whole0 && min(f + kWRows<D, kT>, x.f1) <= whole1;
+                int nt = team;
+                if constexpr (kT < 8) {
+                    // two tiles of rows at a time where nothing is masked: twice the independent products (three
+                    // chunks 326 us, a tile at a time 375)
 #pragma unroll 1
-                for (int nt = team; nt < kWRows<D, kT> / 8; nt += kTeams) {
+                    for (; chunk_whole && nt + kTeams < kWRows<D, kT> / 8 && f + 8 * (nt + kTeams) + 8 <= x.f1; nt += 2 * kTeams) {
+                        float c[2][kSubs][4];
+#pragma unroll
+                        for (int w = 0; w < 2; w++)
+#pragma unroll
+                            for (int k = 0; k < kSubs; k++) c[w][k][0] = c[w][k][1] = c[w][k][2] = c[w][k][3] = 0.f;
+                        const char *row = sm.q[stage] + (8 * nt + g) * (2 * D);
+                        const int flip = ((g + odd) & 1) << 2;
+#pragma unroll
+                        for (int j = 0; j < S; j += 2) {
+#pragma unroll
+                            for (int w = 0; w < 2; w++) {
+                                const uint4 b = *reinterpret_cast<const uint4 *>(row + w * (8 * kTeams * 2 * D) + 16 * ((2 * j + t) ^ flip));
+#pragma unroll
+                                for (int k = 0; k < kSubs; k++) mma_f16(c[w][k], kf[k][j], b.x, b.y);
+#pragma unroll
+                                for (int k = 0; k < kSubs; k++) mma_f16(c[w][k], kf[k][j + 1], b.z, b.w);
+                            }
+                        }
+#pragma unroll
+                        for (int w = 0; w < 2; w++) {
+                            const float2 fa = sm.fac[stage][odd + 8 * (nt + w * kTeams) + 2 * t];
+                            const float2 fb = sm.fac[stage][odd + 8 * (nt + w * kTeams) + 2 * t + 1];
+#pragma unroll
+                            for (int k = 0; k < kSubs; k++)
+#pragma unroll
+                                for (int h = 0; h < 2; h++)
+                                    acc[k][h] += exp2_fast(fmaf(c[w][k][2 * h], fa.x * ks[k][h], fa.y)) +
+                                                 exp2_fast(fmaf(c[w][k][2 * h + 1], fb.x * ks[k][h], fb.y));
+                        }
+                    }
+                }
+#pragma unroll 1
+                for (; nt < kWRows<D, kT> / 8; nt += kTeams) {
                     if (f + 8 * nt >= x.f1) break;
                     float c[kSubs][4];
 #pragma unroll
@@ -455,10 +497,10 @@ int launch_weights(const AttnParams &p, char *workspace, int32_t head_dim, int s
     const bool single = p.T <= p.n;
     const int mates = single || p.Hkv < 2 ? 1 : p.Hkv < 4 ? 2 : p.Hkv < 8 ? 4 : 8;
     if (head_dim == 64)
-        return single ? launch_weights_as<64, 8>(p, packed, mates, sms, s) : launch_weights_as<64, 1>(p, packed, mates, sms, s);
+        return single ? launch_weights_as<64, 8>(p, packed, mates, sms, s) : launch_weights_as<64, 4>(p, packed, mates, sms, s);
     if (head_dim == 128)
-        return single ? launch_weights_as<128, 8>(p, packed, mates, sms, s) : launch_weights_as<128, 1>(p, packed, mates, sms, s);
-    return single ? launch_weights_as<256, 8>(p, packed, mates, sms, s) : launch_weights_as<256, 1>(p, packed, mates, sms, s);
+        return single ? launch_weights_as<128, 8>(p, packed, mates, sms, s) : launch_weights_as<128, 4>(p, packed, mates, sms, s);
+    return single ? launch_weights_as<256, 8>(p, packed, mates, sms, s) : launch_weights_as<256, 4>(p, packed, mates, sms, s);
 }
 
 // Bytes of the packed rows and their factors (a pair of factors may be read past the last row).
