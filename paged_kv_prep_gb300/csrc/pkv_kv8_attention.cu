@@ -19,7 +19,7 @@
 //
 // Bound: for single tokens HBM (D bytes of K per token and KV head, the second
 // read of K), for chunks the tensor pipe (mma.sync) and the exponentials.
-// Measured: 32 single tokens on 8192 cached (271 MB) 76 us, 3.6 TB/s, held by the
+// Measured: 32 single tokens on 8192 cached (271 MB) 75 us, 3.6 TB/s, held by the
 // barriers and row copies of each (256 tokens, head) step; three chunks (145 GFLOP
 // of attention) 267 us with the tensor pipe active 46 % of the time.  Chunks with
 // kT = 1 and 128 rows a chunk 291 us, kT = 2 and 96 rows 286 (a row is fetched by

@@ -24,7 +24,7 @@
 // A range that ends inside a request leaves a partial result (R, sum, O) that
 // a second kernel merges in a fixed order.
 // Measured: 256 single tokens on contexts up to 8192 (2.1 GB, floor 312 us) 381 to
-// 399 us with the merge, 5.3 to 5.5 TB/s; the kernel alone 5.45 TB/s, 80 % of the
+// 390 us with the merge, 5.4 to 5.5 TB/s; the kernel alone 5.45 TB/s, 80 % of the
 // measured copy rate.  Without its arithmetic it reaches 5.7 TB/s.
 #include "pkv_kv8_attention.cuh"
 
