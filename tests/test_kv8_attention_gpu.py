@@ -363,6 +363,13 @@ def test_chunks_match_plain(heads, group, d, dtype):
     check(Case(CHUNKS, 16, heads, group, d, dtype, seed=heads * 10 + group))
 
 
+@pytest.mark.parametrize("heads,d,window", [(8, 64, 0), (8, 64, 333), (5, 128, 0), (9, 256, 150)])
+def test_many_chunks_share_out_their_weights(heads, d, window):
+    """More token tiles than clusters: each works through several, of one request and of the next."""
+    reqs = [(3 + 7 * i % 61, 64 + 41 * i % 900) for i in range(60)]
+    check(Case(reqs, 16, heads, 2, d, seed=heads + d), window=window)
+
+
 @pytest.mark.parametrize("window", [1, 17, 100, 128, 1000])
 @pytest.mark.parametrize("bs", [16, 48])
 def test_chunks_with_windows(window, bs):
