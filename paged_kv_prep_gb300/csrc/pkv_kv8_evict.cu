@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kSelThreads) kv8_select_kernel(const EvictPara
     sync_all<kCluster>();                              // nobody leaves while its memory is read
 }
 
-// grid (new blocks per request, requests)
+// grid (new blocks per request, at most the new tables' width; requests)
 constexpr int kCopyHold = 4;                           // 16-byte pieces of K (and of V) that a thread holds
 
 __global__ void __launch_bounds__(kCopyThreads, 4) kv8_copy_kernel(const EvictParams p, int chunk_shift, int head_shift) {
@@ -400,11 +400,15 @@ extern "C" int pkv_kv8_evict(const pkv_kv8_cache *cache, float *weights,
     // 8192 tokens take 16 us with a CTA each.
     rc = static_cast<int64_t>(p.W) * p.bs > kSelCap ? launch_select<8>(p, n, s) : launch_select<1>(p, n, s);
     if (rc != PKV_OK) return rc;
-    const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(budget) + p.bs - 1) / p.bs);
+    // No request fills more blocks than the budget needs, than its new table names or than its old one
+    // named; with that the copy's reads of new_block_tables stay in their row.
+    int64_t blocks = (static_cast<int64_t>(budget) + p.bs - 1) / p.bs;
+    blocks = blocks < p.W2 ? blocks : p.W2;
+    blocks = blocks < p.W ? blocks : p.W;
     const int chunks = p.line / 16;
     const int chunk_shift = (chunks & (chunks - 1)) ? -1 : 31 - __builtin_clz(static_cast<unsigned>(chunks));
     const int head_shift = cache->head_dim == 64 ? 2 : cache->head_dim == 128 ? 3 : 4;
-    PKV_CUDA_TRY(pkv::launch_pdl(kv8_copy_kernel, dim3(blocks, n), dim3(kCopyThreads), 2 * p.heads * sizeof(float), s, p,
+    PKV_CUDA_TRY(pkv::launch_pdl(kv8_copy_kernel, dim3(static_cast<unsigned>(blocks), n), dim3(kCopyThreads), 2 * p.heads * sizeof(float), s, p,
                                  chunk_shift, head_shift));
     return PKV_OK;
 }

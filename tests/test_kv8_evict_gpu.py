@@ -151,3 +151,62 @@ def test_no_requests():
     dev = [x.cuda() for x in state]
     new, kept = pkv.kv8_evict(*dev, table[:0].cuda(), torch.zeros(0, dtype=torch.int32).cuda(), fresh[:0].cuda(), 8)
     assert new.numel() == 0 and kept.shape == (0, 8)
+
+
+def narrow(lens, bs, heads, d, budget, wide, seed):
+    """New tables that hold `budget` tokens, as rows of a larger tensor, for calls with the larger budget `wide`."""
+    state, table, fresh = make(lens, bs, heads, d, budget, seed)
+    whole = torch.full((len(lens) * fresh.shape[1] + wide // bs + 1,), 2 ** 31 - 1, dtype=torch.int32)
+    whole[:fresh.numel()] = fresh.view(-1)
+    return state, table, fresh, whole.cuda()[:fresh.numel()].view(fresh.shape)
+
+
+def test_new_tables_narrower_than_the_budget():
+    """What fits the new table goes through; a request that does not is refused with its reason."""
+    lens, bs, heads, d, wide = [20, 100, 32, 0, 33], 16, 2, 64, 4096
+    state, table, fresh, given = narrow(lens, bs, heads, d, 32, wide, 8)
+    dev = [x.cuda() for x in state]
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    new, kept = pkv.kv8_evict(*dev, table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), given, wide,
+                              keep_first=2, keep_last=3, d_error=word.data_ptr())
+    assert new.tolist() == [20, -1, 32, 0, -1] and word.item() == pkv.DEVERR_POSITION
+    kc, vc, ks, vs, w = state
+    fits = [0, 2, 3]
+    _, want = ref.evict(kc.view(-1, heads, d), vc.view(-1, heads, d), ks, vs, w, table[fits], [lens[i] for i in fits],
+                        fresh[fits], wide, 2, 3)
+    assert torch.equal(kept.cpu()[fits], want) and int(kept[[1, 4]].max()) == -1
+    assert ref.same_codes(dev[0].cpu(), kc) and ref.same_codes(dev[1].cpu(), vc)
+    assert torch.equal(dev[2].cpu(), ks) and torch.equal(dev[3].cpu(), vs) and torch.equal(dev[4].cpu(), w)
+
+
+@pytest.mark.parametrize("lens,fits,wide", [([20, 32], 32, 4096), ([20, 5], 32, 1 << 20), ([9, 12], 64, 64)])
+def test_the_copy_starts_no_block_past_a_table(lens, fits, wide):
+    """The launches of a call, captured and looked at but not run: a CTA per block of the new tables, and no
+    more of them than either table is wide."""
+    import ctypes as C
+    cuda = C.CDLL("libcuda.so.1")
+
+    class Node(C.Structure):                                 # a kernel node's parameters
+        _fields_ = [("func", C.c_void_p), ("grid", C.c_uint * 3), ("block", C.c_uint * 3), ("shared", C.c_uint),
+                    ("params", C.c_void_p), ("extra", C.c_void_p), ("kern", C.c_void_p), ("ctx", C.c_void_p)]
+
+    state, table, fresh, given = narrow(lens, 16, 2, 64, fits, wide, 9)
+    dev, tab, ln = [x.cuda() for x in state], table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    new, kept = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(2, wide, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    handle, graph = C.c_void_p(side.cuda_stream), C.c_void_p()
+    assert cuda.cuStreamBeginCapture_v2(handle, 2) == 0
+    pkv.kv8_evict(*dev, tab, ln, given, wide, new_seq_lens=new, kept=kept, stream=side)
+    assert cuda.cuStreamEndCapture(handle, C.byref(graph)) == 0
+    count = C.c_size_t(8)
+    nodes = (C.c_void_p * 8)()
+    assert cuda.cuGraphGetNodes(graph, nodes, C.byref(count)) == 0
+    grids = []
+    for k in range(count.value):
+        node = Node()
+        assert cuda.cuGraphKernelNodeGetParams_v2(C.c_void_p(nodes[k]), C.byref(node)) == 0
+        grids.append(tuple(node.grid))
+    cuda.cuGraphDestroy(graph)
+    copies = [g for g in grids if g[1] == len(lens)]
+    assert len(copies) == 1 and copies[0][0] <= min(fresh.shape[1], table.shape[1], -(-wide // 16)), grids
