@@ -11,6 +11,7 @@
 namespace pkv {
 
 constexpr float kE4m3Max = 448.f;
+constexpr int kMaxHeads = 1024;     // KV heads of a cache
 constexpr int kMinScaleExp = -64;   // the store's smallest block scale is 2^-64
 
 // Two floats rounded to e4m3 (to nearest even, saturating at 448; NaN stays NaN): `lo` in the
@@ -76,7 +77,7 @@ inline bool kv8_head_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }
 // The cache's own arguments: sizes, pointers, alignment.
 inline int kv8_check_cache(const pkv_kv8_cache *c) {
     if (!c) return PKV_ERR_INVALID_ARG;
-    if (c->num_blocks < 0 || c->block_size < 1 || c->num_heads < 1 || c->num_heads > 1024 ||
+    if (c->num_blocks < 0 || c->block_size < 1 || c->num_heads < 1 || c->num_heads > kMaxHeads ||
         !kv8_head_dim(c->head_dim) || c->num_blocks > 0x7fffffff ||
         c->num_blocks * c->block_size > 0xffffffffLL)    // slots fit 32 bits
         return PKV_ERR_INVALID_ARG;

@@ -581,7 +581,7 @@ int pkv_kv8_attention(const pkv_kv8_cache *cache, const void *q, int64_t q_strid
     p.scale_log2 = softmax_scale * pkv::kLog2e;
     p.short_rows = 0x7fffffff;
     p.meta = static_cast<int4 *>(workspace);
-    p.part = reinterpret_cast<float *>(p.meta + static_cast<int64_t>(sms) * 16);
+    p.part = reinterpret_cast<float *>(p.meta + pkv::kv8_most_workers(sms));
     p.err = d_error;
     cudaStream_t s = pkv::as_stream(stream);
     // The prefill kernel takes the requests with more than kPrefillRows rows.  It needs head_dim <= 128

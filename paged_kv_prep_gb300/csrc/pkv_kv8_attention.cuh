@@ -40,6 +40,14 @@ struct AttnParams {
     }
 };
 
+// Warps that one launch of the decode kernel may have: sixteen an SM, or one for each KV head (rounded up
+// to whole CTAs) where the heads are more than that.
+constexpr int kMaxWarps = 16;
+inline int64_t kv8_most_workers(int sms) {
+    const int64_t a = static_cast<int64_t>(sms) * kMaxWarps, b = kMaxHeads + kMaxWarps;
+    return a > b ? a : b;
+}
+
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 

@@ -620,10 +620,14 @@ int launch(const AttnParams &p, int sms, cudaStream_t s) {
     static bool set[64] = {false};
     const int rc = kv8_allow_smem(reinterpret_cast<const void *>(kv8_decode_kernel<D, NT, kGrouped>), static_cast<int>(smem), set);
     if (rc != PKV_OK) return rc;
-    // one CTA an SM, or as many as the longest requests the tables can name would give a unit a warp
+    static_assert(kWarps <= kMaxWarps, "the workspace holds this many");
+    // One CTA an SM, or as many as the longest requests the tables can name would give a unit a warp; but a
+    // warp for each KV head at least (with head_dim 256 there are more heads than warps from 913 on), or
+    // the batch would have no range.
     const int64_t tiles = static_cast<int64_t>(p.T) * p.G / (8 * NT) + p.n;
     const int64_t most = tiles * (static_cast<int64_t>(p.W) * p.bs / kUnit + 2) * p.Hkv;
-    const int grid = most < static_cast<int64_t>(sms) * kWarps ? static_cast<int>((most + kWarps - 1) / kWarps) : sms;
+    const int least = (p.Hkv + kWarps - 1) / kWarps, full = sms > least ? sms : least;
+    const int grid = most < static_cast<int64_t>(full) * kWarps ? static_cast<int>((most + kWarps - 1) / kWarps) : full;
     PKV_CUDA_TRY(launch_pdl(kv8_decode_kernel<D, NT, kGrouped>, dim3(grid), dim3(32 * kWarps), smem, s, p));
     return p.whole ? PKV_OK : kv8_launch_merge(p, D, 8 * NT, grid * kWarps, p.Hkv, s);
 }
@@ -648,8 +652,8 @@ int kv8_launch_merge(const AttnParams &p, int32_t head_dim, int rows, int worker
 }
 
 int64_t kv8_decode_workspace(int32_t head_dim, int sms) {
-    // the widest variant: 16 workers an SM, two partial results each of 16 rows
-    return static_cast<int64_t>(sms) * 16 * (2LL * 16 * (head_dim + 2) * 4 + 16);
+    // a note and two partial results of 16 rows (the widest variant's) for each warp
+    return kv8_most_workers(sms) * (2LL * 16 * (head_dim + 2) * 4 + 16);
 }
 
 int kv8_launch_decode(const AttnParams &p, int32_t head_dim, bool one_tile, int sms, cudaStream_t s) {

@@ -419,3 +419,15 @@ def test_chunks_repeat_bit_identically():
     for _ in range(5):
         again = pkv.kv8_attention(*a)
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("reqs", [[(1, 5), (1, 3)], [(2, 4), (1, 3)]], ids=["decodes", "mixed"])
+@pytest.mark.parametrize("heads,d", [(912, 256), (913, 256), (1024, 256), (1024, 64)])
+def test_more_heads_than_warps(heads, d, reqs):
+    """Up to the 1024 KV heads that a cache may have: with head_dim 256 more than the SMs hold warps."""
+    case = Case(reqs, 16, heads, 1, d, seed=heads)
+    a = case.args()
+    out, lse = torch.full_like(a[0], 7.0), torch.full(a[0].shape[:2], 7.0, device="cuda")
+    pkv.kv8_attention(*a, out=out, lse=lse)
+    compare(case, out, lse, case.reference(d ** -0.5, 0))
+    check(case)
