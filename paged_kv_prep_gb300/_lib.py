@@ -889,13 +889,19 @@ def _kv8_stream(stream, tensor):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _kv8_made(made, stream, handle):
-    """Tensors made for a call were allocated on the current stream; the work runs on another."""
-    made = [t for t in made if t.is_cuda]
-    if made:
-        other = _kv8_types()[0].cuda.ExternalStream(handle) if isinstance(stream, int) else stream
-        for t in made:
-            t.record_stream(other)
+def _kv8_make(shape, kind, device, stream, handle, returned=True):
+    """A tensor that a call makes.  On another stream than the current one it is allocated there,
+    behind the work that stream already has: a block of the current stream's pool may still be in use
+    by the current stream's queue.  One that is returned is used, and freed, from the current stream."""
+    torch = _kv8_types()[0]
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=kind, device=device)
+    there = torch.cuda.ExternalStream(handle, device=device) if isinstance(stream, int) else stream
+    with torch.cuda.stream(there):
+        made = torch.empty(shape, dtype=kind, device=device)
+    if returned:
+        made.record_stream(torch.cuda.current_stream(device))
+    return made
 
 
 def kv8_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, d_error=None, stream=None,
@@ -963,27 +969,22 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     kind, q_stride = _kv8_dtype(q), _kv8_rows(q, hq * d, "q")
     if weights is not None:
         _kv8_weights(weights, k_cache.shape[0])
-    handle = _kv8_stream(stream, k_cache)
-    made = []
     if out is None:
-        out = torch.empty(shape, dtype=q.dtype, device=q.device)
-        made.append(out)
         out_stride = hq * d * 2
     else:
         if not (out.shape == shape and out.dtype is q.dtype):
             raise ValueError("out has q's shape and type")
         out_stride = _kv8_rows(out, hq * d, "out")
-    if lse is None:
-        lse = torch.empty((T, hq), dtype=f32, device=q.device)
-        made.append(lse)
-    elif not (lse.shape == (T, hq) and lse.dtype is f32 and lse.is_contiguous()):
+    if not (lse is None or lse.shape == (T, hq) and lse.dtype is f32 and lse.is_contiguous()):
         raise ValueError("lse is contiguous float32 [tokens, q_heads]")
+    handle = _kv8_stream(stream, k_cache)
+    if out is None:
+        out = _kv8_make(shape, q.dtype, q.device, stream, handle)
+    if lse is None:
+        lse = _kv8_make((T, hq), f32, q.device, stream, handle)
     if workspace is None:
-        workspace = torch.empty(kv8_attention_workspace(T, hq, d, weights is not None), dtype=torch.uint8,
-                                device=q.device)
-        made.append(workspace)
-    if stream is not None:
-        _kv8_made(made, stream, handle)
+        size = kv8_attention_workspace(T, hq, d, weights is not None)
+        workspace = _kv8_make(size, torch.uint8, q.device, stream, handle, returned=False)
     rc = lib().pkv_kv8_attention(C.byref(cache), q.data_ptr(), q_stride, kind, hq, block_tables.data_ptr(),
                                  table[1], query_start_loc.data_ptr(), seq_lens.data_ptr(), n, T,
                                  d ** -0.5 if softmax_scale is None else float(softmax_scale), int(window),
@@ -1011,18 +1012,13 @@ def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_len
         raise ValueError("block_tables and new_block_tables are [n, width]")
     _kv8_weights(weights, k_cache.shape[0])
     handle = _kv8_stream(stream, k_cache)
-    made = []
     if new_seq_lens is None:
-        new_seq_lens = torch.empty(n, dtype=torch.int32, device=seq_lens.device)
-        made.append(new_seq_lens)
+        new_seq_lens = _kv8_make(n, torch.int32, seq_lens.device, stream, handle)
     if kept is None:
-        kept = torch.empty((n, max(budget, 0)), dtype=torch.int32, device=seq_lens.device)
-        made.append(kept)
+        kept = _kv8_make((n, max(budget, 0)), torch.int32, seq_lens.device, stream, handle)
     _kv8_int32(new_seq_lens, kept)
     if not (new_seq_lens.numel() == n and kept.numel() == n * max(budget, 0)):
         raise ValueError("new_seq_lens [n], kept [n, budget]")
-    if stream is not None:
-        _kv8_made(made, stream, handle)
     rc = lib().pkv_kv8_evict(C.byref(cache), weights.data_ptr(), block_tables.data_ptr(), old[1],
                              seq_lens.data_ptr(), n, new_block_tables.data_ptr(), new[1], budget,
                              int(keep_first), int(keep_last), new_seq_lens.data_ptr(), kept.data_ptr(),

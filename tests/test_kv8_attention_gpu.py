@@ -431,3 +431,61 @@ def test_more_heads_than_warps(heads, d, reqs):
     pkv.kv8_attention(*a, out=out, lse=lse)
     compare(case, out, lse, case.reference(d ** -0.5, 0))
     check(case)
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_what_a_call_makes_is_not_in_use_by_the_current_stream(raw):
+    """Work queued on the current stream still writes to tensors of the sizes that a call on another stream
+    makes, freed before it: the call's outputs and workspace are not theirs, and the call does not wait for
+    that work."""
+    case = Case([(1, 300), (1, 40), (40, 90)], 16, 2, 4, 128, seed=20)
+    a = case.args()
+    T, hq, d = a[0].shape
+    w = torch.zeros(case.blocks * case.bs, device="cuda")
+    want = case.reference(d ** -0.5, 0)
+    side = torch.cuda.Stream()
+    stream = side.cuda_stream if raw else side
+    sizes = [T * hq * d * 2, T * hq * 4, pkv.kv8_attention_workspace(T, hq, d, True)]
+    torch.empty(1, dtype=torch.uint8, device="cuda").fill_(255)
+    torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    pkv.kv8_attention(*a, weights=w, stream=stream)          # kernels are loaded and that stream's pool filled: both may wait
+    torch.cuda.synchronize()
+    done = torch.cuda.Event()
+    theirs = [torch.empty(x, dtype=torch.uint8, device="cuda") for x in sizes]
+    at = {(x.data_ptr(), x.data_ptr() + x.numel()) for x in theirs}
+    torch.cuda._sleep(400_000_000)
+    for x in theirs:
+        x.fill_(255)
+    done.record()
+    del theirs, x
+    out, lse = pkv.kv8_attention(*a, weights=w, stream=stream)
+    side.synchronize()
+    assert not done.query()                                  # the current stream's work is still to come
+    for y in (out, lse):
+        lo, hi = y.data_ptr(), y.data_ptr() + y.numel() * y.itemsize
+        assert all(hi <= p or lo >= q for p, q in at)
+    torch.cuda.synchronize()
+    compare(case, out, lse, want)
+
+
+def test_outputs_freed_early_are_not_handed_out_while_in_use():
+    """Outputs of a call on another stream that the current stream still reads when they are freed: the next
+    call on that stream gets other memory."""
+    case = Case([(1, 300), (40, 90)], 16, 2, 4, 128, seed=21)
+    a = case.args()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out, lse = pkv.kv8_attention(*a, stream=side)
+    side.synchronize()
+    want, at = out.clone(), out.data_ptr()
+    late = out + 0
+    torch.cuda._sleep(1000)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    late = out + 0                                           # queued behind the sleep
+    del out, lse
+    again, _ = pkv.kv8_attention(*a, softmax_scale=0.5, stream=side)
+    assert again.data_ptr() != at
+    torch.cuda.synchronize()
+    assert torch.equal(late, want)
