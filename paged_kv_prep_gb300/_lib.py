@@ -817,7 +817,8 @@ def _kv8_types():
         import torch
 
         _KV8 = (torch, {torch.bfloat16: 0, torch.float16: 1}, torch.float32, torch.int32, torch.int64,
-                getattr(torch._C, "_cuda_getCurrentRawStream", None))
+                getattr(torch._C, "_cuda_getCurrentRawStream", None),
+                getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
     return _KV8
 
 
@@ -829,7 +830,7 @@ def _need(ok, what):
 def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
     """The C view of an 8-bit cache: lines [num_slots, heads * head_dim] of one byte per element
     and scales [num_blocks, heads]."""
-    f32 = _kv8_types()[2]
+    f32 = _kv8_types()[2]       # a call's first use: from here on _KV8 is set
     shape, scales = k_cache.shape, k_scale.shape
     if not (len(scales) == 2 and v_scale.shape == scales and v_cache.shape == shape and len(shape) >= 1):
         raise ValueError("k_cache and v_cache, k_scale and v_scale have the same shapes; scales are [num_blocks, heads]")
@@ -846,7 +847,7 @@ def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
 
 
 def _kv8_int32(*tensors):
-    i32 = _kv8_types()[3]
+    i32 = _KV8[3]
     for t in tensors:
         if not (t.dtype is i32 and t.is_contiguous()):
             raise ValueError("tables, lengths and locations are contiguous int32")
@@ -867,25 +868,41 @@ def _kv8_rows(x, width, what):
 
 
 def _kv8_dtype(x):
-    kind = _kv8_types()[1].get(x.dtype)
+    kind = _KV8[1].get(x.dtype)
     if kind is None:
         raise ValueError("bfloat16 or float16")
     return kind
 
 
 def _kv8_weights(weights, slots):
-    if not (weights.dtype is _kv8_types()[2] and weights.is_contiguous() and weights.numel() == slots):
+    if not (weights.dtype is _KV8[2] and weights.is_contiguous() and weights.numel() == slots):
         raise ValueError("weights is contiguous float32, one for each slot")
 
 
-def _kv8_stream(stream, tensor):
-    """The stream's handle; without one the current stream of the tensor's device (its raw handle
-    where torch gives it: the stream object costs more than the rest of the marshalling)."""
+def _kv8_device(stream, *tensors):
+    """The operands' device: one CUDA device, the stream's too (None: not given)."""
+    device = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("the tensors are on one device")
+    if device < 0:
+        raise ValueError("the tensors are on a CUDA device")
+    if stream is not None and not isinstance(stream, int) and stream.device_index != device:
+        raise ValueError("the stream is of the tensors' device")
+    return device
+
+
+def _kv8_elsewhere(device):
+    """Whether another device than the operands' is the current one, by which the library launches."""
+    return _KV8[6]() != device
+
+
+def _kv8_stream(stream, device):
+    """The stream's handle; without one the device's current stream (its raw handle where torch
+    gives it: the stream object costs more than the rest of the marshalling)."""
     if stream is None:
-        raw = _kv8_types()[5]
-        if raw is not None and tensor.is_cuda:
-            return raw(tensor.get_device())
-        return _stream(None)
+        raw = _KV8[5]
+        return raw(device) if raw is not None else _stream(None)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -893,8 +910,8 @@ def _kv8_make(shape, kind, device, stream, handle, returned=True):
     """A tensor that a call makes.  On another stream than the current one it is allocated there,
     behind the work that stream already has: a block of the current stream's pool may still be in use
     by the current stream's queue.  One that is returned is used, and freed, from the current stream."""
-    torch = _kv8_types()[0]
-    if stream is None or device.type != "cuda":
+    torch = _KV8[0]
+    if stream is None:
         return torch.empty(shape, dtype=kind, device=device)
     there = torch.cuda.ExternalStream(handle, device=device) if isinstance(stream, int) else stream
     with torch.cuda.stream(there):
@@ -913,14 +930,18 @@ def kv8_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, d_error=No
     head_dim]; k_scale, v_scale: float32 [num_blocks, heads]; slot_mapping: int64."""
     cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     T = slot_mapping.numel()
-    if not (slot_mapping.dtype is _kv8_types()[4] and slot_mapping.is_contiguous()):
+    if not (slot_mapping.dtype is _KV8[4] and slot_mapping.is_contiguous()):
         raise ValueError("slot_mapping is contiguous int64")
     if not (k.dtype is v.dtype and k.shape == v.shape and k.shape[0] >= T):
         raise ValueError("k and v have the same shape and type, a row for each slot")
     width = cache.num_heads * cache.head_dim
-    rc = lib().pkv_kv8_store(C.byref(cache), k.data_ptr(), v.data_ptr(), _kv8_rows(k, width, "k"),
-                             _kv8_rows(v, width, "v"), _kv8_dtype(k), slot_mapping.data_ptr(), T,
-                             d_error or None, _kv8_stream(stream, k_cache))
+    k_stride, v_stride, kind = _kv8_rows(k, width, "k"), _kv8_rows(v, width, "v"), _kv8_dtype(k)
+    device = _kv8_device(stream, k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping)
+    if _kv8_elsewhere(device):
+        with _KV8[0].cuda.device(device):
+            return kv8_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, d_error, stream, check)
+    rc = lib().pkv_kv8_store(C.byref(cache), k.data_ptr(), v.data_ptr(), k_stride, v_stride, kind,
+                             slot_mapping.data_ptr(), T, d_error or None, _kv8_stream(stream, device))
     if check and rc != OK:
         raise PkvError(rc, "pkv_kv8_store")
     return rc
@@ -930,10 +951,11 @@ _KV8_WORKSPACE = {}      # bytes by the sizes they depend on
 
 
 def kv8_attention_workspace(num_tokens, num_q_heads, head_dim, with_weights=False):
-    """Bytes of device workspace an attention call takes (``pkv_kv8_attention_workspace``)."""
-    # without weights the size does not depend on the number of tokens
-    key = (num_tokens if with_weights else 0, num_q_heads, head_dim, bool(with_weights))
-    found = _KV8_WORKSPACE.get(key)
+    """Bytes of device workspace an attention call on the current device takes
+    (``pkv_kv8_attention_workspace``)."""
+    # without weights the size does not depend on the number of tokens; it goes by the device's SMs
+    key = (_kv8_types()[0].cuda.current_device(), num_q_heads, head_dim)
+    found = None if with_weights else _KV8_WORKSPACE.get(key)
     if found is not None:
         return found
     n = C.c_int64(0)
@@ -956,8 +978,8 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     that many positions, its own among them (0: all).  weights: float32 [num_slots], each token's
     softmax weight is added to it.  out, lse, workspace (uint8, kv8_attention_workspace bytes) are
     allocated when not given.  Returns (out, lse); lse is float32 [tokens, q_heads]."""
-    torch, _, f32 = _kv8_types()[:3]
     cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    torch, _, f32 = _KV8[:3]
     _kv8_int32(block_tables, query_start_loc, seq_lens)
     n, table = seq_lens.numel(), block_tables.shape
     if not (len(table) == 2 and table[0] >= n and query_start_loc.numel() >= n + 1):
@@ -969,15 +991,18 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     kind, q_stride = _kv8_dtype(q), _kv8_rows(q, hq * d, "q")
     if weights is not None:
         _kv8_weights(weights, k_cache.shape[0])
-    if out is None:
-        out_stride = hq * d * 2
-    else:
-        if not (out.shape == shape and out.dtype is q.dtype):
-            raise ValueError("out has q's shape and type")
-        out_stride = _kv8_rows(out, hq * d, "out")
+    if out is not None and not (out.shape == shape and out.dtype is q.dtype):
+        raise ValueError("out has q's shape and type")
+    out_stride = hq * d * 2 if out is None else _kv8_rows(out, hq * d, "out")
     if not (lse is None or lse.shape == (T, hq) and lse.dtype is f32 and lse.is_contiguous()):
         raise ValueError("lse is contiguous float32 [tokens, q_heads]")
-    handle = _kv8_stream(stream, k_cache)
+    device = _kv8_device(stream, k_cache, v_cache, k_scale, v_scale, q, block_tables, query_start_loc, seq_lens,
+                         weights, out, lse, workspace)
+    if _kv8_elsewhere(device):
+        with torch.cuda.device(device):
+            return kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_start_loc, seq_lens,
+                                 softmax_scale, window, weights, out, lse, workspace, d_error, stream, check)
+    handle = _kv8_stream(stream, device)
     if out is None:
         out = _kv8_make(shape, q.dtype, q.device, stream, handle)
     if lse is None:
@@ -1003,22 +1028,30 @@ def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_len
               d_error=None, stream=None, check=True):
     """Shrink requests to ``budget`` tokens by accumulated weight, into new blocks
     (``pkv_kv8_evict``).  Returns (new_seq_lens [n], kept [n, budget])."""
-    torch = _kv8_types()[0]
     cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    torch = _KV8[0]
     _kv8_int32(block_tables, new_block_tables, seq_lens)
     n, budget = seq_lens.numel(), int(budget)
     old, new = block_tables.shape, new_block_tables.shape
     if not (len(old) == 2 and len(new) == 2 and old[0] >= n and new[0] >= n):
         raise ValueError("block_tables and new_block_tables are [n, width]")
     _kv8_weights(weights, k_cache.shape[0])
-    handle = _kv8_stream(stream, k_cache)
+    for t, size in ((new_seq_lens, n), (kept, n * max(budget, 0))):
+        if t is not None:
+            _kv8_int32(t)
+            if t.numel() != size:
+                raise ValueError("new_seq_lens [n], kept [n, budget]")
+    device = _kv8_device(stream, k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_lens,
+                         new_block_tables, new_seq_lens, kept)
+    if _kv8_elsewhere(device):
+        with torch.cuda.device(device):
+            return kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_lens, new_block_tables,
+                             budget, keep_first, keep_last, new_seq_lens, kept, d_error, stream, check)
+    handle = _kv8_stream(stream, device)
     if new_seq_lens is None:
         new_seq_lens = _kv8_make(n, torch.int32, seq_lens.device, stream, handle)
     if kept is None:
         kept = _kv8_make((n, max(budget, 0)), torch.int32, seq_lens.device, stream, handle)
-    _kv8_int32(new_seq_lens, kept)
-    if not (new_seq_lens.numel() == n and kept.numel() == n * max(budget, 0)):
-        raise ValueError("new_seq_lens [n], kept [n, budget]")
     rc = lib().pkv_kv8_evict(C.byref(cache), weights.data_ptr(), block_tables.data_ptr(), old[1],
                              seq_lens.data_ptr(), n, new_block_tables.data_ptr(), new[1], budget,
                              int(keep_first), int(keep_last), new_seq_lens.data_ptr(), kept.data_ptr(),

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import paged_kv_prep_gb300 as pkv
+from paged_kv_prep_gb300 import _lib
 from paged_kv_prep_gb300 import build as pbuild
 from paged_kv_prep_gb300._lib import Kv8CacheArgs
 from tests import kv8_reference as ref
@@ -131,3 +132,94 @@ def test_reference_rounding_is_e4m3():
     assert torch.equal(ref.encode(x.double()), want)
     assert ref.decode(ref.encode(torch.tensor([float("nan")]).double())).isnan().all()
     assert ref.block_scale(448.0) == 1.0 and ref.block_scale(448.5) == 2.0 and ref.block_scale(0.0) == 2.0 ** -64
+
+
+def calls():
+    """The three calls on operands that fit together but for their place."""
+    bs, blocks, heads, d = 16, 4, 2, 128
+    kc = torch.zeros(bs * blocks, heads * d, dtype=torch.uint8)
+    sc = torch.ones(blocks, heads)
+    k = torch.zeros(3, heads, d, dtype=torch.bfloat16)
+    tab = torch.zeros(1, 4, dtype=torch.int32)
+    qsl, lens = torch.zeros(2, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    q, w = torch.zeros(3, 8, d, dtype=torch.bfloat16), torch.zeros(bs * blocks)
+    return [lambda **kw: pkv.kv8_store(k, k, kc, kc, sc, sc, torch.zeros(3, dtype=torch.int64), **kw),
+            lambda **kw: pkv.kv8_attention(q, kc, kc, sc, sc, tab, qsl, lens, weights=w, **kw),
+            lambda **kw: pkv.kv8_evict(kc, kc, sc, sc, w, tab, lens, tab, 8, **kw)]
+
+
+@pytest.mark.parametrize("which", range(3))
+@pytest.mark.parametrize("stream", [None, 0])
+def test_operands_are_on_a_cuda_device(which, stream, monkeypatch):
+    """Host operands never reach the library."""
+    reached = []
+    monkeypatch.setattr(_lib, "lib", lambda: reached.append(1))
+    with pytest.raises(ValueError):
+        calls()[which](stream=stream)
+    assert not reached
+
+
+def test_operands_and_stream_are_on_one_device():
+    class On:
+        def __init__(self, device):
+            self.device_index = device
+
+        def get_device(self):
+            return self.device_index
+
+    assert _lib._kv8_device(None, On(1), On(1), None, On(1)) == 1
+    assert _lib._kv8_device(On(1), On(1)) == 1 and _lib._kv8_device(77, On(1)) == 1
+    for bad in ((None, On(0), On(1)), (None, On(0), On(-1)), (None, On(-1), On(-1)), (On(0), On(1), On(1))):
+        with pytest.raises(ValueError):
+            _lib._kv8_device(*bad)
+
+
+class FakeDevices:
+    """Two devices of which `now` is the current one; a library that notes under which it was called."""
+
+    def __init__(self, monkeypatch):
+        self.now, self.seen = 0, []
+        fake = self
+
+        class Switch:
+            def __init__(self, device):
+                self.to = device
+
+            def __enter__(self):
+                self.back, fake.now = fake.now, self.to
+
+            def __exit__(self, *a):
+                fake.now = self.back
+
+        class Library:
+            def __getattr__(self, name):
+                def call(*a):
+                    fake.seen.append((name, fake.now))
+                    if name == "pkv_kv8_attention_workspace":
+                        a[-1]._obj.value = 1000 * (1 + fake.now)
+                    return pkv.OK
+                return call
+
+        monkeypatch.setattr(_lib, "_KV8", _lib._kv8_types()[:6] + (lambda: fake.now,))
+        monkeypatch.setattr(torch.cuda, "current_device", lambda: fake.now)
+        monkeypatch.setattr(torch.cuda, "device", Switch)
+        monkeypatch.setattr(_lib, "lib", Library)
+        monkeypatch.setattr(_lib, "_KV8_WORKSPACE", {})
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_the_operands_device_is_current_in_the_call(which, monkeypatch):
+    fake = FakeDevices(monkeypatch)
+    monkeypatch.setattr(_lib, "_kv8_device", lambda *a: 1)
+    monkeypatch.setattr(_lib, "_kv8_stream", lambda stream, device: 10 + device)
+    calls()[which]()
+    assert fake.seen and all(device == 1 for _, device in fake.seen) and fake.now == 0
+
+
+def test_workspace_sizes_go_by_the_device(monkeypatch):
+    fake = FakeDevices(monkeypatch)
+    assert pkv.kv8_attention_workspace(4, 8, 128) == 1000
+    fake.now = 1
+    assert pkv.kv8_attention_workspace(4, 8, 128) == 2000
+    fake.now = 0
+    assert pkv.kv8_attention_workspace(9, 8, 128) == 1000 and len(fake.seen) == 2
