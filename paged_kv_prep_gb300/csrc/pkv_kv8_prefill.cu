@@ -8,7 +8,8 @@
 // row's maximum over its first unit and then follows lazily: it moves only
 // when the sum of 64 w, which is needed anyway, exceeds 2^14.  So later units
 // take no pass for the maximum, the accumulator is hardly ever rescaled, and w
-// stays inside f16's range with all its bits.
+// stays inside f16's range: it is off by 2^-11 of itself, or by 2^-25 of the
+// reference's weight (w = 1) where it is 2^-14 or less and f16 is subnormal.
 //
 // Bound: the tensor pipe (4 D flops per visible pair); beside it per tile of
 // 256 rows x 128 tokens 32768 exponentials and 32768 codes turned into f16.

@@ -118,6 +118,32 @@ def attention(q, kc, vc, ks, vs, tables, starts, lens, scale, window, weights=No
     return out, lse, size, reach
 
 
+def carried(q, kc, vc, ks, vs, tables, starts, lens, scale, window):
+    """Per (query, head) of `attention`'s rows: the largest p * v_scale of a token it sees, and how many it sees."""
+    T, hq, _ = q.shape
+    blocks, heads = ks.shape
+    bs, group = kc.shape[0] // blocks, hq // heads
+    most, count = torch.zeros(T, hq, dtype=torch.float64), torch.zeros(T, dtype=torch.float64)
+    for i, length in enumerate(lens):
+        a, b = starts[i], starts[i + 1]
+        keys = [s for s in range(max(length, 0)) if s // bs < tables.shape[1] and 0 <= tables[i, s // bs] < blocks]
+        if a == b or not keys:
+            continue
+        at = torch.tensor(keys)
+        block = tables[i].long()[at // bs]
+        pos = length - b + torch.arange(a, b)
+        seen = at[None, :] <= pos[:, None]
+        if window:
+            seen &= at[None, :] > pos[:, None] - window
+        count[a:b] = seen.sum(1).double()
+        for h in range(heads):
+            k = decode(kc[block * bs + at % bs, h]) * ks[block, h].double()[:, None]
+            logits = (q[a:b, h * group:(h + 1) * group].double() @ k.T * scale).masked_fill(~seen[:, None], -math.inf)
+            p = torch.exp(logits - torch.logsumexp(logits, -1)[..., None]).masked_fill(~seen[:, None], 0.0)
+            most[a:b, h * group:(h + 1) * group] = (p * vs[block, h].double()).amax(-1)
+    return most, count
+
+
 def evict(kc, vc, ks, vs, weights, tables, lens, fresh, budget, first, last):
     """In place on the CPU tensors; returns new lengths and kept positions."""
     blocks = ks.shape[0]

@@ -489,3 +489,41 @@ def test_outputs_freed_early_are_not_handed_out_while_in_use():
     assert again.data_ptr() != at
     torch.cuda.synchronize()
     assert torch.equal(late, want)
+
+
+def own_tolerance(case, want, scale, window=0):
+    """As in compare, but with what a row itself carries in the place of the cache's largest value scale: a
+    weight times its value scale is rounded to f16 by 2^-11 of itself, or by 2^-25 of the row's reference
+    where it is 2^-14 of that or less; the reference is below twice the largest of the row, and a weight that
+    has moved with it was rounded twice.  A code is at most 448."""
+    w_out, w_lse, size, reach = want
+    most, count = ref.carried(case.q, *case.caches, *case.scales, case.tables, case.starts, case.lens, scale, window)
+    logit = 2.0 ** -19 * reach + 2.0 ** -22 * w_lse.abs().clamp(max=1e30) + 2.0 ** -17
+    tol = (2.0 ** -11 + 2.0 ** -17 + 2 * logit[..., None]) * size
+    tol = tol + (count[:, None] * 2.0 ** -23 * 448.0 * most)[..., None]
+    return tol + HALF[case.dtype] * (w_out.abs() + tol) + 2.0 ** -25
+
+
+@pytest.mark.parametrize("spread", [10, 20])
+@pytest.mark.parametrize("reqs", [[(1, 100), (1, 33), (1, 250)], [(1, 100), (6, 60)], [(40, 100), (100, 300)]],
+                         ids=["decodes", "short", "chunks"])
+def test_rows_keep_what_is_small_in_the_cache(reqs, spread):
+    """Value scales up to 2^40 apart between requests, 2^20 within one: each row is held to what it carries
+    itself, so that a row of small values lost as a whole would show."""
+    case = Case(reqs, 16, 2, 4, 128, seed=22 + spread, dtype=torch.float16)
+    for i in range(2):
+        case.scales[i] = torch.exp2(torch.randint(-8, -5, case.scales[i].shape, generator=case.gen).float())
+    step = torch.linspace(-spread, spread, len(reqs)).round()
+    for i in range(len(reqs)):
+        used = case.tables[i][case.tables[i] >= 0].long()
+        case.scales[1][used] = torch.exp2(step[i] + torch.randint(-spread // 2, spread // 2 + 1, (len(used), case.heads),
+                                                                   generator=case.gen).float() - 6).clamp(max=2.0)
+    scale = case.d ** -0.5
+    out, lse = pkv.kv8_attention(*case.args(), softmax_scale=scale)
+    want = case.reference(scale, 0)
+    tol = own_tolerance(case, want, scale)
+    lost = (want[0].abs() > tol).double().mean((1, 2))       # the share of a row whose loss would show
+    assert (lost > 0.5).double().mean() > 0.9, lost
+    compare(case, out, lse, want)
+    bad = (out.cpu().double() - want[0]).abs() > tol
+    assert not bad.any(), (int(bad.sum()), float(((out.cpu().double() - want[0]).abs() / tol).max()))
