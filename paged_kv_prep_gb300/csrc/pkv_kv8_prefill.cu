@@ -5,8 +5,10 @@
 // from the tensor core, a_b = k_scale * softmax_scale * log2(e) and lv_b =
 // log2(v_scale), both constant over 16 tokens; w = 2^(x - R) goes into the
 // second product as f16, the softmax sum adds w / v_scale in fp32.  R is the
-// row's maximum over its first unit and then follows lazily: it moves only
-// when the sum of 64 w, which is needed anyway, exceeds 2^14.  So later units
+// row's maximum over its first unit, rounded up to an integer, and then follows
+// lazily: it moves only when the sum of 64 w, which is needed anyway, exceeds
+// 2^14, and by a whole power of two, so that weights which are f16 already are
+// not rounded again (unless they turn subnormal).  So later units
 // take no pass for the maximum, the accumulator is hardly ever rescaled, and w
 // stays inside f16's range: it is off by 2^-11 of itself, or by 2^-25 of the
 // reference's weight (w = 1) where it is 2^-14 or less and f16 is subnormal.
@@ -209,8 +211,13 @@ __device__ __forceinline__ float2 weights32(const uint32_t (&s)[32], uint32_t (&
     return sums;
 }
 
+// 2^d of an integer d <= 0 (0 below 2^-126, and of -inf).
+__device__ __forceinline__ float power2_down(float d) {
+    return d >= -126.f ? __uint_as_float(static_cast<uint32_t>(static_cast<int>(d) + 127) << 23) : d < 0.f ? 0.f : d;
+}
+
 // Columns 32 c .. of a unit from `c` on, where some row's weights outgrow its reference: the reference
-// moves up to their largest x, with the row's sum, its weights of this unit so far and its
+// moves up to the next integer of their largest x, with the row's sum, its weights of this unit so far and its
 // accumulator (o_cols columns, 0 while it holds nothing).  Rare.
 template <int D>
 __device__ __forceinline__ void grow_rows(const Smem<D> *sm, int c, uint32_t ts, uint32_t to, int o_cols, int ring, float cf,
@@ -230,11 +237,10 @@ __device__ __forceinline__ void grow_rows(const Smem<D> *sm, int c, uint32_t ts,
         for (int k = 0; k < 32; k++) most = fmaxf(most, fmaf(__uint_as_float(s[k]), k < 16 ? a.x : a.y, k < 16 ? lv.x : lv.y));
         const bool grow = most > top;
         // an infinite maximum cannot be followed: its row is NaN
-        if (most == INFINITY) most = NAN;
-        const float f = grow ? exp2_fast(top - most) : 1.f;
+        most = most == INFINITY ? NAN : ceilf(most);
+        const float f = grow ? power2_down(top - most) : 1.f;
         if (grow) top = most;
         sum *= f;
-        const __half2 ff = __float2half2_rn(f);
 #pragma unroll 1
         for (int k = 0; k < c; k++) {
             uint32_t y[16];
@@ -242,8 +248,8 @@ __device__ __forceinline__ void grow_rows(const Smem<D> *sm, int c, uint32_t ts,
             tc_wait_ld();
 #pragma unroll
             for (int q = 0; q < 16; q++) {
-                const __half2 z = __hmul2(*reinterpret_cast<const __half2 *>(&y[q]), ff);
-                y[q] = *reinterpret_cast<const uint32_t *>(&z);
+                const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&y[q]));
+                y[q] = pack_f16(z.x * f, z.y * f);       // f may be below f16's range
             }
             tmem_st16(ts + 16 * k, y);
         }
@@ -376,7 +382,7 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk, in
             // the first unit that shows a row anything sets its reference (no weight has been added before)
             if (__any_sync(~0u, top == -INFINITY)) {
                 const float most = row_max<D>(sm, ts, ring, cf, lo, hi);
-                if (top == -INFINITY) top = most == INFINITY ? NAN : most;
+                if (top == -INFINITY) top = most == INFINITY ? NAN : ceilf(most);
             }
             row_weights<D>(sm, ts, to, t > 0 ? D : 0, ring, cf, top, sum, whole, lo, hi);
             tc_wait_st();

@@ -527,3 +527,37 @@ def test_rows_keep_what_is_small_in_the_cache(reqs, spread):
     compare(case, out, lse, want)
     bad = (out.cpu().double() - want[0]).abs() > tol
     assert not bad.any(), (int(bad.sum()), float(((out.cpu().double() - want[0]).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("high,low", [(22, 7), (30, 7), (24, 0), (9, 7)])
+def test_weights_before_a_moved_reference_keep_their_bits(high, low, d):
+    """Chunks whose second unit of 128 keys raises the rows' reference in its second half: the weights of its
+    first half, already rounded, follow the reference.  The key that raises it has the value zero in some
+    dimensions, where the output is what those weights carry."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    one = Case([(16, 272)], 16, 1, 4, d, torch.float16, seed=23)
+    gen = one.gen
+    order = one.tables[0, :17].long()
+    slots = (order[:, None] * 16 + torch.arange(16)).view(-1)
+    one.scales = [torch.ones_like(s) for s in one.scales]
+    value = torch.zeros(272, dtype=torch.float64)            # a key's first element; a query's is 0.95 ln 2
+    value[128:192], value[200] = low, high
+    keys = torch.zeros(272, 1, d, dtype=torch.float64)
+    keys[:, 0, 0] = value
+    values = torch.randint(64, 127, (272, 1, d), generator=gen, dtype=torch.uint8)   # 2 to 448
+    values[200, 0, :d // 2] = 0
+    one.caches[0][slots], one.caches[1][slots] = ref.encode(keys), values
+    one.q = torch.zeros_like(one.q)
+    one.q[:, :, 0] = 0.95 * math.log(2)
+    want = one.reference(1.0, 0)
+    tol = own_tolerance(one, want, 1.0)
+    # as many requests on the same blocks as give every CTA whole requests
+    n = 2 * sms
+    q, kc, vc, ks, vs, tab, _, lens = one.args()
+    starts = torch.arange(0, 16 * n + 1, 16, dtype=torch.int32, device="cuda")
+    out, lse = pkv.kv8_attention(q.repeat(n, 1, 1), kc, vc, ks, vs, tab.repeat(n, 1), starts, lens.repeat(n), softmax_scale=1.0)
+    out, lse = out.cpu().double().view(n, 16, 4, d), lse.cpu().double().view(n, 16, 4)
+    assert ((lse - want[1]).abs() <= 2.0 ** -19 * want[3] + 2.0 ** -22 * want[1].abs() + 2.0 ** -17).all()
+    bad = (out - want[0]).abs() > tol
+    assert not bad.any(), (int(bad.sum()), float(((out - want[0]).abs() / tol).max()))
