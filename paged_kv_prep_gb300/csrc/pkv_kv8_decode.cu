@@ -166,7 +166,9 @@ struct Tile {
         };
         // A stage's keys are refilled when every lane has taken them out, then its values.
         auto fetch_k = [&](const Place &y, Stage<D> &st) {
-            const bool on = kGrouped ? y.block >= 0 : (y.mask >> lane) & 1;
+            // a group's scales count where some row sees one of its tokens: whatever those of an unseen block
+            // hold (one given away before the window) stays out
+            const bool on = (y.mask >> (kGrouped ? lane & 16 : lane)) & (kGrouped ? 0xffffu : 1u);
             const int64_t sc = on ? static_cast<int64_t>(y.block) * p.Hkv + head : 0;
             if constexpr (kGrouped) {
                 // lanes 0, 16: K scales; lanes 1, 17: V scales

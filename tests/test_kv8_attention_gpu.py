@@ -561,3 +561,24 @@ def test_weights_before_a_moved_reference_keep_their_bits(high, low, d):
     assert ((lse - want[1]).abs() <= 2.0 ** -19 * want[3] + 2.0 ** -22 * want[1].abs() + 2.0 ** -17).all()
     bad = (out - want[0]).abs() > tol
     assert not bad.any(), (int(bad.sum()), float(((out - want[0]).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, 0.0, -1.0])
+def test_scales_before_the_window_do_not_count(bad):
+    """A block that no query of the call sees, still in the table, whose scales hold anything: a freed block that
+    another request has been given and not yet written."""
+    case = Case([(1, 100), (1, 300), (3, 120), (40, 200)], 16, 2, 4, 128, seed=24)
+    window = 20
+    seen = torch.zeros(case.blocks, dtype=torch.bool)
+    for i, (c, x) in enumerate(case.reqs):
+        seen[case.tables[i, max(0, x - c - window + 1) // 16:-(-x // 16)].long()] = True
+    for s in case.scales:
+        s[~seen] = bad
+    a = case.args()
+    w = torch.zeros(case.blocks * case.bs, device="cuda")
+    out, lse = pkv.kv8_attention(*a, window=window, weights=w)
+    for s in case.scales:                                    # what they hold must not matter
+        s[~seen] = 1.0
+    want = case.reference(case.d ** -0.5, window)
+    compare(case, out, lse, want)
+    assert torch.isfinite(w).all() and not seen.all()
