@@ -64,7 +64,8 @@ struct Smem {
     uint64_t q_full[2], k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2], o_full[2], done;
     uint32_t tmem;
     int32_t failed;
-    int32_t nan_seen;                   // this CTA has met a V code that is NaN
+    int32_t nan_seen;                   // this CTA has met a V code that is NaN,
+    uint32_t nan_units[32];             // in units of these numbers, modulo 1024
 };
 
 // The keys that rows f0 .. of a tile see: [lo, hi), and the 16-aligned start of their units.
@@ -303,6 +304,42 @@ __device__ __forceinline__ void row_weights(const Smem<D> *sm, uint32_t ts, uint
     if (c < 4) grow_rows<D>(sm, c, ts, to, o_cols, ring, cf, top, sum, lo, hi);
 }
 
+// Which of 16 bytes are NaN codes, a bit each.
+__device__ __forceinline__ uint32_t nan_bytes(uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t bits = 0;
+#pragma unroll
+    for (int k = 0; k < 4; k++)
+        bits |= (((__vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0x08040201u) * 0x01010101u) >> 24) << (4 * k);
+    return bits;
+}
+
+// Which of a row's dimensions 32 c .. + 31 (at `values` within a line) meet a NaN value: its tokens s0 .. s1 - 1,
+// of which those from `a` on are in units numbered from `unit` on, where the converting warps met one.  (Looked
+// for in all of a long context, one NaN would hold its rows up for longer than the other warps wait.)
+__device__ __noinline__ uint32_t nan_dims(const AttnParams &p, const uint32_t *units, const int32_t *table, const uint8_t *values,
+                                             int64_t line, uint32_t unit, int a, int s0, int s1) {
+    uint32_t hit = 0;
+#pragma unroll 1
+    for (; a < s1 && hit != ~0u; a += kKeys, unit++) {
+        if (!((*static_cast<const volatile uint32_t *>(&units[(unit >> 5) & 31]) >> (unit & 31)) & 1)) continue;
+#pragma unroll 1
+        for (int g = a; g < a + kKeys; g += 16) {
+            if (g + 16 <= s0 || g >= s1) continue;
+            const int b = block_of(p, table, g);     // 16 tokens from a multiple of 16 on lie in one block
+            if (b < 0) continue;
+            const uint8_t *v = values + (static_cast<int64_t>(b) * p.bs + g % p.bs) * line;
+            const int from = max(s0 - g, 0), to = min(s1 - g, 16);
+#pragma unroll 2
+            for (int k = from; k < to; k++) {
+                const uint4 *at = reinterpret_cast<const uint4 *>(v + k * line);
+                hit |= nan_bytes(__ldg(at)) | nan_bytes(__ldg(at + 1)) << 16;
+            }
+        }
+    }
+    return hit;
+}
+
 // ---- softmax warps: a thread per row ----------------------------------------------------------
 template <int D>
 __device__ void softmax_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk, int64_t total, int64_t ranges) {
@@ -402,19 +439,16 @@ __device__ void softmax_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk, in
         char *out = p.out + static_cast<int64_t>(x.r.start + j) * p.out_stride + 2 * static_cast<int64_t>(hq) * D;
 #pragma unroll 1
         for (int c = 0; c < D / 32; c++) {
+            // NaN codes were left out of the product: they go to the rows that see their token
+            uint32_t hit = 0;
+            if (nan && live)
+                hit = nan_dims(p, sm->nan_units, x.table, p.vc + x.head * D + 32 * c, static_cast<int64_t>(p.Hkv) * D, unit - nu,
+                               x.s.base + x.ua * kKeys, lo_of(p, pos), min(min(pos + 1, x.s.hi), x.s.base + x.ub * kKeys));
+            __syncwarp();
             uint32_t o[32];
             tmem_ld32(o, to + 32 * c);
             tc_wait_ld();
-            if (nan && live) {
-                // NaN codes were left out of the product: they go to the rows that see their token
-                uint32_t hit = 0;
-                const int s1 = min(min(pos + 1, x.s.hi), x.s.base + x.ub * kKeys);
-                for (int s = max(max(lo_of(p, pos), x.s.lo), x.s.base + x.ua * kKeys); s < s1; s++) {
-                    const int b = block_of(p, x.table, s);
-                    if (b < 0) continue;
-                    const uint8_t *v = p.vc + ((static_cast<int64_t>(b) * p.bs + s % p.bs) * p.Hkv + x.head) * D + 32 * c;
-                    for (int k = 0; k < 32; k++) hit |= ((v[k] & 127) == 127 ? 1u : 0u) << k;
-                }
+            if (nan) {
 #pragma unroll
                 for (int k = 0; k < 32; k++)
                     if ((hit >> k) & 1) o[k] = 0x7fffffffu;
@@ -527,7 +561,7 @@ __device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
         cp_async<16>(smem_addr(raw + r * kRaw + i * 16), cache + (live ? from + mine : 0), live);
     };
     // Turn a half (keys or values) of unit `a` into f16, and refill its pieces with the next unit's.
-    auto half = [&](const uint8_t *cache, char *raw, char *dst, const Feed &b, bool next, bool values) {
+    auto half = [&](const uint8_t *cache, char *raw, char *dst, const Feed &b, bool next, bool values, uint32_t unit) {
         bool nan = false;
 #pragma unroll 1
         for (int r0 = 0; r0 < kRounds; r0 += kStep) {
@@ -567,7 +601,10 @@ __device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
 #pragma unroll
                 for (int r = 0; r < kStep; r++) fetch(cache, b, r0 + r, raw);
         }
-        if (nan) *static_cast<volatile int32_t *>(&sm->nan_seen) = 1;
+        if (nan) {
+            atomicOr(&sm->nan_units[(unit >> 5) & 31], 1u << (unit & 31));
+            *static_cast<volatile int32_t *>(&sm->nan_seen) = 1;
+        }
         cp_commit();
     };
 
@@ -601,13 +638,13 @@ __device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
             sm->lv[ring][i] = named ? __log2f(v) : -INFINITY;
             sm->iv[ring][i] = named ? __frcp_rn(v) : 0.f;
         }
-        half(p.kc, sm->raw[0], sm->k[stage], b, next, false);
+        half(p.kc, sm->raw[0], sm->k[stage], b, next, false, unit);
         fence_async_shared();
         mbar_arrive(&sm->k_full[stage]);
         cp_wait<1>();
         ok = wait(sm, &sm->v_free[stage], parity);
         if (!__all_sync(~0u, ok)) break;
-        half(p.vc, sm->raw[1], sm->v[stage], b, next, true);
+        half(p.vc, sm->raw[1], sm->v[stage], b, next, true, unit);
         fence_async_shared();
         mbar_arrive(&sm->v_full[stage]);
         a = b;
@@ -716,6 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const AttnPara
         mbar_init(&sm->done, 1);
         sm->failed = 0;
         sm->nan_seen = 0;
+        for (int k = 0; k < 32; k++) sm->nan_units[k] = 0;
         fence_mbar_init();
     }
     tc_fence_before();

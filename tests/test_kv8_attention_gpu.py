@@ -582,3 +582,43 @@ def test_scales_before_the_window_do_not_count(bad):
     want = case.reference(case.d ** -0.5, window)
     compare(case, out, lse, want)
     assert torch.isfinite(w).all() and not seen.all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_nan_in_a_long_context_is_found_where_it_is(d):
+    """NaN values far apart in a context of more units than a CTA numbers apart: every row takes those it sees,
+    and looking for them is little beside the call."""
+    L, T, group, bs = 140000, 4864, 8, 16
+    gen = torch.Generator(device="cuda").manual_seed(25)
+    blocks = L // bs
+    kc = torch.randint(0, 100, (L, d), generator=gen, device="cuda", dtype=torch.uint8)
+    vc = torch.randint(0, 100, (L, d), generator=gen, device="cuda", dtype=torch.uint8)
+    sc = torch.full((blocks, 1), 2.0 ** -6, device="cuda")
+    table = torch.randperm(blocks, generator=gen, device="cuda").to(torch.int32)[None]
+    q = torch.randn(T, group, d, generator=gen, device="cuda").bfloat16()
+    qsl, lens = torch.tensor([0, T], dtype=torch.int32, device="cuda"), torch.tensor([L], dtype=torch.int32, device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def timed():
+        best = math.inf
+        for _ in range(4):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            out, lse = pkv.kv8_attention(q, kc, vc, sc, sc, table, qsl, lens, d_error=word.data_ptr())
+            b.record()
+            torch.cuda.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return out, lse, best
+
+    plain, plain_lse, plain_ms = timed()
+    want = torch.zeros(T, d, dtype=torch.bool)
+    pos = torch.arange(L - T, L)
+    for at, dim in ((3, 5), (70001, 33), (136000, 63), (136001, 62), (139990, 1)):
+        vc[int(table[0, at // bs]) * bs + at % bs, dim] = 127 if at % 2 else 255
+        want[:, dim] |= pos >= at
+    out, lse, ms = timed()
+    assert word.item() == 0 and torch.equal(lse, plain_lse)
+    assert torch.equal(out.isnan().cpu(), want[:, None].expand(T, group, d))
+    same = ~want.cuda()[:, None].expand(T, group, d)
+    assert torch.equal(out[same], plain[same])
+    assert ms < 4 * plain_ms, (ms, plain_ms)
