@@ -822,11 +822,6 @@ def _kv8_types():
     return _KV8
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
-
 def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
     """The C view of an 8-bit cache: lines [num_slots, heads * head_dim] of one byte per element
     and scales [num_blocks, heads]."""
