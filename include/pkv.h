@@ -573,8 +573,9 @@ int pkv_selftest_wait_timeout(int32_t *d_error, uint32_t polls, pkv_stream_t s);
  * The lines of pkv_kv_cache_write's caches hold e4m3 codes, and every (block,
  * KV head) has one float32 scale for K and one for V: a value is code * scale.
  *   k_cache, v_cache: [num_blocks * block_size][num_heads][head_dim] bytes, 16-byte aligned;
- *   k_scale, v_scale: [num_blocks][num_heads], positive (pkv_kv8_store makes powers of two;
- *                     a V scale below 2^-100 counts as 2^-100).
+ *   k_scale, v_scale: [num_blocks][num_heads], positive and finite where a token of the block
+ *                     is read (pkv_kv8_store makes powers of two; a V scale below 2^-100 counts
+ *                     as 2^-100).
  * head_dim is 64, 128 or 256; num_heads (KV heads) at most 1024; any block_size,
  * with fewer than 2^32 slots.
  */
@@ -660,6 +661,10 @@ int pkv_kv8_attention(const pkv_kv8_cache *cache, const void *q, int64_t q_strid
  * order, into the blocks of new_block_tables[i], which no request's
  * block_tables name; the old blocks keep their contents and may be shared.  A
  * new block's scale is the largest of its tokens' scales, codes are rounded to it.
+ * The lines themselves move unchanged: keys that carry a position (rotary ones)
+ * keep the one they were stored with.  pkv_prepare_batch gives positions by the
+ * cache index, so a request that goes on after this has new_seq_lens[i] where
+ * such a model needs the old seq_lens[i]: it has to keep that offset itself.
  *   new_seq_lens[n]:  min(seq_lens[i], budget), or -1 for a request left alone
  *                     because a table names no block where one is needed
  *                     (PKV_DEVERR_BLOCK) or is too short (PKV_DEVERR_POSITION);
