@@ -622,3 +622,15 @@ def test_a_nan_in_a_long_context_is_found_where_it_is(d):
     same = ~want.cuda()[:, None].expand(T, group, d)
     assert torch.equal(out[same], plain[same])
     assert ms < 4 * plain_ms, (ms, plain_ms)
+
+
+@pytest.mark.parametrize("reqs", [[(1, 90), (1, 70), (1, 200), (1, 64)], [(1, 90), (30, 70), (80, 200), (3, 64)]],
+                         ids=["decodes", "mixed"])
+def test_blocks_shared_by_requests(reqs):
+    """Requests with a common prefix on the same blocks: each block adds up what every request gave it."""
+    case = Case(reqs, 16, 2, 4, 128, seed=26)
+    for i in range(1, len(reqs)):
+        case.tables[i, :3] = case.tables[0, :3]
+    check(case)
+    case.tables[1, 3] = case.tables[0, 3]                    # one that the first request fills further
+    check(case, window=50)

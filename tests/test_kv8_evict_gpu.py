@@ -210,3 +210,9 @@ def test_the_copy_starts_no_block_past_a_table(lens, fits, wide):
     cuda.cuGraphDestroy(graph)
     copies = [g for g in grids if g[1] == len(lens)]
     assert len(copies) == 1 and copies[0][0] <= min(fresh.shape[1], table.shape[1], -(-wide // 16)), grids
+
+
+@pytest.mark.parametrize("shape", ["heavy", "ties"])
+def test_more_candidates_than_are_held(shape):
+    """A request whose keys do not fit a cluster's shared memory, beside one whose keys do."""
+    check([140001, 20000], 32, 1, 64, 2001, 4, 64, seed=10, shape=shape)

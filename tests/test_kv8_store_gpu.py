@@ -196,3 +196,18 @@ def test_slots_past_32_bits():
     ref.store(k.cpu(), k.cpu(), small, small.clone(), ss, ss.clone(), torch.arange(0, 20), 2)
     assert torch.equal(kc[-32:].cpu().view(small.shape), small) and torch.equal(vc[-32:], kc[-32:])
     assert torch.equal(ks[-2:].cpu(), ss) and int(kc[:-32].max()) == 0
+
+
+def test_more_tokens_than_a_round():
+    """So many tokens that a CTA takes several segments of the line one after the other."""
+    gen = torch.Generator().manual_seed(9)
+    heads, d, bs = 2, 256, 32
+    lengths = [9001, 700, 1, 33, 11003]
+    blocks = sum(-(-n // bs) + 1 for n in lengths) + 3
+    slots = runs_of(gen, bs, blocks, lengths)
+    T = len(slots)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert -(-12 * sms // -(-T // 32)) < 2 * heads * d // 256
+    mag = torch.exp2(torch.randint(-6, 7, (T, 1), generator=gen).float())
+    k, v = [(torch.randn(T, heads * d, generator=gen) * mag).bfloat16() for _ in range(2)]
+    check(k, v, slots, blocks, bs, heads, d, gen)
