@@ -991,6 +991,8 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     out_stride = hq * d * 2 if out is None else _kv8_rows(out, hq * d, "out")
     if not (lse is None or lse.shape == (T, hq) and lse.dtype is f32 and lse.is_contiguous()):
         raise ValueError("lse is contiguous float32 [tokens, q_heads]")
+    if not (workspace is None or workspace.is_contiguous()):
+        raise ValueError("workspace is contiguous")
     device = _kv8_device(stream, k_cache, v_cache, k_scale, v_scale, q, block_tables, query_start_loc, seq_lens,
                          weights, out, lse, workspace)
     if _kv8_elsewhere(device):

@@ -223,3 +223,15 @@ def test_workspace_sizes_go_by_the_device(monkeypatch):
     assert pkv.kv8_attention_workspace(4, 8, 128) == 2000
     fake.now = 0
     assert pkv.kv8_attention_workspace(9, 8, 128) == 1000 and len(fake.seen) == 2
+
+
+def test_a_workspace_with_gaps_is_refused(monkeypatch):
+    """Its bytes are written one behind the other: what lies between the elements of a view is not its."""
+    fake = FakeDevices(monkeypatch)
+    monkeypatch.setattr(_lib, "_kv8_device", lambda *a: 0)
+    calls()[1](workspace=torch.zeros(4096, dtype=torch.uint8), stream=0, lse=torch.zeros(3, 8), out=torch.zeros(3, 8, 128).bfloat16())
+    assert [name for name, _ in fake.seen] == ["pkv_kv8_attention"]
+    with pytest.raises(ValueError):
+        calls()[1](workspace=torch.zeros(8192, dtype=torch.uint8)[::2], stream=0, lse=torch.zeros(3, 8),
+                   out=torch.zeros(3, 8, 128).bfloat16())
+    assert len(fake.seen) == 1
