@@ -869,6 +869,14 @@ def _kv8_dtype(x):
     return kind
 
 
+def _kv8_size(x, what):
+    """An integer argument as the library takes it; a larger one would be cut to its low 32 bits."""
+    x = int(x)
+    if not -1 << 31 <= x < 1 << 31:
+        raise ValueError(f"{what} is a 32-bit integer")
+    return x
+
+
 def _kv8_weights(weights, slots):
     if not (weights.dtype is _KV8[2] and weights.is_contiguous() and weights.numel() == slots):
         raise ValueError("weights is contiguous float32, one for each slot")
@@ -983,6 +991,7 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     if not (len(shape) == 3 and shape[2] == cache.head_dim):
         raise ValueError("q is [tokens, q_heads, head_dim]")
     T, hq, d = shape
+    window = _kv8_size(window, "window")
     kind, q_stride = _kv8_dtype(q), _kv8_rows(q, hq * d, "q")
     if weights is not None:
         _kv8_weights(weights, k_cache.shape[0])
@@ -1009,7 +1018,7 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
         workspace = _kv8_make(size, torch.uint8, q.device, stream, handle, returned=False)
     rc = lib().pkv_kv8_attention(C.byref(cache), q.data_ptr(), q_stride, kind, hq, block_tables.data_ptr(),
                                  table[1], query_start_loc.data_ptr(), seq_lens.data_ptr(), n, T,
-                                 d ** -0.5 if softmax_scale is None else float(softmax_scale), int(window),
+                                 d ** -0.5 if softmax_scale is None else float(softmax_scale), window,
                                  out.data_ptr(), out_stride, lse.data_ptr(),
                                  None if weights is None else weights.data_ptr(), workspace.data_ptr(),
                                  workspace.numel() * workspace.itemsize, d_error or None, handle)
@@ -1028,7 +1037,8 @@ def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_len
     cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     torch = _KV8[0]
     _kv8_int32(block_tables, new_block_tables, seq_lens)
-    n, budget = seq_lens.numel(), int(budget)
+    n, budget = seq_lens.numel(), _kv8_size(budget, "budget")
+    keep_first, keep_last = _kv8_size(keep_first, "keep_first"), _kv8_size(keep_last, "keep_last")
     old, new = block_tables.shape, new_block_tables.shape
     if not (len(old) == 2 and len(new) == 2 and old[0] >= n and new[0] >= n):
         raise ValueError("block_tables and new_block_tables are [n, width]")
@@ -1051,8 +1061,8 @@ def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_len
         kept = _kv8_make((n, max(budget, 0)), torch.int32, seq_lens.device, stream, handle)
     rc = lib().pkv_kv8_evict(C.byref(cache), weights.data_ptr(), block_tables.data_ptr(), old[1],
                              seq_lens.data_ptr(), n, new_block_tables.data_ptr(), new[1], budget,
-                             int(keep_first), int(keep_last), new_seq_lens.data_ptr(), kept.data_ptr(),
-                             d_error or None, handle)
+                             keep_first, keep_last, new_seq_lens.data_ptr(), kept.data_ptr(), d_error or None,
+                             handle)
     if rc != OK:
         if check:
             raise PkvError(rc, "pkv_kv8_evict")

@@ -235,3 +235,18 @@ def test_a_workspace_with_gaps_is_refused(monkeypatch):
         calls()[1](workspace=torch.zeros(8192, dtype=torch.uint8)[::2], stream=0, lse=torch.zeros(3, 8),
                    out=torch.zeros(3, 8, 128).bfloat16())
     assert len(fake.seen) == 1
+
+
+@pytest.mark.parametrize("which,kw", [(1, dict(window=2 ** 32 + 5)), (1, dict(window=-2 ** 32 + 5)), (2, dict(keep_first=2 ** 32 + 1)),
+                                      (2, dict(keep_last=2 ** 33)), (1, dict(window=2 ** 31))])
+def test_sizes_past_32_bits_are_refused(which, kw, monkeypatch):
+    """Not taken by their low 32 bits."""
+    fake = FakeDevices(monkeypatch)
+    monkeypatch.setattr(_lib, "_kv8_device", lambda *a: 0)
+    monkeypatch.setattr(_lib, "_kv8_stream", lambda stream, device: 0)
+    calls()[which]()
+    reached = len(fake.seen)
+    assert reached > 0
+    with pytest.raises(ValueError):
+        calls()[which](**kw)
+    assert len(fake.seen) == reached
