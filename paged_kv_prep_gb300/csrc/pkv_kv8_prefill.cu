@@ -65,7 +65,7 @@ struct Smem {
     uint32_t tmem;
     int32_t failed;
     int32_t nan_seen;                   // this CTA has met a V code that is NaN,
-    uint32_t nan_units[32];             // in units of these numbers, modulo 1024
+    uint8_t nan_units[1024];            // in units of these numbers, modulo 1024
 };
 
 // The keys that rows f0 .. of a tile see: [lo, hi), and the 16-aligned start of their units.
@@ -317,12 +317,12 @@ __device__ __forceinline__ uint32_t nan_bytes(uint4 v) {
 // Which of a row's dimensions 32 c .. + 31 (at `values` within a line) meet a NaN value: its tokens s0 .. s1 - 1,
 // of which those from `a` on are in units numbered from `unit` on, where the converting warps met one.  (Looked
 // for in all of a long context, one NaN would hold its rows up for longer than the other warps wait.)
-__device__ __noinline__ uint32_t nan_dims(const AttnParams &p, const uint32_t *units, const int32_t *table, const uint8_t *values,
+__device__ __forceinline__ uint32_t nan_dims(const AttnParams &p, const uint8_t *units, const int32_t *table, const uint8_t *values,
                                              int64_t line, uint32_t unit, int a, int s0, int s1) {
     uint32_t hit = 0;
 #pragma unroll 1
     for (; a < s1 && hit != ~0u; a += kKeys, unit++) {
-        if (!((*static_cast<const volatile uint32_t *>(&units[(unit >> 5) & 31]) >> (unit & 31)) & 1)) continue;
+        if (!*static_cast<const volatile uint8_t *>(&units[unit & 1023])) continue;
 #pragma unroll 1
         for (int g = a; g < a + kKeys; g += 16) {
             if (g + 16 <= s0 || g >= s1) continue;
@@ -602,7 +602,7 @@ __device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
                 for (int r = 0; r < kStep; r++) fetch(cache, b, r0 + r, raw);
         }
         if (nan) {
-            atomicOr(&sm->nan_units[(unit >> 5) & 31], 1u << (unit & 31));
+            *static_cast<volatile uint8_t *>(&sm->nan_units[unit & 1023]) = 1;
             *static_cast<volatile int32_t *>(&sm->nan_seen) = 1;
         }
         cp_commit();
@@ -753,9 +753,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const AttnPara
         mbar_init(&sm->done, 1);
         sm->failed = 0;
         sm->nan_seen = 0;
-        for (int k = 0; k < 32; k++) sm->nan_units[k] = 0;
         fence_mbar_init();
     }
+    for (int k = threadIdx.x; k < 1024; k += kThreads) sm->nan_units[k] = 0;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
