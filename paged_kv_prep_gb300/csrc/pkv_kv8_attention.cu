@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
                 int nt = team;
                 if constexpr (kT < 8) {
                     // two tiles of rows at a time where nothing is masked: twice the independent products (three
-                    // chunks 326 us, a tile at a time 375)
+                    // chunks 518 us with the attention, a tile at a time 537)
 #pragma unroll 1
                     for (; chunk_whole && nt + kTeams < kWRows<D, kT> / 8 && f + 8 * (nt + kTeams) + 8 <= x.f1; nt += 2 * kTeams) {
                         float c[2][kSubs][4];
@@ -463,8 +463,8 @@ int launch_weights_as(const AttnParams &p, const Packed &packed, int mates, int 
     attr[1].val.clusterDim.x = static_cast<unsigned>(mates);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
-    // Clusters that become resident while the packing still runs end up unevenly placed: three chunks'
-    // weights took 702 us with the early start and 500 us without it.
+    // Clusters that become resident while the packing still runs end up unevenly placed: three chunks
+    // took 608 us with the early start and 518 us without it, the attention included.
     cfg.attrs = mates == 1 ? attr : attr + 1;
     cfg.numAttrs = mates == 1 ? 2 : 1;
     // Every cluster takes one stretch of the units, so no more of them are started than run at once
@@ -590,9 +590,9 @@ int pkv_kv8_attention(const pkv_kv8_cache *cache, const void *q, int64_t q_strid
     const bool prefill = cache->head_dim <= 128 && p.bs % 16 == 0 &&
                          static_cast<int64_t>(num_tokens - n + 1) * p.G > pkv::kPrefillRows && num_tokens > n;
     // Tables of at most 256 tokens (eight units) and tiles enough for two warps an SM: a warp takes a
-    // whole row tile, and no merge follows.  Contexts of 100 to 200 tokens, 8 KV heads, cut / whole: 8
-    // requests 14.3 / 19.2 us, 64 requests 24.2 / 19.5, 512 requests 63.8 / 48.9; contexts of 250 to 500,
-    // 64 requests 28.3 / 33.0.
+    // whole row tile, and no merge follows.  Contexts of 100 to 200 tokens, 8 KV heads of 4 query heads,
+    // cut / whole: 8 requests 13.7 / 18.7 us, 64 requests 20.3 / 18.8, 512 requests 55.2 / 48.6; contexts of
+    // 250 to 500, 64 requests 24.2 / 32.0.  The host knows no lengths: short requests in wide tables are cut.
     p.whole = static_cast<int64_t>(p.W) * p.bs <= 256 && static_cast<int64_t>(n) * p.Hkv >= 2 * sms;
     p.short_rows = prefill ? pkv::kPrefillRows : 0x7fffffff;
     // one 8-row tile holds every request of a pure decode step

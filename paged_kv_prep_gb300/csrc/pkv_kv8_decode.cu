@@ -23,9 +23,8 @@
 // 4.3 TB/s with or without its arithmetic.
 // A range that ends inside a request leaves a partial result (R, sum, O) that
 // a second kernel merges in a fixed order.
-// Measured: 256 single tokens on contexts up to 8192 (2.1 GB, floor 312 us) 381 to
-// 390 us with the merge, 5.4 to 5.5 TB/s; the kernel alone 5.45 TB/s, 80 % of the
-// measured copy rate.  Without its arithmetic it reaches 5.7 TB/s.
+// Measured: 256 single tokens on contexts up to 8192 (2.1 GB, floor 316 us) 377 to
+// 389 us with the merge, 5.4 to 5.6 TB/s, 81 to 84 % of the measured copy rate.  Without its arithmetic it reaches 5.7 TB/s.
 #include "pkv_kv8_attention.cuh"
 
 namespace pkv {
@@ -542,7 +541,7 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv8_decode_kernel(c
 constexpr int kMergeThreads = 256;
 
 // kBatch: partial rows on their way at a time.  Sixteen for the long chains of a few decodes (four long
-// ones 135 us, with eight 140), eight for a full batch (256 decodes 372 us, with sixteen 382: fewer
+// ones 139 us, with eight 144), eight for a full batch (256 decodes 389 us, with sixteen 398: fewer
 // warps resident), two for the thousands of rows of row tiles, mostly of two pieces.
 template <int D, int kBatch>
 __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnParams p, int rows, int workers, int stride) {

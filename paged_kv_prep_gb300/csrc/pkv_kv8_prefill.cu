@@ -27,8 +27,8 @@
 // for a merge in a fixed order.
 //
 // Measured: 913 GFLOP of chunks (2 x 2048 tokens, 4 heads a group, contexts up to
-// 16384) 810 us, 1.13 PFLOP/s, 59 % of the measured rate, the tensor pipe active
-// 47 % of the time.  A unit takes about 4150 cycles against 2048 of products: the
+// 16384) 803 us, 1.14 PFLOP/s, 58 % of the measured rate, the tensor pipe active
+// 48 % of the time.  A unit takes about 4150 cycles against 2048 of products: the
 // way from a tile's scores through its softmax (2100 cycles at two warps a
 // scheduler) and back into its next scores is longer than the other tile's
 // products.  Not kept: a second issuing warp (1020 us), eight converting warps

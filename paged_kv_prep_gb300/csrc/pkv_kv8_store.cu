@@ -23,7 +23,7 @@
 // shared memory as integers (order-free); one barrier stands between them and
 // the rounding.
 // Measured (16384 tokens, 4096 of them first in their run, 8 heads x 128, bf16;
-// 101 MB, floor 14.9 us): 41 us; reading the runs' slots and scales, the two
+// 101 MB, floor 15.1 us): 41 us; reading the runs' slots and scales, the two
 // barriers and the integer work around eight elements a lane hold it there
 // (0.55 instructions issued a cycle).  One search of the runs per segment: 46 us;
 // without holding the lines past the chunk in registers: 58 us.
