@@ -950,25 +950,28 @@ def kv8_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, d_error=No
     return rc
 
 
-_KV8_WORKSPACE = {}      # bytes by the sizes they depend on
-
-
 def kv8_attention_workspace(num_tokens, num_q_heads, head_dim, with_weights=False):
     """Bytes of device workspace an attention call on the current device takes
     (``pkv_kv8_attention_workspace``)."""
-    # without weights the size does not depend on the number of tokens; it goes by the device's SMs
-    key = (_kv8_types()[0].cuda.current_device(), num_q_heads, head_dim)
-    found = None if with_weights else _KV8_WORKSPACE.get(key)
-    if found is not None:
-        return found
     n = C.c_int64(0)
     rc = lib().pkv_kv8_attention_workspace(int(num_tokens), int(num_q_heads), int(head_dim),
                                            int(bool(with_weights)), C.byref(n))
     if rc != OK:
         raise PkvError(rc, "pkv_kv8_attention_workspace")
-    if not with_weights:
-        _KV8_WORKSPACE[key] = n.value
     return n.value
+
+
+_KV8_WORKSPACE = {}      # bytes of calls without weights, which do not go by the number of tokens
+
+
+def _kv8_workspace(device, num_tokens, num_q_heads, head_dim, with_weights):
+    if with_weights:
+        return kv8_attention_workspace(num_tokens, num_q_heads, head_dim, True)
+    key = (device, num_q_heads, head_dim)        # by the device: its SMs
+    found = _KV8_WORKSPACE.get(key)
+    if found is None:
+        found = _KV8_WORKSPACE[key] = kv8_attention_workspace(num_tokens, num_q_heads, head_dim)
+    return found
 
 
 def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_start_loc, seq_lens,
@@ -980,7 +983,8 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     query_start_loc [n + 1] and seq_lens [n] as prepare_batch gives them.  window: a query sees
     that many positions, its own among them (0: all).  weights: float32 [num_slots], each token's
     softmax weight is added to it.  out, lse, workspace (uint8, kv8_attention_workspace bytes) are
-    allocated when not given.  Returns (out, lse); lse is float32 [tokens, q_heads]."""
+    allocated when not given, on `stream` where one is.  Every tensor is on one CUDA device.  Returns
+    (out, lse); lse is float32 [tokens, q_heads]."""
     cache = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     torch, _, f32 = _KV8[:3]
     _kv8_int32(block_tables, query_start_loc, seq_lens)
@@ -1014,7 +1018,7 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     if lse is None:
         lse = _kv8_make((T, hq), f32, q.device, stream, handle)
     if workspace is None:
-        size = kv8_attention_workspace(T, hq, d, weights is not None)
+        size = _kv8_workspace(device, T, hq, d, weights is not None)
         workspace = _kv8_make(size, torch.uint8, q.device, stream, handle, returned=False)
     rc = lib().pkv_kv8_attention(C.byref(cache), q.data_ptr(), q_stride, kind, hq, block_tables.data_ptr(),
                                  table[1], query_start_loc.data_ptr(), seq_lens.data_ptr(), n, T,

@@ -218,11 +218,19 @@ def test_the_operands_device_is_current_in_the_call(which, monkeypatch):
 
 def test_workspace_sizes_go_by_the_device(monkeypatch):
     fake = FakeDevices(monkeypatch)
-    assert pkv.kv8_attention_workspace(4, 8, 128) == 1000
-    fake.now = 1
-    assert pkv.kv8_attention_workspace(4, 8, 128) == 2000
-    fake.now = 0
-    assert pkv.kv8_attention_workspace(9, 8, 128) == 1000 and len(fake.seen) == 2
+    for device, tokens, want in ((0, 4, 1000), (1, 4, 2000), (0, 9, 1000), (1, 9, 2000)):
+        fake.now = device
+        assert _lib._kv8_workspace(device, tokens, 8, 128, False) == want
+    assert len(fake.seen) == 2
+    assert _lib._kv8_workspace(0, 4, 8, 128, True) == 2000 and len(fake.seen) == 3    # asked each time
+
+
+@pytest.mark.parametrize("args", [(-1, 8, 128), (4, 0, 128), (4, 8, 96)])
+def test_workspace_refusals(args):
+    """The library's own, also where there is no device."""
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.kv8_attention_workspace(*args)
+    assert e.value.code == pkv.ERR_INVALID_ARG
 
 
 def test_a_workspace_with_gaps_is_refused(monkeypatch):
