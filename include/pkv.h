@@ -676,6 +676,161 @@ int pkv_kv8_evict(const pkv_kv8_cache *cache, float *weights, const int32_t *blo
                   int32_t keep_first, int32_t keep_last, int32_t *new_seq_lens, int32_t *kept,
                   int32_t *d_error, pkv_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Appending with the rotation by position applied on the way
+ * ---------------------------------------------------------------------------
+ * Rotary positions.  The first rot_dim elements of every query and key head are
+ * rotated pair by pair; the rest, and the values, pass unchanged.  Pair i
+ * (0 <= i < rot_dim / 2) consists of the elements i and i + rot_dim / 2, or of 2i
+ * and 2i + 1 (interleaved).  A token has num_axes positions (one, or for images
+ * and video its time, row and column); pair i goes by axis pair_axes[i]:
+ *   c = table[p][i], s = table[p][rot_dim / 2 + i], p = positions[pair_axes[i]][token]
+ *   (x0, x1) -> (x0 c - x1 s, x1 c + x0 s)
+ * in fp32, every product and sum rounded to nearest by itself.
+ *   table:     device float32 [max_position][rot_dim], 16-byte aligned: cosines, then sines
+ *              (any scaling of the rotation is in it);
+ *   positions: device int32, axis a's at positions + a * axis_stride (pkv_prepare_batch's
+ *              positions for one axis);
+ *   pair_axes: host [rot_dim / 2], NULL: all 0.  Read before the call returns.
+ * rot_dim is a multiple of 16, at most head_dim; 1 <= num_axes <= 8.  A token with a
+ * position outside [0, max_position) on any axis sets PKV_DEVERR_POSITION and is
+ * left alone: its query is not written and its lines are not stored.
+ */
+typedef struct {
+    const float *table;
+    const int32_t *positions;
+    const uint8_t *pair_axes;
+    int64_t axis_stride;           /* elements between the axes' positions */
+    int32_t max_position;
+    int32_t rot_dim;
+    int32_t num_axes;
+    int32_t interleaved;
+} pkv_rope;
+
+/*
+ * Rotate a step's keys (and queries) and store the lines at their slots.
+ *   k, v: device, PKV_BF16 or PKV_FP16 (dtype), token t's num_heads * head_dim elements at
+ *   k + t * k_stride_bytes; head_dim is 64, 128 or 256;
+ *   q, q_out: [num_q_heads][head_dim] a token, strides likewise; q_out may be q itself.
+ *   num_q_heads 0: no queries;
+ *   k_cache, v_cache: num_slots lines of num_heads * head_dim elements of dtype;
+ *   slot_mapping: as in pkv_kv_cache_write (-1: not stored; the query is rotated all the same).
+ * Pointers and strides are multiples of 16 bytes (PKV_ERR_ALIGN).  One launch, capturable.
+ */
+int pkv_rope_store(const pkv_rope *rope, const void *k, const void *v, int64_t k_stride_bytes,
+                   int64_t v_stride_bytes, int32_t num_heads, int32_t head_dim, int32_t dtype,
+                   const void *q, int64_t q_stride_bytes, int32_t num_q_heads, void *q_out,
+                   int64_t q_out_stride_bytes, void *k_cache, void *v_cache, int64_t num_slots,
+                   const int64_t *slot_mapping, int32_t num_tokens, int32_t *d_error,
+                   pkv_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * A paged cache held in 4 bits
+ * ---------------------------------------------------------------------------
+ * Elements are e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; the sign is
+ * bit 3), and every 16 of them along a line have one e4m3 scale: a value is
+ * code * scale * unit, with one unit for all keys and one for all values.
+ *   k_cache, v_cache: [num_blocks][num_heads][block_size][head_dim / 2] bytes, the even
+ *                     element in the low four bits;
+ *   k_scale, v_scale: [num_blocks][num_heads][block_size][head_dim / 16] bytes.
+ * So the lines of one block and head stand next to each other.  head_dim is 64, 128 or
+ * 256; block_size a multiple of 16; num_heads (KV heads) at most 1024; fewer than 2^32
+ * slots; pointers 16-byte aligned; units in [2^-64, 2^64].  Value scales are never NaN
+ * (pkv_kv4_store makes none); a NaN key scale gives NaN keys.
+ */
+typedef struct {
+    void *k_cache;
+    void *v_cache;
+    void *k_scale;
+    void *v_scale;
+    int64_t num_blocks;
+    int32_t block_size;
+    int32_t num_heads;
+    int32_t head_dim;
+    float k_unit;
+    float v_unit;
+} pkv_kv4_cache;
+
+/*
+ * Quantise a step's K and V lines into their slots, keys (and queries) rotated on the
+ * way (rope NULL: not).  Arguments as in pkv_rope_store; q needs rope.
+ * For 16 elements x (fp32 after the rotation): scale = e4m3(max |x| / (6 unit)) and
+ * code = e2m1(x / (scale * unit)), both to nearest even and saturating (an infinity
+ * becomes the largest value); a scale of 0 gives codes 0.  A NaN key makes its scale
+ * NaN.  A NaN value makes the first key scale of its token and head NaN, and its own
+ * scale 0: every query that sees the token gives NaN, and no other.
+ * One launch, capturable.
+ */
+int pkv_kv4_store(const pkv_kv4_cache *cache, const pkv_rope *rope, const void *k, const void *v,
+                  int64_t k_stride_bytes, int64_t v_stride_bytes, int32_t dtype, const void *q,
+                  int64_t q_stride_bytes, int32_t num_q_heads, void *q_out,
+                  int64_t q_out_stride_bytes, const int64_t *slot_mapping, int32_t num_tokens,
+                  int32_t *d_error, pkv_stream_t stream);
+
+/*
+ * Read the lines of slots[0 .. count) (device int64) back: k, v [count][num_heads]
+ * [head_dim] of dtype, contiguous, 16-byte aligned (v or k NULL: not written).  A
+ * negative slot gives zeros; one past the cache does too and sets PKV_DEVERR_SLOT.
+ */
+int pkv_kv4_load(const pkv_kv4_cache *cache, const int64_t *slots, int32_t count, int32_t dtype,
+                 void *k, void *v, int32_t *d_error, pkv_stream_t stream);
+
+/* Bytes of device workspace that pkv_kv4_attention takes on the current device.  Its
+   contents need no initialisation and it may be reused by the next call on the same
+   stream; calls that may run at the same time take one each. */
+int pkv_kv4_attention_workspace(int32_t head_dim, int64_t *bytes);
+
+/*
+ * Attention of a prepared batch's queries over the 4-bit cache.  Everything is as in
+ * pkv_kv8_attention (without its weights): which positions a query sees, rows that
+ * see nothing, device errors, the layout of q, out and lse.
+ * The products' operands are f16: a value without its unit (code * scale, six bits) and a
+ * query after scaling its row by a power of two are exact in it, a softmax weight is
+ * rounded; sums and softmax statistics are fp32.
+ */
+int pkv_kv4_attention(const pkv_kv4_cache *cache, const void *q, int64_t q_stride_bytes,
+                      int32_t dtype, int32_t num_q_heads, const int32_t *block_tables,
+                      int32_t table_width, const int32_t *query_start_loc,
+                      const int32_t *seq_lens, int32_t n, int32_t num_tokens,
+                      float softmax_scale, int32_t window, void *out, int64_t out_stride_bytes,
+                      float *lse, void *workspace, int64_t workspace_bytes, int32_t *d_error,
+                      pkv_stream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Verification of drafted tokens
+ * ---------------------------------------------------------------------------
+ * Request i has the rows query_start_loc[i] .. query_start_loc[i + 1] - 1: one for each
+ * of its drafted tokens and a last one for the token after them.  Row r of target_probs
+ * is the target's distribution of the token after r; draft_ids[r] is the token drafted
+ * there and row r of draft_probs the distribution it was drawn from (neither is
+ * read for a request's last row; draft_probs NULL: drafts are certain, q = 1).
+ * Draft r stands if the ones before it do and uniforms[r] * q(draft) < p(draft).  The
+ * token after the last one that stands is drawn from the weights
+ *   max(0, p - q)          at a rejected draft (without draft_probs: p with the draft at 0),
+ *   p                      after the last row, or where the former are all 0:
+ * the first token whose weights, added up from token 0, exceed u times their total, u =
+ * uniforms of the request's last row.  Weights are fp32 differences, at most 1 (NaN
+ * counts as 0), and are added up as whole multiples of 2^-40 (to nearest even), so that
+ * the result does not depend on an order; u times the total is rounded once to fp64.
+ *   target_probs, draft_probs: dtype PKV_BF16, PKV_FP16 or PKV_FP32, [num_rows][vocab],
+ *       rows *_stride elements apart; uniforms: float32 in [0, 1);
+ *   tokens [n][max_drafts + 1]: the drafts that stand, the drawn token, then -1;
+ *   accepted [n]: how many drafts stand.
+ * A draft outside the vocabulary is rejected.  A row without a positive weight gives -1
+ * for its token.  A request without rows gives 0 and -1; one whose rows leave the
+ * batch, descend or are more than max_drafts + 1 does too and sets PKV_DEVERR_COUNT.
+ * One launch, no workspace, capturable.
+ */
+#define PKV_FP32 2
+int pkv_verify_drafts(const void *target_probs, int64_t target_stride, const void *draft_probs,
+                      int64_t draft_stride, int32_t dtype, int32_t vocab, int32_t num_rows,
+                      const int32_t *draft_ids, const int32_t *query_start_loc, int32_t n,
+                      const float *uniforms, int32_t max_drafts, int32_t *tokens,
+                      int32_t *accepted, int32_t *d_error, pkv_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,7 +16,7 @@ from ._lib import (  # noqa: F401
     ERR_NOT_ACTIVE, EXPORTS, MAX_BATCH, MAX_GROUPS, OK, Batch, KvStepCall, KvStoreCall,
     PkvError, PrefixCache, PrepareDeviceCall, PrepareHostCall, State, kv_cache_write, kv_cache_write_layers,
     kv_cache_write_step, kv8_attention, kv8_attention_workspace, kv8_evict, kv8_store, lib,
-    selftest_wait_timeout,
+    kv4_attention, kv4_attention_workspace, kv4_load, kv4_store, rope_store, selftest_wait_timeout, verify_drafts,
 )
 
 __version__ = "0.1.0"

@@ -57,7 +57,8 @@ EXPORTS = [
     "pkv_pool_read", "pkv_allocate_slots", "pkv_release_blocks", "pkv_get_error",
     "pkv_state_error_word", "pkv_row_info", "pkv_read_row", "pkv_last_cuda_error",
     "pkv_version", "pkv_selftest_wait_timeout", "pkv_kv8_store", "pkv_kv8_attention_workspace",
-    "pkv_kv8_attention", "pkv_kv8_evict",
+    "pkv_kv8_attention", "pkv_kv8_evict", "pkv_rope_store", "pkv_kv4_store", "pkv_kv4_load",
+    "pkv_kv4_attention_workspace", "pkv_kv4_attention", "pkv_verify_drafts",
 ]
 
 
@@ -104,6 +105,19 @@ class Kv8CacheArgs(C.Structure):
     _fields_ = [("k_cache", C.c_void_p), ("v_cache", C.c_void_p), ("k_scale", C.c_void_p),
                 ("v_scale", C.c_void_p), ("num_blocks", C.c_int64), ("block_size", C.c_int32),
                 ("num_heads", C.c_int32), ("head_dim", C.c_int32)]
+
+
+class Kv4CacheArgs(C.Structure):
+    _fields_ = [("k_cache", C.c_void_p), ("v_cache", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("num_blocks", C.c_int64), ("block_size", C.c_int32),
+                ("num_heads", C.c_int32), ("head_dim", C.c_int32), ("k_unit", C.c_float),
+                ("v_unit", C.c_float)]
+
+
+class RopeArgs(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("positions", C.c_void_p), ("pair_axes", C.c_char_p),
+                ("axis_stride", C.c_int64), ("max_position", C.c_int32), ("rot_dim", C.c_int32),
+                ("num_axes", C.c_int32), ("interleaved", C.c_int32)]
 
 
 _P32 = C.POINTER(C.c_int32)
@@ -154,6 +168,15 @@ def _declare(lib):
                               i32, C.c_float, i32, _VP, i64, _VP, _VP, _VP, i64, _VP, _VP],
         "pkv_kv8_evict": [C.POINTER(Kv8CacheArgs), _VP, _VP, i32, _VP, i32, _VP, i32, i32, i32, i32,
                           _VP, _VP, _VP, _VP],
+        "pkv_rope_store": [C.POINTER(RopeArgs), _VP, _VP, i64, i64, i32, i32, i32, _VP, i64, i32, _VP, i64,
+                           _VP, _VP, i64, _VP, i32, _VP, _VP],
+        "pkv_kv4_store": [C.POINTER(Kv4CacheArgs), C.POINTER(RopeArgs), _VP, _VP, i64, i64, i32, _VP, i64,
+                          i32, _VP, i64, _VP, i32, _VP, _VP],
+        "pkv_kv4_load": [C.POINTER(Kv4CacheArgs), _VP, i32, i32, _VP, _VP, _VP, _VP],
+        "pkv_kv4_attention_workspace": [i32, C.POINTER(i64)],
+        "pkv_kv4_attention": [C.POINTER(Kv4CacheArgs), _VP, i64, i32, i32, _VP, i32, _VP, _VP, i32, i32,
+                              C.c_float, i32, _VP, i64, _VP, _VP, i64, _VP, _VP],
+        "pkv_verify_drafts": [_VP, i64, _VP, i64, i32, i32, i32, _VP, _VP, i32, _VP, i32, _VP, _VP, _VP, _VP],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -1072,3 +1095,306 @@ def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_len
             raise PkvError(rc, "pkv_kv8_evict")
         return rc
     return new_seq_lens, kept
+
+
+# -- appending with the rotation by position ----------------------------------
+
+
+def _rope_args(positions, table, axes, interleaved, tokens):
+    """The C view of a rotation, and what it points to."""
+    f32, i32 = _kv8_types()[2:4]
+    shape = positions.shape
+    if not (positions.dtype is i32 and len(shape) in (1, 2) and shape[-1] >= tokens):
+        raise ValueError("positions is int32 [tokens] or [axes, tokens]")
+    if positions.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError("an axis's positions are contiguous")
+    if not (table.dtype is f32 and table.dim() == 2 and table.is_contiguous()):
+        raise ValueError("table is contiguous float32 [max_position, rot_dim]: cosines, then sines")
+    count = shape[0] if len(shape) == 2 else 1
+    rows, rot = table.shape
+    if axes is not None:
+        axes = bytes(axes)
+        if len(axes) != rot // 2:
+            raise ValueError("axes has a row of positions for each of the rot_dim / 2 pairs")
+    return RopeArgs(table.data_ptr(), positions.data_ptr(), axes, positions.stride(0) if count > 1 else 0,
+                    _kv8_size(rows, "max_position"), rot, count, int(bool(interleaved)))
+
+
+def _append_rows(k, v, q, q_out, slot_mapping, heads, dim):
+    """Checks what a step appends; (tokens, type, strides of k, v, q and q_out in bytes, query heads)."""
+    T = slot_mapping.numel()
+    if not (slot_mapping.dtype is _kv8_types()[4] and slot_mapping.is_contiguous()):
+        raise ValueError("slot_mapping is contiguous int64")
+    if not (k.dtype is v.dtype and k.shape == v.shape and k.shape[0] >= T):
+        raise ValueError("k and v have the same shape and type, a row for each slot")
+    kind = _kv8_dtype(k)
+    k_stride, v_stride = _kv8_rows(k, heads * dim, "k"), _kv8_rows(v, heads * dim, "v")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        return T, kind, k_stride, v_stride, 0, 0, 0
+    shape = q.shape
+    if not (len(shape) == 3 and shape[2] == dim and shape[0] >= T and q.dtype is k.dtype):
+        raise ValueError("q is [tokens, q_heads, head_dim] of k's type, a row for each slot")
+    if q_out is not None and not (q_out.shape == shape and q_out.dtype is q.dtype):
+        raise ValueError("q_out has q's shape and type")
+    width = shape[1] * dim
+    return (T, kind, k_stride, v_stride, _kv8_rows(q, width, "q"),
+            width * 2 if q_out is None else _kv8_rows(q_out, width, "q_out"), shape[1])
+
+
+def rope_store(k, v, k_cache, v_cache, slot_mapping, positions, table, axes=None, interleaved=False,
+               q=None, q_out=None, d_error=None, stream=None, check=True):
+    """Rotate a step's keys (and queries) by position and store K and V at their slots in a 16-bit
+    paged cache (``pkv_rope_store``).
+
+    k, v: bfloat16 or float16 [tokens, heads, head_dim], token stride allowed; k_cache, v_cache: the
+    same type, contiguous [num_slots, heads, head_dim] (or [num_slots, heads * head_dim]);
+    slot_mapping: int64, -1: not stored; positions: int32 [tokens] or [axes, tokens]; table: float32
+    [max_position, rot_dim], cosines then sines; axes: the row of positions that each of the rot_dim /
+    2 pairs goes by (None: the first); interleaved: pairs are neighbouring elements.  q: [tokens,
+    q_heads, head_dim], rotated into q_out (allocated when not given; may be q).  Returns q_out (None
+    without q)."""
+    torch = _kv8_types()[0]
+    if not (len(k.shape) == 3 and k_cache.shape == v_cache.shape and k_cache.dtype is k.dtype and
+            v_cache.dtype is k.dtype and k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("k is [tokens, heads, head_dim], the caches contiguous and of its type")
+    heads, dim = k.shape[1:]
+    slots, size = k_cache.shape[0], k_cache.numel()
+    if size != slots * heads * dim:
+        raise ValueError("the caches hold num_slots lines of heads * head_dim elements")
+    T, kind, ks, vs, qs, os_, hq = _append_rows(k, v, q, q_out, slot_mapping, heads, dim)
+    rope = _rope_args(positions, table, axes, interleaved, T)
+    device = _kv8_device(stream, k_cache, v_cache, k, v, slot_mapping, positions, table, q, q_out)
+    if _kv8_elsewhere(device):
+        with torch.cuda.device(device):
+            return rope_store(k, v, k_cache, v_cache, slot_mapping, positions, table, axes, interleaved, q, q_out,
+                              d_error, stream, check)
+    handle = _kv8_stream(stream, device)
+    if q is not None and q_out is None:
+        q_out = _kv8_make(q.shape, q.dtype, q.device, stream, handle)
+    rc = lib().pkv_rope_store(C.byref(rope), k.data_ptr(), v.data_ptr(), ks, vs, heads, dim, kind,
+                              None if q is None else q.data_ptr(), qs, hq, None if q is None else q_out.data_ptr(), os_,
+                              k_cache.data_ptr(), v_cache.data_ptr(), slots, slot_mapping.data_ptr(), T,
+                              d_error or None, handle)
+    if rc != OK:
+        if check:
+            raise PkvError(rc, "pkv_rope_store")
+        return rc
+    return q_out
+
+
+# -- the cache held in 4 bits -------------------------------------------------
+
+
+def _kv4_cache(k_cache, v_cache, k_scale, v_scale, k_unit, v_unit):
+    """The C view of a 4-bit cache: codes [num_blocks, heads, block_size, head_dim / 2] and scales
+    [num_blocks, heads, block_size, head_dim / 16], one byte an element."""
+    _kv8_types()                # a call's first use: from here on _KV8 is set
+    shape, scales = k_cache.shape, k_scale.shape
+    if not (len(shape) == 4 and v_cache.shape == shape and v_scale.shape == scales and
+            scales[:3] == shape[:3] and len(scales) == 4 and shape[3] == 8 * scales[3]):
+        raise ValueError("the caches are [num_blocks, heads, block_size, head_dim / 2], the scales "
+                         "[num_blocks, heads, block_size, head_dim / 16]")
+    for t in (k_cache, v_cache, k_scale, v_scale):
+        if not (t.itemsize == 1 and t.is_contiguous()):
+            raise ValueError("caches and scales are contiguous, one byte an element")
+    return Kv4CacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                        shape[0], shape[2], shape[1], 2 * shape[3], float(k_unit), float(v_unit))
+
+
+def kv4_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, positions=None, table=None, axes=None,
+              interleaved=False, q=None, q_out=None, k_unit=1.0, v_unit=1.0, d_error=None, stream=None,
+              check=True):
+    """Quantise a step's K and V lines into the 4-bit cache, keys (and queries) rotated on the way
+    (``pkv_kv4_store``; the rotation as in ``rope_store``, left out where positions and table are).
+
+    k_cache, v_cache: one byte an element, [num_blocks, heads, block_size, head_dim / 2]; k_scale,
+    v_scale: [num_blocks, heads, block_size, head_dim / 16] (uint8 or float8_e4m3fn); k_unit, v_unit:
+    what all keys' and all values' scales are multiplied with.  Returns q_out (None without q)."""
+    cache = _kv4_cache(k_cache, v_cache, k_scale, v_scale, k_unit, v_unit)
+    heads, dim = cache.num_heads, cache.head_dim
+    T, kind, ks, vs, qs, os_, hq = _append_rows(k, v, q, q_out, slot_mapping, heads, dim)
+    if (positions is None) != (table is None):
+        raise ValueError("positions and table come together")
+    if positions is None and (q is not None or axes is not None):
+        raise ValueError("q and axes need positions and table")
+    rope = None if positions is None else _rope_args(positions, table, axes, interleaved, T)
+    device = _kv8_device(stream, k_cache, v_cache, k_scale, v_scale, k, v, slot_mapping, positions, table, q, q_out)
+    if _kv8_elsewhere(device):
+        with _KV8[0].cuda.device(device):
+            return kv4_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, positions, table, axes,
+                             interleaved, q, q_out, k_unit, v_unit, d_error, stream, check)
+    handle = _kv8_stream(stream, device)
+    if q is not None and q_out is None:
+        q_out = _kv8_make(q.shape, q.dtype, q.device, stream, handle)
+    rc = lib().pkv_kv4_store(C.byref(cache), None if rope is None else C.byref(rope), k.data_ptr(), v.data_ptr(),
+                             ks, vs, kind, None if q is None else q.data_ptr(), qs, hq,
+                             None if q is None else q_out.data_ptr(), os_, slot_mapping.data_ptr(), T,
+                             d_error or None, handle)
+    if rc != OK:
+        if check:
+            raise PkvError(rc, "pkv_kv4_store")
+        return rc
+    return q_out
+
+
+def kv4_load(k_cache, v_cache, k_scale, v_scale, slots, dtype=None, k=None, v=None, k_unit=1.0, v_unit=1.0,
+             d_error=None, stream=None, check=True):
+    """Read the lines of ``slots`` (int64) of the 4-bit cache back as 16-bit values
+    (``pkv_kv4_load``).  dtype: bfloat16 (the default) or float16; k, v: contiguous [slots, heads,
+    head_dim], allocated when not given.  A negative slot gives zeros.  Returns (k, v)."""
+    cache = _kv4_cache(k_cache, v_cache, k_scale, v_scale, k_unit, v_unit)
+    torch = _KV8[0]
+    n = slots.numel()
+    if not (slots.dtype is _KV8[4] and slots.is_contiguous()):
+        raise ValueError("slots is contiguous int64")
+    given = k if k is not None else v
+    if dtype is None:
+        dtype = torch.bfloat16 if given is None else given.dtype
+    kind, shape = _KV8[1].get(dtype), (n, cache.num_heads, cache.head_dim)
+    if kind is None:
+        raise ValueError("bfloat16 or float16")
+    for t in (k, v):
+        if t is not None and not (t.shape == shape and t.dtype is dtype and t.is_contiguous()):
+            raise ValueError("k and v are contiguous [slots, heads, head_dim] of dtype")
+    device = _kv8_device(stream, k_cache, v_cache, k_scale, v_scale, slots, k, v)
+    if _kv8_elsewhere(device):
+        with torch.cuda.device(device):
+            return kv4_load(k_cache, v_cache, k_scale, v_scale, slots, dtype, k, v, k_unit, v_unit, d_error, stream,
+                            check)
+    handle = _kv8_stream(stream, device)
+    if k is None:
+        k = _kv8_make(shape, dtype, k_cache.device, stream, handle)
+    if v is None:
+        v = _kv8_make(shape, dtype, k_cache.device, stream, handle)
+    rc = lib().pkv_kv4_load(C.byref(cache), slots.data_ptr(), _kv8_size(n, "slots"), kind, k.data_ptr(), v.data_ptr(),
+                            d_error or None, handle)
+    if rc != OK:
+        if check:
+            raise PkvError(rc, "pkv_kv4_load")
+        return rc
+    return k, v
+
+
+def kv4_attention_workspace(head_dim):
+    """Bytes of device workspace an attention call on the current device takes
+    (``pkv_kv4_attention_workspace``)."""
+    n = C.c_int64(0)
+    rc = lib().pkv_kv4_attention_workspace(int(head_dim), C.byref(n))
+    if rc != OK:
+        raise PkvError(rc, "pkv_kv4_attention_workspace")
+    return n.value
+
+
+_KV4_WORKSPACE = {}      # bytes, by device (its SMs) and head_dim
+
+
+def kv4_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_start_loc, seq_lens,
+                  softmax_scale=None, window=0, k_unit=1.0, v_unit=1.0, out=None, lse=None, workspace=None,
+                  d_error=None, stream=None, check=True):
+    """Attention of a prepared batch's queries over the 4-bit cache (``pkv_kv4_attention``).
+
+    The cache as in ``kv4_store``; everything else as in ``kv8_attention``, which also adds up weights.
+    workspace: uint8, kv4_attention_workspace bytes.  Returns (out, lse)."""
+    cache = _kv4_cache(k_cache, v_cache, k_scale, v_scale, k_unit, v_unit)
+    torch, _, f32 = _KV8[:3]
+    _kv8_int32(block_tables, query_start_loc, seq_lens)
+    n, table = seq_lens.numel(), block_tables.shape
+    if not (len(table) == 2 and table[0] >= n and query_start_loc.numel() >= n + 1):
+        raise ValueError("block_tables [n, W], query_start_loc [n + 1], seq_lens [n]")
+    shape = q.shape
+    if not (len(shape) == 3 and shape[2] == cache.head_dim):
+        raise ValueError("q is [tokens, q_heads, head_dim]")
+    T, hq, d = shape
+    window = _kv8_size(window, "window")
+    kind, q_stride = _kv8_dtype(q), _kv8_rows(q, hq * d, "q")
+    if out is not None and not (out.shape == shape and out.dtype is q.dtype):
+        raise ValueError("out has q's shape and type")
+    out_stride = hq * d * 2 if out is None else _kv8_rows(out, hq * d, "out")
+    if not (lse is None or lse.shape == (T, hq) and lse.dtype is f32 and lse.is_contiguous()):
+        raise ValueError("lse is contiguous float32 [tokens, q_heads]")
+    if not (workspace is None or workspace.is_contiguous()):
+        raise ValueError("workspace is contiguous")
+    device = _kv8_device(stream, k_cache, v_cache, k_scale, v_scale, q, block_tables, query_start_loc, seq_lens,
+                         out, lse, workspace)
+    if _kv8_elsewhere(device):
+        with torch.cuda.device(device):
+            return kv4_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_start_loc, seq_lens,
+                                 softmax_scale, window, k_unit, v_unit, out, lse, workspace, d_error, stream, check)
+    handle = _kv8_stream(stream, device)
+    if out is None:
+        out = _kv8_make(shape, q.dtype, q.device, stream, handle)
+    if lse is None:
+        lse = _kv8_make((T, hq), f32, q.device, stream, handle)
+    if workspace is None:
+        size = _KV4_WORKSPACE.get((device, d))
+        if size is None:
+            size = _KV4_WORKSPACE[device, d] = kv4_attention_workspace(d)
+        workspace = _kv8_make(size, torch.uint8, q.device, stream, handle, returned=False)
+    rc = lib().pkv_kv4_attention(C.byref(cache), q.data_ptr(), q_stride, kind, hq, block_tables.data_ptr(),
+                                 table[1], query_start_loc.data_ptr(), seq_lens.data_ptr(), n, T,
+                                 d ** -0.5 if softmax_scale is None else float(softmax_scale), window,
+                                 out.data_ptr(), out_stride, lse.data_ptr(), workspace.data_ptr(),
+                                 workspace.numel() * workspace.itemsize, d_error or None, handle)
+    if rc != OK:
+        if check:
+            raise PkvError(rc, "pkv_kv4_attention")
+        return rc
+    return out, lse
+
+
+# -- verification of drafted tokens -------------------------------------------
+
+
+def verify_drafts(target_probs, draft_ids, query_start_loc, uniforms, max_drafts, draft_probs=None,
+                  tokens=None, accepted=None, d_error=None, stream=None, check=True):
+    """Which drafted tokens stand, and the token after them (``pkv_verify_drafts``).
+
+    target_probs: float32, bfloat16 or float16 [rows, vocab], a row for each drafted token of a
+    request and a last one for the token after them; draft_ids: int32, the token drafted at each row
+    (input_ids[1:] of a prepared batch whose requests run one token and their drafts; not read for a
+    request's last row, so rows - 1 entries do); query_start_loc: int32 [n + 1] of the rows; uniforms:
+    float32 [rows] in [0, 1); draft_probs: like target_probs, the distributions the drafts were drawn
+    from (None: drafts are certain).  Rows may be apart by a stride.  Returns (tokens int32 [n,
+    max_drafts + 1]: the drafts that stand, the drawn token, then -1; accepted int32 [n])."""
+    torch, kinds, f32, i32 = _kv8_types()[:4]
+    kind = 2 if target_probs.dtype is f32 else kinds.get(target_probs.dtype)
+    if kind is None or target_probs.dim() != 2:
+        raise ValueError("target_probs is float32, bfloat16 or float16 [rows, vocab]")
+    rows, vocab = target_probs.shape
+    for p in (target_probs, draft_probs):
+        if p is not None and not (p.dtype is target_probs.dtype and p.shape == target_probs.shape and
+                                  (p.stride(1) == 1 or vocab == 1)):
+            raise ValueError("draft_probs has target_probs' shape and type, a row's elements are contiguous")
+    _kv8_int32(draft_ids, query_start_loc)
+    n, max_drafts = query_start_loc.numel() - 1, _kv8_size(max_drafts, "max_drafts")
+    if n < 0 or max_drafts < 0 or draft_ids.numel() < rows - 1:
+        raise ValueError("query_start_loc [n + 1], draft_ids a token for each row but the last")
+    if not (uniforms.dtype is f32 and uniforms.is_contiguous() and uniforms.numel() >= rows):
+        raise ValueError("uniforms is contiguous float32, one for each row")
+    for t, shape in ((tokens, (n, max_drafts + 1)), (accepted, (n,))):
+        if t is not None:
+            _kv8_int32(t)
+            if t.shape != shape:
+                raise ValueError("tokens is [n, max_drafts + 1], accepted [n]")
+    device = _kv8_device(stream, target_probs, draft_probs, draft_ids, query_start_loc, uniforms, tokens, accepted)
+    if _kv8_elsewhere(device):
+        with torch.cuda.device(device):
+            return verify_drafts(target_probs, draft_ids, query_start_loc, uniforms, max_drafts, draft_probs, tokens,
+                                 accepted, d_error, stream, check)
+    handle = _kv8_stream(stream, device)
+    if tokens is None:
+        tokens = _kv8_make((n, max_drafts + 1), i32, target_probs.device, stream, handle)
+    if accepted is None:
+        accepted = _kv8_make(n, i32, target_probs.device, stream, handle)
+    rc = lib().pkv_verify_drafts(target_probs.data_ptr(), target_probs.stride(0) if rows > 1 else vocab,
+                                 None if draft_probs is None else draft_probs.data_ptr(),
+                                 0 if draft_probs is None else draft_probs.stride(0) if rows > 1 else vocab, kind, vocab,
+                                 rows, draft_ids.data_ptr(), query_start_loc.data_ptr(), n, uniforms.data_ptr(),
+                                 max_drafts, tokens.data_ptr(), accepted.data_ptr(), d_error or None, handle)
+    if rc != OK:
+        if check:
+            raise PkvError(rc, "pkv_verify_drafts")
+        return rc
+    return tokens, accepted

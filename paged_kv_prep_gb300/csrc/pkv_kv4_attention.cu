@@ -1,0 +1,98 @@
+// Host side of the attention over the 4-bit paged cache: argument checks, which
+// kernels take which requests.
+#include "pkv_kv4_attention.cuh"
+
+namespace pkv {
+namespace {
+
+int64_t workspace_of(int32_t head_dim, int sms) {
+    const int64_t a = kv4_decode_workspace(head_dim, sms), b = kv4_prefill_workspace(head_dim, sms);
+    return ((a > b ? a : b) + 255) & ~255LL;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+int pkv_kv4_attention_workspace(int32_t head_dim, int64_t *bytes) {
+    if (!bytes || !pkv::kv8_head_dim(head_dim)) return PKV_ERR_INVALID_ARG;
+    int sms = 0;
+    const int rc = pkv::kv8_sm_count(&sms);
+    if (rc != PKV_OK) return rc;
+    *bytes = pkv::workspace_of(head_dim, sms);
+    return PKV_OK;
+}
+
+int pkv_kv4_attention(const pkv_kv4_cache *cache, const void *q, int64_t q_stride_bytes, int32_t dtype,
+                      int32_t num_q_heads, const int32_t *block_tables, int32_t table_width,
+                      const int32_t *query_start_loc, const int32_t *seq_lens, int32_t n, int32_t num_tokens,
+                      float softmax_scale, int32_t window, void *out, int64_t out_stride_bytes, float *lse,
+                      void *workspace, int64_t workspace_bytes, int32_t *d_error, pkv_stream_t stream) {
+    int rc = pkv::kv4_check_cache(cache);
+    if (rc != PKV_OK) return rc;
+    if (n < 0 || n > PKV_MAX_BATCH || num_tokens < 0 || num_tokens >= PKV_MAX_TOKENS ||
+        (dtype != PKV_BF16 && dtype != PKV_FP16) || num_q_heads < 1 || num_q_heads % cache->num_heads ||
+        table_width < 0 || window < 0 || q_stride_bytes < 0 || out_stride_bytes < 0)
+        return PKV_ERR_INVALID_ARG;
+    const int64_t row = 2LL * num_q_heads * cache->head_dim;
+    // (query, head) rows are counted in 32 bits, with room for a last tile
+    if (static_cast<int64_t>(num_tokens) * (num_q_heads / cache->num_heads) >= (1LL << 31) - 1024 || row >= (1LL << 31))
+        return PKV_ERR_INVALID_ARG;
+    if (n == 0 || num_tokens == 0) return PKV_OK;
+    if (!q || !out || !query_start_loc || !seq_lens || (table_width > 0 && !block_tables) || !workspace)
+        return PKV_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(out) & 15) || (q_stride_bytes & 15) ||
+        (out_stride_bytes & 15) || (reinterpret_cast<uintptr_t>(workspace) & 15))
+        return PKV_ERR_ALIGN;
+    if (num_tokens > 1 && (q_stride_bytes < row || out_stride_bytes < row)) return PKV_ERR_INVALID_ARG;
+    int sms = 0;
+    rc = pkv::kv8_sm_count(&sms);
+    if (rc != PKV_OK) return rc;
+    if (workspace_bytes < pkv::workspace_of(cache->head_dim, sms)) return PKV_ERR_INVALID_ARG;
+    pkv::Kv4Params p = {};
+    p.q = static_cast<const char *>(q);
+    p.q_stride = q_stride_bytes;
+    p.out = static_cast<char *>(out);
+    p.out_stride = out_stride_bytes;
+    p.lse = lse;
+    p.kc = static_cast<const uint8_t *>(cache->k_cache);
+    p.vc = static_cast<const uint8_t *>(cache->v_cache);
+    p.k_sf = static_cast<const uint8_t *>(cache->k_scale);
+    p.v_sf = static_cast<const uint8_t *>(cache->v_scale);
+    p.v_unit = cache->v_unit;
+    p.tables = block_tables;
+    p.qsl = query_start_loc;
+    p.lens = seq_lens;
+    p.num_blocks = cache->num_blocks;
+    p.n = n;
+    p.T = num_tokens;
+    p.W = table_width;
+    p.bs = cache->block_size;
+    p.Hkv = cache->num_heads;
+    p.G = num_q_heads / cache->num_heads;
+    p.window = window;
+    p.fp16 = dtype == PKV_FP16;
+    p.scale_log2 = softmax_scale * pkv::kLog2e * cache->k_unit;
+    p.meta = static_cast<int4 *>(workspace);
+    p.part = reinterpret_cast<float *>(p.meta + pkv::kv8_most_workers(sms));
+    p.err = d_error;
+    cudaStream_t s = pkv::as_stream(stream);
+    // The prefill kernel takes the requests with more than kKv4PrefillRows rows.  It needs head_dim <= 128
+    // (two accumulators beside two score tiles in TMEM); otherwise the decode kernel's row tiles take everything.
+    const bool prefill = cache->head_dim <= 128 && num_tokens > n &&
+                         static_cast<int64_t>(num_tokens - n + 1) * p.G > pkv::kKv4PrefillRows;
+    // Tables of at most 256 tokens and tiles enough for two warps an SM: a warp takes a whole row tile, and
+    // no merge follows.
+    p.whole = static_cast<int64_t>(p.W) * p.bs <= 256 && static_cast<int64_t>(n) * p.Hkv >= 2 * sms;
+    p.short_rows = prefill ? pkv::kKv4PrefillRows : 0x7fffffff;
+    // one 8-row tile holds every request of a pure decode step
+    const bool one_tile = num_tokens <= n && p.G <= 8;
+    if (prefill) {
+        rc = pkv::kv4_launch_prefill(p, cache->head_dim, sms, s);
+        if (rc != PKV_OK) return rc;
+    }
+    return pkv::kv4_launch_decode(p, cache->head_dim, one_tile, sms, s);
+}
+
+}  // extern "C"
