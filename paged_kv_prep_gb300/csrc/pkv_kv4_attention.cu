@@ -78,16 +78,19 @@ int pkv_kv4_attention(const pkv_kv4_cache *cache, const void *q, int64_t q_strid
     p.part = reinterpret_cast<float *>(p.meta + pkv::kv8_most_workers(sms));
     p.err = d_error;
     cudaStream_t s = pkv::as_stream(stream);
-    // The prefill kernel takes the requests with more than kKv4PrefillRows rows.  It needs head_dim <= 128
-    // (two accumulators beside two score tiles in TMEM); otherwise the decode kernel's row tiles take everything.
-    const bool prefill = cache->head_dim <= 128 && num_tokens > n &&
-                         static_cast<int64_t>(num_tokens - n + 1) * p.G > pkv::kKv4PrefillRows;
+    // The prefill kernel takes the requests of many rows.  It needs head_dim <= 128 (two accumulators beside two
+    // score tiles in TMEM); otherwise the decode kernel's row tiles take everything.  Where the requests have
+    // many rows on average the step has prompt chunks, and the others are single tokens as a rule: the
+    // decode kernel then takes what fits its eight-row tiles, which go through the cache faster than sixteen.
+    const bool chunks = static_cast<int64_t>(num_tokens) * p.G > 32LL * n && p.G <= 8;
+    const int rows = chunks ? 8 : pkv::kKv4PrefillRows;
+    const bool prefill = cache->head_dim <= 128 && num_tokens > n && static_cast<int64_t>(num_tokens - n + 1) * p.G > rows;
     // Tables of at most 256 tokens and tiles enough for two warps an SM: a warp takes a whole row tile, and
     // no merge follows.
     p.whole = static_cast<int64_t>(p.W) * p.bs <= 256 && static_cast<int64_t>(n) * p.Hkv >= 2 * sms;
-    p.short_rows = prefill ? pkv::kKv4PrefillRows : 0x7fffffff;
-    // one 8-row tile holds every request of a pure decode step
-    const bool one_tile = num_tokens <= n && p.G <= 8;
+    p.short_rows = prefill ? rows : 0x7fffffff;
+    // one 8-row tile holds every request that the decode kernel takes
+    const bool one_tile = (num_tokens <= n && p.G <= 8) || (prefill && chunks);
     if (prefill) {
         rc = pkv::kv4_launch_prefill(p, cache->head_dim, sms, s);
         if (rc != PKV_OK) return rc;

@@ -12,7 +12,7 @@ struct Kv4Params : AttnParams {
     float v_unit;
 };
 
-// Rows (query, head) of a request from which on the prefill kernel takes it.
+// Requests with more (query, head) rows than this take the prefill kernel.
 constexpr int kKv4PrefillRows = 32;
 
 int64_t kv4_decode_workspace(int32_t head_dim, int sms);

@@ -29,7 +29,7 @@ namespace pkv {
 namespace {
 
 constexpr int kUnit = 32;          // tokens per unit, two groups of 16, each inside one block
-constexpr int kDepth = 2;          // units whose codes are held or on their way
+constexpr int kDepth = 1;          // units whose codes are held or on their way
 constexpr float kHead = 11.f;      // how far below a row's maximum (log2) R is set,
 constexpr float kSlack = 15.f;     // and how far it may come to be
 
@@ -51,7 +51,7 @@ __device__ __forceinline__ int at(int token, int piece) {
 }
 
 template <int D, int NT>
-constexpr int warps_of() { return D == 256 ? 8 : NT == 2 ? 8 : 16; }
+constexpr int warps_of() { return D == 256 ? 8 : 12; }
 
 // Units of a request: 32-token units of its visible range, once per tile of 8 * NT rows.
 template <int NT>

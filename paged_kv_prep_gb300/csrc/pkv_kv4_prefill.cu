@@ -1,5 +1,5 @@
 // Attention over the 4-bit paged cache for requests with many query rows
-// (prompt chunks), on the tensor cores.
+// (prompt chunks, drafted tokens of large groups), on the tensor cores.
 //
 // Mathematics: as in pkv_kv4_decode.cu.  S = q . k comes from the tensor core with keys that
 // carry their scales, so x = S * a - R with one a per row; w = 2^(x - R) goes into the second
@@ -15,62 +15,207 @@
 //
 // Layout.  A CTA holds 256 (query, head) rows of one KV head in two tiles of
 // 128.  Warps 0-3 and 4-7 do the softmax of one tile each, a thread per row;
-// warps 8-11 read the codes of 128 tokens, turn them into f16 times their scales (exact) and
-// lay them out for the tensor core, so one conversion serves both tiles; warp 12
-// issues the products: S = Q K^T (both in shared memory), O += P V with P in
-// TMEM in the place of S.  While one tile's softmax runs, the tensor core
-// works on the other.  The batch's (row tile, KV head, 128 tokens) units are
-// split evenly over the CTAs; a row tile that is cut leaves partial results
-// for a merge in a fixed order.
+// warps 8-11 (keys) and 12-15 (values) read the codes of 128 tokens a unit ahead into registers, turn
+// them into f16 times their scales (exact) and lay them out for the tensor core, so one
+// conversion serves both tiles; warp 16 issues the products: S = Q K^T (both in shared memory),
+// O += P V with P in TMEM in the place of S; warp 17 goes through the CTA's units and block tables
+// and tells the others.  While one tile's softmax runs, the tensor core works on the other; a tile's
+// second product begins when half of its weights are there.  The next row tile's queries are loaded
+// while the last products of this one run.
+// A row tile of at most 128 rows is taken by both softmax warpgroups: one does the units of even
+// numbers, the other those of odd ones, each with an accumulator of its own; they are put together
+// at the end, out of TMEM.
+// The batch's (row tile, KV head, 128 tokens) units are split evenly over the CTAs, by what they cost; a row
+// tile that is cut leaves partial results for a merge in a fixed order.
 //
 // Every wait has a limit; one that runs out sets PKV_DEVERR_TIMEOUT, the other
 // waits give up after it, and the CTA drains its products and frees its TMEM.
 #include "pkv_kv4_attention.cuh"
-#include "pkv_prefill.cuh"
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
-// Registers a thread: launched with 128; 256 x 176 + 128 x 104 + 128 x 56 = 512 x 128.
-constexpr int kSoftRegs = 176, kConvRegs = 104, kIssueRegs = 56;
-static_assert(32 * (kSoftWarps * kSoftRegs + kConvWarps * kConvRegs + 4 * kIssueRegs) <= 65536, "registers");
-static_assert((kThreads + 1 + kThreads / 32) * 8 <= 2 * kKeys * 32, "the plan's sums lie in the raw codes' place");
+constexpr int kRows = 256;              // rows of a CTA, two tiles of 128
+constexpr int kKeys = 128;              // tokens per unit
+constexpr int kSoftWarps = 8, kConvWarps = 4;          // converting warps: as many for the keys as for the values
+constexpr int kThreads = 32 * (kSoftWarps + 2 * kConvWarps + 4);   // and a warpgroup: issue, walk, two idle warps
+constexpr int kUnits = 8;                // units that are known ahead
+// Registers a thread: launched with 96; 256 x 144 + 256 x 64 + 128 x 64 = 640 x 96.
+constexpr int kSoftRegs = 144, kConvRegs = 64, kIssueRegs = 64;
+static_assert(32 * (kSoftWarps * kSoftRegs + 2 * kConvWarps * kConvRegs + 4 * kIssueRegs) <= kThreads * 96, "registers");
+constexpr uint32_t kTries = 1u << 22;   // polls before a wait gives up (half a second or more)
 constexpr float kHead = 9.f;            // how far below a row's maximum (log2) R is set
 constexpr float kMostSum = 32768.f;     // sum of 64 w that makes it move
 constexpr float kHuge = 0x1p20f;        // a reference from which on a logit's rounding may count
+// Costs, in units of a row tile that one warpgroup's half of the units takes: a unit of two tiles, and what a
+// row tile costs beside its units (queries, first scores, output).
+constexpr int kPairCost = 2, kTileCost = 6;
+
+// Kinds of units: of two tiles, a row tile's last of this CTA, the CTA's last; no unit at all.
+constexpr int kPair = 1, kTileEnd = 2, kEnd = 4, kNone = 8;
+constexpr int kItems = 16;
+
+// One stretch of units: a row tile, a KV head, and which of its 128-token units.
+struct Item {
+    int start, count, len;              // of the request: first token, scheduled and cached tokens; count 0: the end
+    int lo, hi, base, units;            // keys that the tile's rows see, the 16-aligned start of its units
+    int i, rt, head, ua, ub;
+    int64_t last;                       // the cost at which the row tile's last unit begins
+    bool pair;                          // more than 128 rows
+};
 
 template <int D>
 struct Smem {
     char q[2][128 * D * 2];
     char k[2][kKeys * D * 2];
     char v[2][kKeys * D * 2];
-    char raw[2][kKeys * D / 2];         // codes of the unit that is converted next: keys, values
-    uint64_t q_full[2], k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_full[2], o_full[2], done;
-    uint32_t named[4];                  // which groups of 16 of a unit's tokens lie in a block, a bit each
+    float top[128], sum[128];           // the odd units' statistics of a row tile that both warpgroups take
+    uint64_t q_full[2], k_full[2], v_full[2], k_free[2], v_free[2], s_full[2], p_half[2], p_full[2], h_done[2], o_full[2];
+    uint64_t unit_full[kUnits], unit_free[kUnits], side_full, side_free, item_full[kItems], done;
+    // Of the units from the walking warp: first token that some row sees, the token behind the last one, which groups of
+    // 16 have a block, what kind of unit it is; and the groups' first lines.
+    int4 unit[kUnits];
+    int64_t line[kUnits][8];
+    Item item[kItems];                  // row tiles, from the walking warp; a last one without rows
     uint32_t tmem;
     int32_t failed;
 };
 
-// Scores of 32 columns, of which groups 2 c, 2 c + 1 may have no block.
-__device__ __forceinline__ void hide_unnamed(uint32_t (&s)[32], uint32_t two) {
-#pragma unroll
-    for (int h = 0; h < 2; h++)
-        if (!((two >> h) & 1)) {
-#pragma unroll
-            for (int k = 0; k < 16; k++) s[16 * h + k] = 0xff800000u;
-        }
+// The keys that rows f0 .. of a tile see: [lo, hi), and the 16-aligned start of their units.
+struct Span {
+    int lo, hi, base, units;
+};
+__device__ __forceinline__ Span span_of(const AttnParams &p, const Req &r, int rt) {
+    const int rows = r.count * p.G, f0 = rt * kRows, f1 = min(rows, f0 + kRows) - 1;
+    const int back = r.len - r.count, pos0 = back + f0 / p.G, pos1 = back + f1 / p.G;
+    Span s;
+    s.lo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
+    s.hi = min(pos1 + 1, r.keys);
+    s.base = s.lo & ~15;
+    s.units = s.hi > s.base ? (s.hi - s.base + kKeys - 1) / kKeys : 1;   // a tile without keys writes zeros
+    return s;
+}
+__device__ __forceinline__ bool is_pair(int64_t rows, int rt) { return rows - static_cast<int64_t>(rt) * kRows > 128; }
+__device__ __forceinline__ int64_t cost_of(const Span &s, bool pair) { return kTileCost + static_cast<int64_t>(s.units) * (pair ? kPairCost : 1); }
+__device__ __forceinline__ int64_t cost_of_tile(const AttnParams &p, const Req &r, int64_t rows, int rt) {
+    return cost_of(span_of(p, r, rt), is_pair(rows, rt)) * p.Hkv;
+}
+// Row tiles of a request.
+__device__ __forceinline__ int tiles_of(const AttnParams &p, const Req &r, int64_t rows) {
+    return r.count <= 0 || rows <= p.short_rows ? 0 : static_cast<int>((rows + kRows - 1) / kRows);
+}
+// A request's cost, by a thread, or by a warp (a lane for each row tile).
+__device__ __forceinline__ int64_t cost_of_request(const AttnParams &p, const Req &r, int lane = 0, int step = 1) {
+    const int64_t rows = static_cast<int64_t>(r.count) * p.G;
+    const int tiles = tiles_of(p, r, rows);
+    int64_t sum = 0;
+    for (int rt = lane; rt < tiles; rt += step) sum += cost_of_tile(p, r, rows, rt);
+    return sum;
 }
 
-// What a row sees of a unit: columns lo .. hi, and of those the named groups'.
+// Costs u .. end - 1 of the batch; a unit belongs to whoever has the cost at which it begins.
+struct Walk {
+    const AttnParams &p;
+    int64_t u, end, at;                 // at: where the row tile `rt` begins
+    int i, rt;
+    Req r;
+
+    // By a whole warp: a lane looks at every 32nd row tile of the request that u lies in.  `costs`: the requests'.
+    template <typename CostOf>
+    __device__ __forceinline__ Walk(const AttnParams &p_, const int64_t *prefix, int64_t u0, int64_t u1, CostOf costs) : p(p_), u(u0), end(u1) {
+        const int lane = threadIdx.x & 31;
+        i = plan_find<kThreads>(prefix, p.n, u, costs, &at);
+        r = request_of(p, i);
+        const int64_t rows = static_cast<int64_t>(r.count) * p.G;
+        const int tiles = tiles_of(p, r, rows);
+        for (rt = 0; rt + 32 < tiles; rt += 32) {
+            int64_t sum = cost_of_tile(p, r, rows, rt + lane);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+            if (u < at + sum) break;
+            at += sum;
+        }
+    }
+    __device__ __forceinline__ bool next(Item &x) {
+        while (u < end) {
+            const int64_t rows = static_cast<int64_t>(r.count) * p.G;
+            if (r.count <= 0 || rows <= p.short_rows || static_cast<int64_t>(rt) * kRows >= rows) {
+                r = request_of(p, ++i);
+                rt = 0;
+                continue;
+            }
+            const Span s = span_of(p, r, rt);
+            const bool pair = is_pair(rows, rt);
+            const int64_t one = cost_of(s, pair), all = one * p.Hkv;
+            if (u >= at + all) {
+                at += all;
+                rt++;
+                continue;
+            }
+            x.head = static_cast<int>((u - at) / one);
+            const int64_t tile = at + x.head * one + kTileCost;              // where its first unit begins
+            const int step = pair ? kPairCost : 1;
+            const int64_t a = (u - tile + step - 1) / step, b = (end - tile + step - 1) / step;
+            x.ua = u > tile ? static_cast<int>(a) : 0;
+            x.ub = end <= tile ? 0 : b < s.units ? static_cast<int>(b) : s.units;
+            u = tile - kTileCost + one;
+            if (x.ua >= x.ub) continue;
+            x.start = r.start;
+            x.count = r.count;
+            x.len = r.len;
+            x.lo = s.lo;
+            x.hi = s.hi;
+            x.base = s.base;
+            x.units = s.units;
+            x.i = i;
+            x.rt = rt;
+            x.pair = pair;
+            x.last = tile + static_cast<int64_t>(s.units - 1) * step;
+            return true;
+        }
+        x.count = 0;
+        return false;
+    }
+};
+
+template <int D>
+__device__ __forceinline__ bool wait(Smem<D> *sm, uint64_t *bar, uint32_t parity) {
+    if (mbar_try(bar, parity)) return true;
+    volatile int32_t *failed = &sm->failed;
+    for (uint32_t k = 0; k < kTries; k++) {
+        if (mbar_try(bar, parity)) return true;
+        if ((k & 63) == 63 && *failed) return false;
+    }
+    *failed = 1;
+    return false;
+}
+template <int D>
+__device__ __forceinline__ bool wait_all(Smem<D> *sm, uint64_t *bar, uint32_t parity) {
+    return __all_sync(~0u, wait(sm, bar, parity)) != 0;
+}
+// What a warp's threads have written counts as there once its first lane has arrived.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// What a row sees of a unit: columns lo .. hi, and of those the groups of 16 that have a block.
 struct Seen {
     bool whole;
     int lo, hi;
     uint32_t named;
     __device__ __forceinline__ void apply(uint32_t (&s)[32], int c) const {
-        hide(s, lo - 32 * c, hi - 32 * c);
-        hide_unnamed(s, named >> (2 * c));
+#pragma unroll
+        for (int k = 0; k < 32; k++)
+            if (k > hi - 32 * c || k < lo - 32 * c || !((named >> (2 * c + (k >> 4))) & 1)) s[k] = 0xff800000u;
     }
 };
+
+// 2^d of an integer d <= 0 (0 below 2^-126, and of -inf).
+__device__ __forceinline__ float power2_down(float d) {
+    return d >= -126.f ? __uint_as_float(static_cast<uint32_t>(static_cast<int>(d) + 127) << 23) : d < 0.f ? 0.f : d;
+}
 
 // Largest score of a row in the unit.
 __device__ __forceinline__ float row_max(uint32_t ts, const Seen &seen) {
@@ -80,7 +225,7 @@ __device__ __forceinline__ float row_max(uint32_t ts, const Seen &seen) {
         uint32_t s[32];
         tmem_ld32(s, ts + 32 * c);
         tc_wait_ld();
-        seen.apply(s, c);
+        if (!seen.whole) seen.apply(s, c);
 #pragma unroll
         for (int k = 0; k < 32; k += 2) most = max3(most, __uint_as_float(s[k]), __uint_as_float(s[k + 1]));
     }
@@ -106,12 +251,12 @@ __device__ __forceinline__ float weights32(const uint32_t (&s)[32], uint32_t (&w
     return low_of(both) + high_of(both);
 }
 
-// Columns 32 c .. of a unit from `c` on, where some row's weights outgrow its reference or its logits are huge: the reference
-// moves to 9 below the next integer of their largest x, with the row's sum, its weights of this unit so far and its
-// accumulator (o_cols columns, 0 while it holds nothing).  Rare.
-__device__ __forceinline__ void grow_rows(int c, uint32_t ts, uint32_t to, int o_cols, float a, float &top, float &sum, const Seen &seen) {
+// Columns 64 h .. + 63, where some row's weights outgrow its reference or its logits are huge: the reference
+// moves to 9 below the next integer of their largest x, with the row's sum, its weights of these columns
+// so far and its accumulator (o_cols columns, 0 while it holds nothing).  Rare.
+__device__ __forceinline__ void grow_rows(int h, uint32_t ts, uint32_t to, int o_cols, float a, float &top, float &sum, const Seen &seen) {
 #pragma unroll 1
-    for (; c < 4; c++) {
+    for (int c = 2 * h; c < 2 * h + 2; c++) {
         uint32_t s[32], w[16];
         tc_wait_st();
         tmem_ld32(s, ts + 32 * c);
@@ -127,17 +272,16 @@ __device__ __forceinline__ void grow_rows(int c, uint32_t ts, uint32_t to, int o
         const float f = grow ? power2_down(top - most) : 1.f;
         if (grow) top = most;
         sum *= f;
-#pragma unroll 1
-        for (int k = 0; k < c; k++) {
+        if (c & 1) {
             uint32_t y[16];
-            tmem_ld16(y, ts + 16 * k);
+            tmem_ld16(y, ts + 16 * (c - 1));
             tc_wait_ld();
 #pragma unroll
             for (int q = 0; q < 16; q++) {
                 const float2 z = __half22float2(*reinterpret_cast<const __half2 *>(&y[q]));
                 y[q] = pack_f16(z.x * f, z.y * f);       // f may be below f16's range
             }
-            tmem_st16(ts + 16 * k, y);
+            tmem_st16(ts + 16 * (c - 1), y);
         }
 #pragma unroll 1
         for (int k = 0; k < o_cols; k += 16) {
@@ -153,188 +297,251 @@ __device__ __forceinline__ void grow_rows(int c, uint32_t ts, uint32_t to, int o
     }
 }
 
-// All of a unit's columns, 64 at a time: their exponentials, sums and packing are one block of
-// independent work.  Weights stand in the place of S (32 columns of scores become 16 of packed
-// f16).  The loop is not unrolled: the body of a whole unit would not stay in the instruction cache
-// beside the other warps' code.
-__device__ __forceinline__ void row_weights(uint32_t ts, uint32_t to, int o_cols, float a, float &top, float &sum, const Seen &seen) {
+// Columns 64 h .. + 63 of a unit: their exponentials, sums and packing are one block of independent work.
+// Weights stand in the place of S (32 columns of scores become 16 of packed f16).  False where the
+// rows' references have to be looked at first (nothing is changed then).
+__device__ __forceinline__ bool row_weights(int h, uint32_t ts, float a, float top, float &sum, const Seen &seen) {
     const float ref = top == -INFINITY ? 0.f : -top;
-    int c = 0;
-    const bool huge = __any_sync(~0u, fabsf(ref) > kHuge);
-#pragma unroll 1
-    for (; c < 4 && !huge; c += 2) {
-        uint32_t s0[32], s1[32], w0[16], w1[16];
-        tmem_ld32(s0, ts + 32 * c);
-        tmem_ld32(s1, ts + 32 * (c + 1));
-        tc_wait_ld();
-        if (!seen.whole) {
-            seen.apply(s0, c);
-            seen.apply(s1, c + 1);
-        }
-        const float p0 = weights32<false>(s0, w0, a, ref);
-        const float p1 = weights32<false>(s1, w1, a, ref);
-        if (__any_sync(~0u, p0 + p1 > kMostSum)) break;
-        sum += p0 + p1;
-        tmem_st16(ts + 16 * c, w0);
-        tmem_st16(ts + 16 * (c + 1), w1);
+    uint32_t s0[32], s1[32], w0[16], w1[16];
+    tmem_ld32(s0, ts + 64 * h);
+    tmem_ld32(s1, ts + 64 * h + 32);
+    tc_wait_ld();
+    if (!seen.whole) {
+        seen.apply(s0, 2 * h);
+        seen.apply(s1, 2 * h + 1);
     }
-    if (c < 4) grow_rows(c, ts, to, o_cols, a, top, sum, seen);
+    const float p0 = weights32<false>(s0, w0, a, ref);
+    const float p1 = weights32<false>(s1, w1, a, ref);
+    if (__any_sync(~0u, p0 + p1 > kMostSum || fabsf(ref) > kHuge)) return false;
+    sum += p0 + p1;
+    tmem_st16(ts + 32 * h, w0);
+    tmem_st16(ts + 32 * h + 16, w1);
+    return true;
+}
+
+// Loads a warp's 32 query rows (`mine`: where this lane's row begins, -1: no row) as f16, each scaled by a power of
+// two 2^(14 - E) (negated for a negative softmax scale, so that a larger S is a larger x), into rows row0 ..
+// of a tile; returns this lane's E.  All loads are on their way at once.
+template <int D>
+__device__ __forceinline__ int load_rows(const Kv4Params &p, char *qs, int row0, int64_t mine) {
+    constexpr int kLine = D / 8, kAtOnce = 32 / kLine;                // lanes of a row, rows of a step
+    const int lane = threadIdx.x & 31, c = lane % kLine;
+    const bool fp16 = p.fp16 != 0;
+    uint4 raw[kLine];
+#pragma unroll
+    for (int i = 0; i < kLine; i++) {
+        const int64_t from = __shfl_sync(~0u, mine, i * kAtOnce + lane / kLine);
+        raw[i] = make_uint4(0, 0, 0, 0);
+        if (from >= 0) raw[i] = __ldg(reinterpret_cast<const uint4 *>(p.q + from) + c);
+    }
+    int own = 0;
+#pragma unroll
+    for (int i = 0; i < kLine; i++) {
+        const uint4 y = raw[i];
+        uint32_t most = __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
+#pragma unroll
+        for (int o = kLine / 2; o; o >>= 1) most = __vmaxu2(most, __shfl_xor_sync(~0u, most, o));
+        const float2 two = widen2(most, fp16);
+        const int e = row_exponent((most & 0xffffu) > (most >> 16) ? two.x : two.y);
+        const int theirs = __shfl_sync(~0u, e, lane % kAtOnce * kLine);
+        if (lane / kAtOnce == i) own = theirs;
+        const float f = p.scale_log2 < 0.f ? -power2(14 - e) : power2(14 - e);
+        uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float2 z = widen2(w[k], fp16);
+            w[k] = pack_f16(z.x * f, z.y * f);
+        }
+        const int row = row0 + i * kAtOnce + lane / kLine;
+        *reinterpret_cast<uint4 *>(qs + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return own;
 }
 
 // ---- softmax warps: a thread per row ----------------------------------------------------------
 template <int D>
-__device__ void softmax_role(const Kv4Params &p, Smem<D> *sm, Walk &walk, int64_t total, int64_t ranges) {
+__device__ void softmax_role(const Kv4Params &p, Smem<D> *sm, int64_t total, int64_t ranges) {
     constexpr int kPart = kRows * (D + 2);
     const int m = threadIdx.x >> 7, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;      // TMEM lane of the warp
     const uint32_t ts = sm->tmem + lanes + m * 128, to = sm->tmem + lanes + 256 + m * D;
     const bool fp16 = p.fp16 != 0;
-    char *qs = sm->q[m];
-    uint32_t unit = 0, s_phase = 0, o_phase = 0;
+    uint32_t unit = 0, s_phase = 0, o_phase[2] = {0, 0}, h_phase = 0, side = 0;
     int4 note = make_int4(-1, 0, 0, 0);
-    Item x;
-    while (walk.next(x)) {
-        const int nu = x.ub - x.ua;
-        if (m >= x.tiles) {
-            unit += nu;
-            continue;
-        }
-        const int rows = x.r.count * p.G, f = x.rt * kRows + m * 128 + row;
-        const bool live = f < rows;
-        const int j = f / p.G, hq = x.head * p.G + f - j * p.G;
-        const int back = x.r.len - x.r.count;
-        const int pos = live ? back + j : -1;
-        // this row's query as f16, scaled by a power of two
-        float cf;
-        {
-            const char *src = p.q + static_cast<int64_t>(x.r.start + j) * p.q_stride + 2 * static_cast<int64_t>(hq) * D;
-            float largest = 0.f;
-            if (live) {
-#pragma unroll 4
-                for (int c = 0; c < D / 8; c++) {
-                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const float2 z = widen2(w[k], fp16);
-                        largest = fmaxf(largest, fmaxf(fabsf(z.x), fabsf(z.y)));
-                    }
-                }
-            }
-            const int e = row_exponent(largest);
-            // a negative softmax scale moves into the query, so that a larger S is a larger x
-            const float fq = p.scale_log2 < 0.f ? -power2(14 - e) : power2(14 - e);
-            cf = fabsf(p.scale_log2) * power2(e - 14);
-            if (cf < 1e-37f) cf = 1e-37f;                // never zero, so that a hidden score stays -inf
-#pragma unroll 4
-            for (int c = 0; c < D / 8; c++) {
-                uint4 y = make_uint4(0, 0, 0, 0);
-                if (live) y = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-                uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const float2 z = widen2(w[k], fp16);
-                    w[k] = pack_f16(z.x * fq, z.y * fq);
-                }
-                *reinterpret_cast<uint4 *>(qs + (c >> 3) * (128 * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-        fence_async_shared();
-        mbar_arrive(&sm->q_full[m]);
 
-        const int f0 = x.rt * kRows + m * 128, f1 = min(rows, f0 + 128) - 1;
+    // This thread's row of an item: its number among the request's rows.
+    auto row_of = [&](const Item &x) { return x.rt * kRows + (x.pair ? m * 128 : 0) + row; };
+    // The next item's place; its queries' loading, and its rows' factor.
+    uint32_t items = 0;
+    auto find = [&](bool &ok) -> const Item & {
+        const uint32_t k = items % kItems;
+        ok = wait_all(sm, &sm->item_full[k], items / kItems & 1);
+        items++;
+        return sm->item[k];
+    };
+    auto load = [&](const Item &x) {
+        const int f = row_of(x), j = f / p.G;
+        const int64_t at = static_cast<int64_t>(x.start + j) * p.q_stride + 2 * static_cast<int64_t>(x.head * p.G + f - j * p.G) * D;
+        const int e = load_rows<D>(p, sm->q[m], row & ~31, f < x.count * p.G ? at : -1);
+        fence_async_shared();
+        warp_arrive(&sm->q_full[m]);
+        return fmaxf(fabsf(p.scale_log2) * power2(e - 14), 1e-37f);          // never zero, so that a hidden score stays -inf
+    };
+    // Whether this tile has units of it (the second of a row tile that both take has none of a single one).
+    auto needs = [&](const Item &x) { return x.count && (x.pair || m == 0 || x.ub - x.ua > 1); };
+    bool ok = true;
+    const Item *now = &find(ok);
+    if (!ok) return;
+    float next_a = 0.f;
+    if (needs(*now)) next_a = load(*now);
+    while (now->count) {
+        const Item &x = *now;
+        const float a = next_a;
+        const int nu = x.ub - x.ua, rows = x.count * p.G, f = row_of(x), j = f / p.G;
+        const bool pair = x.pair;
+        const bool live = f < rows;
+        const int back = x.len - x.count, first_key = x.base + x.ua * kKeys, pos = live ? back + j : -1;
+        const int f0 = f - row, f1 = min(rows, f0 + 128) - 1;
         const int pos0 = back + f0 / p.G, pos1 = back + f1 / p.G;
         // a row past the tile's last sees nothing and needs no reference to be looked for
         float top = live ? -INFINITY : 0.f, sum = 0.f;
-        bool ok = true;
-        for (int t = 0; t < nu && ok; t++, unit++) {
-            ok = wait(sm, &sm->s_full[m], s_phase);
+        const int begin = pair ? 0 : m, step = pair ? 1 : 2;
+        bool first = true;
+        for (int t = begin; t < nu; t += step) {
+            if (!wait_all(sm, &sm->s_full[m], s_phase)) return;
             s_phase ^= 1;
-            ok = __all_sync(~0u, ok);
-            if (!ok) break;
             tc_fence_after();
-            const int s0 = x.s.base + (x.ua + t) * kKeys;
+            const int s0 = first_key + t * kKeys;
             Seen seen;
-            seen.named = sm->named[unit & 3];
+            seen.named = static_cast<uint32_t>(sm->unit[(unit + t) % kUnits].z);
             seen.whole = s0 + kKeys - 1 <= pos0 && (p.window <= 0 || s0 > pos1 - p.window) && seen.named == 0xffu;
             seen.hi = pos - s0;                                              // columns lo .. hi are visible
             seen.lo = p.window > 0 && p.window <= pos ? pos - p.window + 1 - s0 : -0x40000000;
             // the first unit that shows a row anything sets its reference (no weight has been added before)
             if (__any_sync(~0u, top == -INFINITY)) {
-                const float most = row_max(ts, seen) * cf;
+                const float most = row_max(ts, seen) * a;
                 if (top == -INFINITY) top = most == INFINITY ? NAN : ceilf(most) - kHead;
             }
-            row_weights(ts, to, t > 0 ? D : 0, cf, top, sum, seen);
-            tc_wait_st();
-            tc_fence_before();
-            mbar_arrive(&sm->p_full[m]);
+            // one body for both halves, not unrolled: a whole unit's would not stay in the instruction cache
+#pragma unroll 1
+            for (int h = 0; h < 2; h++) {
+                if (!row_weights(h, ts, a, top, sum, seen)) {
+                    // the accumulator is not touched while the first half's product is under way
+                    if (h == 1 && !wait_all(sm, &sm->h_done[m], h_phase)) return;
+                    tc_fence_after();
+                    grow_rows(h, ts, to, first && h == 0 ? 0 : D, a, top, sum, seen);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                warp_arrive(h ? &sm->p_full[m] : &sm->p_half[m]);
+            }
+            h_phase ^= 1;
+            first = false;
         }
+        unit += nu;
+        // All scores of this tile are there: its queries' place takes the next item's.
+        const Item &y = find(ok);
         if (!ok) return;
-        ok = wait(sm, &sm->o_full[m], o_phase);
-        o_phase ^= 1;
-        if (!__all_sync(~0u, ok)) return;
-        tc_fence_after();
-        const bool full = x.ua == 0 && x.ub == x.s.units;
-        const bool none = top == -INFINITY && sum == 0.f;
+        if (needs(y)) next_a = load(y);
+
+        const bool full = x.ua == 0 && x.ub == x.units;
+        const int hq = x.head * p.G + f - j * p.G;
+        float scale = 1.f, scale2 = 0.f;          // of this warpgroup's accumulator, and of the other's
+        if (!first) {
+            if (!wait_all(sm, &sm->o_full[m], o_phase[m])) return;
+            o_phase[m] ^= 1;
+            tc_fence_after();
+        }
+        if (!pair) {
+            side ^= 1;
+            if (m == 1) {
+                // leave the statistics, and the accumulator in TMEM, until the other warpgroup has read them
+                sm->top[row] = top;
+                sm->sum[row] = sum;
+                tc_fence_before();
+                warp_arrive(&sm->side_full);
+                if (!wait_all(sm, &sm->side_free, side ^ 1)) return;
+                now = &y;
+                continue;
+            }
+            if (!wait_all(sm, &sm->side_full, side ^ 1)) return;
+            tc_fence_after();
+            const float top2 = sm->top[row], sum2 = sm->sum[row];
+            const bool none2 = top2 == -INFINITY && sum2 == 0.f, none1 = top == -INFINITY && sum == 0.f;
+            if (!none2) {
+                const float most = none1 ? top2 : fmaxf(top, top2);          // references are integers (or NaN)
+                scale = none1 ? 0.f : power2_down(top - most);
+                scale2 = power2_down(top2 - most);
+                sum = (none1 ? 0.f : sum * scale) + sum2 * scale2;
+                top = top != top || top2 != top2 ? NAN : most;
+            }
+        }
+        const bool none = !live || (top == -INFINITY && sum == 0.f);
         const float inv = full ? (none ? 0.f : p.v_unit / sum) : p.v_unit;
+        scale *= inv;
+        scale2 *= inv;
         float *part = p.part + (2LL * blockIdx.x + (x.ua == 0)) * kPart;
-        char *out = p.out + static_cast<int64_t>(x.r.start + j) * p.out_stride + 2 * static_cast<int64_t>(hq) * D;
+        char *out = p.out + static_cast<int64_t>(x.start + j) * p.out_stride + 2 * static_cast<int64_t>(hq) * D;
+        const bool both = !pair && __any_sync(~0u, scale2 != 0.f);        // NaN too; a pair's second tile has no other
 #pragma unroll 1
         for (int c = 0; c < D / 32; c++) {
             uint32_t o[32];
             tmem_ld32(o, to + 32 * c);
             tc_wait_ld();
-            if (full && live) {
-                uint32_t y[16];
 #pragma unroll
-                for (int k = 0; k < 16; k++)
-                    y[k] = none ? 0u : pack_out(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv, fp16);
+            for (int k = 0; k < 32; k++) o[k] = none || scale == 0.f ? 0u : __float_as_uint(__uint_as_float(o[k]) * scale);
+            if (both) {
+                uint32_t o2[32];
+                tmem_ld32(o2, to + D + 32 * c);
+                tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; k++)
+                    if (scale2 != 0.f) o[k] = __float_as_uint(fmaf(__uint_as_float(o2[k]), scale2, __uint_as_float(o[k])));
+            }
+            if (full && live) {
+                uint32_t y16[16];
+#pragma unroll
+                for (int k = 0; k < 16; k++) y16[k] = pack_out(__uint_as_float(o[2 * k]), __uint_as_float(o[2 * k + 1]), fp16);
 #pragma unroll
                 for (int k = 0; k < 4; k++)
-                    *reinterpret_cast<uint4 *>(out + 64 * c + 16 * k) = make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                    *reinterpret_cast<uint4 *>(out + 64 * c + 16 * k) = make_uint4(y16[4 * k], y16[4 * k + 1], y16[4 * k + 2], y16[4 * k + 3]);
             } else if (live) {
-                float *at = part + 2 * kRows + (m * 128 + row) * D + 32 * c;
+                float *at = part + 2 * kRows + ((pair ? m * 128 : 0) + row) * D + 32 * c;
 #pragma unroll
                 for (int k = 0; k < 8; k++)
-                    *reinterpret_cast<float4 *>(at + 4 * k) =
-                        make_float4(__uint_as_float(o[4 * k]) * inv, __uint_as_float(o[4 * k + 1]) * inv,
-                                    __uint_as_float(o[4 * k + 2]) * inv, __uint_as_float(o[4 * k + 3]) * inv);
+                    *reinterpret_cast<uint4 *>(at + 4 * k) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
             }
             __syncwarp();
         }
         if (live) {
             if (full) {
                 if (p.lse)
-                    p.lse[static_cast<int64_t>(x.r.start + j) * p.Hkv * p.G + hq] = none ? -INFINITY : (top + log2f(sum)) * kLn2;
+                    p.lse[static_cast<int64_t>(x.start + j) * p.Hkv * p.G + hq] = none ? -INFINITY : (top + log2f(sum)) * kLn2;
             } else {
-                part[m * 128 + row] = top;
-                part[kRows + m * 128 + row] = sum;
+                part[(pair ? m * 128 : 0) + row] = top;
+                part[kRows + (pair ? m * 128 : 0) + row] = sum;
             }
         }
         if (!full && x.ua == 0) {
-            const int64_t last = ((x.tile + x.s.units) * ranges - 1) / total;
+            const int64_t last = ((x.last + 1) * ranges - 1) / total;        // the range with the tile's last unit
             note = make_int4(x.i, x.rt, static_cast<int>(last - blockIdx.x) + 1, x.head);
         }
         tc_fence_before();
+        if (!pair) warp_arrive(&sm->side_free);
+        now = &y;
     }
     if (m == 0 && row == 0) p.meta[blockIdx.x] = note;
 }
 
 // ---- converting warps: codes to f16 operand tiles ---------------------------------------------
-// What a unit's copies need: the first line of the 16-token group (lane & 7) (-1: not read); klo,
-// khi: the unit's tokens that some row sees.
-struct Feed {
-    int64_t line;
-    int klo, khi;
-};
-
+// A warpgroup for the keys, one for the values.  A thread's codes and scales of the next unit are on their way
+// into registers while it converts this one's.
 template <int D>
-__device__ void convert_role(const Kv4Params &p, Smem<D> *sm, Walk &walk) {
+__device__ void convert_role(const Kv4Params &p, Smem<D> *sm, bool values) {
     constexpr int kC = D / 32;                       // 16-byte pieces of a token's codes
     constexpr int kTok = 32 * kConvWarps / kC;       // tokens per round of the threads, a multiple of 16
-    constexpr int kRounds = kKeys / kTok, kRaw = 32 * kConvWarps * 16;
-    const int i = threadIdx.x - 32 * kSoftWarps, lane = i & 31;
+    constexpr int kRounds = kKeys / kTok;
+    const int i = (threadIdx.x - 32 * kSoftWarps) % (32 * kConvWarps);
     const int c = i % kC, tok = i / kC;              // this thread's piece, and its token within a round
     // The four 16-byte places of a piece's 32 converted codes in a 128-byte row; threads of the upper 64
     // dimensions begin with the third, so that eight neighbours write to eight bank groups.
@@ -343,180 +550,264 @@ __device__ void convert_role(const Kv4Params &p, Smem<D> *sm, Walk &walk) {
     uint32_t to[4];
 #pragma unroll
     for (int k = 0; k < 4; k++) to[k] = row + ((((c & 1) * 4 + (k ^ turn)) ^ (tok & 7)) << 4);
+    const uint8_t *codes = (values ? p.vc : p.kc) + (tok & 15) * (D / 2) + 16 * c;
+    const uint8_t *scales = (values ? p.v_sf : p.k_sf) + (tok & 15) * (D / 16) + 2 * c;
+    char *dst = values ? sm->v[0] : sm->k[0];
+    uint64_t *freed = values ? sm->v_free : sm->k_free, *filled = values ? sm->v_full : sm->k_full;
 
-    Item x;
-    int t = 0;
-    bool more = walk.next(x);
-    if (!more) return;
-    t = x.ua;
-    // a block id that has been asked for but not yet looked at
-    int32_t id = -1;
-    auto ask = [&]() {
-        const int s = x.s.base + t * kKeys + 16 * (lane & 7);
-        id = -1;
-        if (s < x.s.hi && s + 16 > x.s.lo) id = p.table_at(x.table, s);
-    };
-    auto resolve = [&]() {
-        Feed f;
-        const int s = x.s.base + t * kKeys + 16 * (lane & 7);
-        if (id >= p.num_blocks) {
-            if (p.err) atomicOr(p.err, PKV_DEVERR_BLOCK);
-            id = -1;
-        }
-        f.line = id >= 0 ? (static_cast<int64_t>(id) * p.Hkv + x.head) * p.bs + s % p.bs : -1;
-        f.klo = x.s.lo - x.s.base - t * kKeys;
-        f.khi = x.s.hi - x.s.base - t * kKeys;
-        return f;
-    };
-    auto advance = [&]() {
-        t++;
-        if (t == x.ub) {
-            more = walk.next(x);
-            t = x.ua;
-        }
-        if (more) ask();
-    };
-    // Each thread copies its own 16-byte pieces and reads only those back: no barrier.  A piece's two
-    // scales wait in a register.
-    auto fetch = [&](const uint8_t *cache, const uint8_t *scales, const Feed &f, int r, char *raw) {
+    uint4 y[kRounds];
+    uint32_t sc[kRounds];
+    // A token that no row sees, or without a block: scales of zero (codes are finite whatever they are).
+    auto load = [&](uint32_t unit, const int4 &of, int r) {
         const int k = r * kTok + tok;
-        const int64_t from = __shfl_sync(~0u, f.line, k >> 4);
-        const bool live = from >= 0 && k >= f.klo && k < f.khi;
-        const int64_t line = live ? from + (k & 15) : 0;
-        cp_async<16>(smem_addr(raw + r * kRaw + i * 16), cache + line * (D / 2) + 16 * c, live);
-        return live ? static_cast<uint32_t>(__ldg(reinterpret_cast<const uint16_t *>(scales + line * (D / 16)) + c)) : 0u;
+        const bool on = k >= of.x && k < of.y && ((of.z >> (k >> 4)) & 1);
+        const int64_t line = sm->line[unit % kUnits][k >> 4];
+        sc[r] = 0;
+        if (on) {
+            y[r] = __ldg(reinterpret_cast<const uint4 *>(codes + line * (D / 2)));
+            sc[r] = __ldg(reinterpret_cast<const uint16_t *>(scales + line * (D / 16)));
+        }
     };
-    // Turn a half (keys or values) of unit `a` into f16, and refill its pieces with the next unit's.
-    auto half = [&](const uint8_t *cache, const uint8_t *scales, char *raw, char *dst, const Feed &b, bool next, uint32_t (&sc)[kRounds]) {
+    if (!wait_all(sm, &sm->unit_full[0], 0)) return;
+    int4 of = sm->unit[0];
+    if (of.w & kNone) {
+        warp_arrive(&filled[0]);
+        return;
+    }
+#pragma unroll
+    for (int r = 0; r < kRounds; r++) {
+        y[r] = make_uint4(0, 0, 0, 0);
+        load(0, of, r);
+    }
+    for (uint32_t unit = 0;; unit++) {
+        const uint32_t stage = unit & 1, next = unit + 1;
+        const bool end = of.w & kEnd;
+        if (!end) {
+            if (!wait_all(sm, &sm->unit_full[next % kUnits], next / kUnits & 1)) return;
+            of = sm->unit[next % kUnits];
+        }
+        if (!wait_all(sm, &freed[stage], ((unit >> 1) & 1) ^ 1)) return;
+        char *at = dst + stage * (kKeys * D * 2);
 #pragma unroll
         for (int r = 0; r < kRounds; r++) {
-            const uint4 y = *reinterpret_cast<const uint4 *>(raw + r * kRaw + i * 16);
             const uint32_t s = f16x2_of(sc[r]), s0 = turn ? high_twice(s) : low_twice(s), s1 = turn ? low_twice(s) : high_twice(s);
-            const uint32_t w[4] = {turn ? y.z : y.x, turn ? y.w : y.y, turn ? y.x : y.z, turn ? y.y : y.w};
+            const uint32_t w[4] = {turn ? y[r].z : y[r].x, turn ? y[r].w : y[r].y, turn ? y[r].x : y[r].z, turn ? y[r].y : y[r].w};
 #pragma unroll
             for (int k = 0; k < 4; k++) {
                 uint32_t h[4];
                 f16_of_e2m1x8(w[k], h);
-                const uint32_t m = k < 2 ? s0 : s1;
-                *reinterpret_cast<uint4 *>(dst + to[k] + r * kTok * 128) =
-                    make_uint4(mul_f16x2(h[0], m), mul_f16x2(h[1], m), mul_f16x2(h[2], m), mul_f16x2(h[3], m));
+                const uint32_t f = k < 2 ? s0 : s1;
+                *reinterpret_cast<uint4 *>(at + to[k] + r * kTok * 128) =
+                    make_uint4(mul_f16x2(h[0], f), mul_f16x2(h[1], f), mul_f16x2(h[2], f), mul_f16x2(h[3], f));
             }
-            if (next) sc[r] = fetch(cache, scales, b, r, raw);
         }
-        cp_commit();
-    };
-
-    uint32_t ksc[kRounds], vsc[kRounds];
-    ask();
-    Feed a = resolve();
-#pragma unroll
-    for (int r = 0; r < kRounds; r++) ksc[r] = fetch(p.kc, p.k_sf, a, r, sm->raw[0]);
-    cp_commit();
-#pragma unroll
-    for (int r = 0; r < kRounds; r++) vsc[r] = fetch(p.vc, p.v_sf, a, r, sm->raw[1]);
-    cp_commit();
-    advance();
-    bool ok = true, now = true;
-    for (uint32_t unit = 0; now; unit++) {
-        const bool next = more;
-        Feed b = {};
-        if (next) {
-            b = resolve();
-            advance();                               // the block ids of the unit after it are on their way
-        }
-        const int stage = unit & 1;
-        const uint32_t parity = ((unit >> 1) & 1) ^ 1;
-        cp_wait<1>();
-        ok = wait(sm, &sm->k_free[stage], parity);
-        if (!__all_sync(~0u, ok)) break;
-        const uint32_t named = __ballot_sync(~0u, a.line >= 0) & 0xffu;
-        if (i == 0) sm->named[unit & 3] = named;
-        half(p.kc, p.k_sf, sm->raw[0], sm->k[stage], b, next, ksc);
         fence_async_shared();
-        mbar_arrive(&sm->k_full[stage]);
-        cp_wait<1>();
-        ok = wait(sm, &sm->v_free[stage], parity);
-        if (!__all_sync(~0u, ok)) break;
-        half(p.vc, p.v_sf, sm->raw[1], sm->v[stage], b, next, vsc);
-        fence_async_shared();
-        mbar_arrive(&sm->v_full[stage]);
-        a = b;
-        now = next;
+        warp_arrive(&filled[stage]);
+        if (end) return;
+#pragma unroll
+        for (int r = 0; r < kRounds; r++) load(next, of, r);
     }
-    cp_wait<0>();
+}
+
+// ---- walking warp -----------------------------------------------------------------------------
+// Finds the CTA's units and where their lines are, and tells the others; lane g looks up group g.
+template <int D>
+__device__ void walk_role(const Kv4Params &p, Smem<D> *sm, Walk &walk) {
+    const int lane = threadIdx.x & 31, g = lane & 7;
+    const int jump = kKeys / p.bs, rest = kKeys - jump * p.bs;
+    uint32_t items = 0;
+    Item x;
+    const int32_t *table = nullptr;
+    int s = 0, entry = 0, offset = 0;                // the group's first token, its table entry and place in the block
+    auto next = [&]() {
+        const bool more = walk.next(x);
+        if (lane == 0) {
+            sm->item[items % kItems] = x;
+            mbar_arrive(&sm->item_full[items % kItems]);
+        }
+        items++;
+        table = p.tables + static_cast<int64_t>(x.i) * p.W;
+        s = x.base + x.ua * kKeys + 16 * g;
+        entry = s / p.bs;
+        offset = s - entry * p.bs;
+        return more;
+    };
+    // a block id that has been asked for but not yet looked at, of the unit after the one that is told of
+    int32_t id = -1;
+    auto ask = [&]() { id = s < x.hi && s + 16 > x.lo && entry < p.W ? table[entry] : -1; };
+    bool more = next();
+    if (more) {
+        ask();
+    } else if (lane == 0) {
+        sm->unit[0] = make_int4(0, 0, 0, kNone);
+        mbar_arrive(&sm->unit_full[0]);
+    }
+    int left = x.ub - x.ua;
+    for (uint32_t unit = 0; more; unit++) {
+        if (id >= p.num_blocks) {
+            if (p.err) atomicOr(p.err, PKV_DEVERR_BLOCK);
+            id = -1;
+        }
+        const int64_t line = (static_cast<int64_t>(id) * p.Hkv + x.head) * p.bs + offset;
+        const uint32_t named = __ballot_sync(~0u, id >= 0) & 0xffu;
+        const int at = s - 16 * g;
+        int4 of = make_int4(x.lo - at, x.hi - at, static_cast<int>(named), x.pair ? kPair : 0);
+        s += kKeys;
+        entry += jump;
+        offset += rest;
+        if (offset >= p.bs) {
+            offset -= p.bs;
+            entry++;
+        }
+        if (--left == 0) {
+            more = next();
+            left = x.ub - x.ua;
+            of.w |= kTileEnd | (more ? 0 : kEnd);
+        }
+        if (more) ask();                             // on its way while this unit's place becomes free
+        if (!wait_all(sm, &sm->unit_free[unit % kUnits], (unit / kUnits & 1) ^ 1)) return;
+        if (lane < 8) sm->line[unit % kUnits][g] = line;
+        if (lane == 0) sm->unit[unit % kUnits] = of;
+        warp_arrive(&sm->unit_full[unit % kUnits]);
+    }
 }
 
 // ---- issuing warp ------------------------------------------------------------------------------
-// The whole warp walks the units, so that addresses and descriptors stay in uniform registers; one
-// lane issues.
+// The whole warp goes through the units, so that addresses and descriptors stay in uniform registers; one
+// lane issues.  (A warp for each tile: 551 us where this takes 486, the tiles' products delay each other.)
+// Operand descriptors as in smem_desc: the upper word is the same for all, the lower one holds the address.
+constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) { return ((addr & 0x3ffffu) >> 4) | (lead >> 4 << 16); }
+__device__ __forceinline__ uint64_t desc_of(uint32_t low) { return static_cast<uint64_t>(kDescHigh) << 32 | low; }
+
 template <int D>
-__device__ void issue_role(Smem<D> *sm, Walk &walk) {
+__device__ void issue_role(Smem<D> *sm) {
     constexpr uint32_t kQk = f16_idesc(128, kKeys, false), kPv = f16_idesc(128, D, true);
-    const uint32_t tmem = __shfl_sync(~0u, sm->tmem, 0);
+    constexpr uint32_t kStage = kKeys * D * 2 >> 4;
+    const uint32_t q_low = desc_low(smem_addr(sm->q[0]), 16), k_low = desc_low(smem_addr(sm->k[0]), 16);
+    const uint32_t v_low = desc_low(smem_addr(sm->v[0]), kKeys * 128);
     uint32_t unit = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
     const bool leader = elect_one();
-    Item x;
     bool ok = true;
-    auto all = [&](uint64_t *bar, uint32_t parity) { return __all_sync(~0u, wait(sm, bar, parity)) != 0; };
-    auto qk = [&](int m, int stage) {
-        const uint64_t da = smem_desc(smem_addr(sm->q[m]), 16), db = smem_desc(smem_addr(sm->k[stage]), 16);
-        if (leader) {
-#pragma unroll
-            for (int k = 0; k < D / 16; k++) {
-                constexpr int kPanel = 128 * 128;
-                const uint64_t off = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
-                mma_ss(tmem + m * 128, da + off, db + off, kQk, k > 0);
-            }
-            mbar_arrive(&sm->s_full[m]);
-            tc_commit(&sm->s_full[m]);
-        }
-        __syncwarp();
-    };
-    auto pv = [&](int m, int stage, bool add) {
-        const uint64_t db = smem_desc(smem_addr(sm->v[stage]), kKeys * 128);
-        if (leader) {
-#pragma unroll
-            for (int k = 0; k < kKeys / 16; k++)
-                mma_ts(tmem + 256 + m * D, tmem + m * 128 + 8 * k, db + k * (2048 >> 4), kPv, add || k > 0);
-        }
-        __syncwarp();
-    };
     auto commit = [&](uint64_t *bar) {
         if (leader) tc_commit(bar);
         __syncwarp();
     };
-    while (ok && walk.next(x)) {
-        const int nu = __shfl_sync(~0u, x.ub - x.ua, 0), tiles = __shfl_sync(~0u, x.tiles, 0);
-        for (int m = 0; m < tiles && ok; m++) {
-            ok = all(&sm->q_full[m], q_phase[m]);
+    // Scores of unit u in tile m, whose keys are there.  (All of TMEM is this CTA's: its addresses begin at 0.)
+    auto qk = [&](auto tile, uint32_t u) {
+        constexpr int m = decltype(tile)::value;
+        if (leader && ok) {
+            const uint32_t da = q_low + m * (128 * D * 2 >> 4), db = k_low + (u & 1) * kStage;
+#pragma unroll
+            for (int k = 0; k < D / 16; k++) {
+                constexpr uint32_t kPanel = 128 * 128;
+                const uint32_t off = ((k >> 2) * kPanel + (k & 3) * 32) >> 4;
+                mma_ss(m * 128, desc_of(da + off), desc_of(db + off), kQk, k > 0);
+            }
+            mbar_arrive(&sm->s_full[m]);             // what this warp knows of the unit, as well as the products
+            tc_commit(&sm->s_full[m]);
+        }
+        __syncwarp();
+    };
+    // Waits for a unit's keys; what kind of unit it is.
+    auto keys = [&](uint32_t u) {
+        ok = ok && wait_all(sm, &sm->k_full[u & 1], (u >> 1) & 1);
+        tc_fence_after();
+        return ok ? __shfl_sync(~0u, sm->unit[u % kUnits].w, 0) : kNone;
+    };
+    // A tile's second product, in two halves of 64 tokens.
+    auto pv = [&](auto tile, uint32_t u, bool add) {
+        constexpr int m = decltype(tile)::value;
+        const uint32_t db = v_low + (u & 1) * kStage;
+        ok = ok && wait(sm, &sm->v_full[u & 1], (u >> 1) & 1) && wait(sm, &sm->p_half[m], p_phase[m]);
+        tc_fence_after();
+        if (leader && ok) {
+#pragma unroll
+            for (int k = 0; k < kKeys / 32; k++) mma_ts(256 + m * D, m * 128 + 8 * k, desc_of(db + k * (2048 >> 4)), kPv, add || k > 0);
+            tc_commit(&sm->h_done[m]);
+        }
+        __syncwarp();
+        ok = ok && wait(sm, &sm->p_full[m], p_phase[m]);
+        p_phase[m] ^= 1;
+        tc_fence_after();
+        if (leader && ok) {
+#pragma unroll
+            for (int k = kKeys / 32; k < kKeys / 16; k++) mma_ts(256 + m * D, m * 128 + 8 * k, desc_of(db + k * (2048 >> 4)), kPv, true);
+        }
+        ok = __all_sync(~0u, ok);
+    };
+    constexpr std::integral_constant<int, 0> tile0{};
+    constexpr std::integral_constant<int, 1> tile1{};
+    for (int kind = 0; ok && !(kind & kEnd);) {
+        kind = keys(unit);
+        if (kind & kNone) break;
+        for (int m = 0; m < 2 && ok; m++) {
+            if (m == 1 && !(kind & kPair) && (kind & kTileEnd)) continue;    // the second tile has no unit of it
+            ok = wait_all(sm, &sm->q_full[m], q_phase[m]);
             q_phase[m] ^= 1;
         }
-        ok = ok && all(&sm->k_full[unit & 1], (unit >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        for (int m = 0; m < tiles; m++) qk(m, unit & 1);
-        commit(&sm->k_free[unit & 1]);
-        for (int t = 0; t < nu && ok; t++, unit++) {
-            const int stage = unit & 1, next = stage ^ 1;
-            for (int m = 0; m < tiles && ok; m++) {
-                if (m == 0) {
-                    // the operands are usually there before the weights are: off the weights' path
-                    ok = all(&sm->v_full[stage], (unit >> 1) & 1) && (t + 1 == nu || all(&sm->k_full[next], ((unit + 1) >> 1) & 1));
-                }
-                ok = ok && all(&sm->p_full[m], p_phase[m]);
-                p_phase[m] ^= 1;
+        if (kind & kPair) {
+            qk(tile0, unit);
+            qk(tile1, unit);
+            commit(&sm->k_free[unit & 1]);
+            for (bool add = false; ok; add = true, unit++) {
+                const bool end = kind & kTileEnd;
+                int next = kind;
+                pv(tile0, unit, add);
+                if (!end) next = keys(unit + 1);
                 if (!ok) break;
-                tc_fence_after();
-                pv(m, stage, t > 0);
-                if (t + 1 < nu) {
-                    qk(m, next);
-                } else {
-                    commit(&sm->o_full[m]);
+                if (end) commit(&sm->o_full[0]);
+                else qk(tile0, unit + 1);
+                pv(tile1, unit, add);
+                if (!ok) break;
+                if (leader) {
+                    mbar_arrive(&sm->unit_free[unit % kUnits]);
+                    tc_commit(&sm->v_free[unit & 1]);
                 }
+                __syncwarp();
+                if (end) {
+                    commit(&sm->o_full[1]);
+                    break;
+                }
+                qk(tile1, unit + 1);
+                commit(&sm->k_free[(unit + 1) & 1]);
+                kind = next;
             }
-            if (!ok) break;
-            commit(&sm->v_free[stage]);
-            if (t + 1 < nu) commit(&sm->k_free[next]);
+            unit++;
+        } else {
+            // tile t & 1 takes unit t: the same rows
+            qk(tile0, unit);
+            commit(&sm->k_free[unit & 1]);
+            int next = kind;                         // the kind of the unit after this one, if there is one
+            if (!(kind & kTileEnd)) {
+                next = keys(unit + 1);
+                if (!ok) break;
+                qk(tile1, unit + 1);
+                commit(&sm->k_free[(unit + 1) & 1]);
+            }
+            for (int t = 0; ok; t++, unit++) {
+                if (t & 1) pv(tile1, unit, t > 1);
+                else pv(tile0, unit, t > 1);
+                if (!ok) break;
+                if (leader) mbar_arrive(&sm->unit_free[unit % kUnits]);
+                commit(&sm->v_free[unit & 1]);
+                int after = next;
+                if (!((kind | next) & kTileEnd)) {
+                    after = keys(unit + 2);
+                    if (!ok) break;
+                    if (t & 1) qk(tile1, unit + 2);
+                    else qk(tile0, unit + 2);
+                    commit(&sm->k_free[unit & 1]);
+                } else {
+                    commit(&sm->o_full[t & 1]);
+                }
+                if (kind & kTileEnd) break;
+                kind = next;
+                next = after;
+            }
+            unit++;
         }
     }
     // the products end before the TMEM is freed
@@ -530,19 +821,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Param
     extern __shared__ char s_raw[];
     // the swizzle goes by address bits: the operand tiles start on 1024 bytes
     Smem<D> *sm = reinterpret_cast<Smem<D> *>(s_raw + (-smem_addr(s_raw) & 1023u));
-    const int warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (warp == 0) tmem_alloc(&sm->tmem, 512);
     if (threadIdx.x == 32) {
         for (int k = 0; k < 2; k++) {
-            mbar_init(&sm->q_full[k], 128);
-            mbar_init(&sm->k_full[k], 32 * kConvWarps);
-            mbar_init(&sm->v_full[k], 32 * kConvWarps);
+            mbar_init(&sm->q_full[k], 4);
+            mbar_init(&sm->k_full[k], kConvWarps);
+            mbar_init(&sm->v_full[k], kConvWarps);
             mbar_init(&sm->k_free[k], 1);
             mbar_init(&sm->v_free[k], 1);
             mbar_init(&sm->s_full[k], 2);
-            mbar_init(&sm->p_full[k], 128);
+            mbar_init(&sm->p_half[k], 4);
+            mbar_init(&sm->p_full[k], 4);
+            mbar_init(&sm->h_done[k], 1);
             mbar_init(&sm->o_full[k], 1);
         }
+        for (int k = 0; k < kUnits; k++) {
+            mbar_init(&sm->unit_full[k], 1);
+            mbar_init(&sm->unit_free[k], 1);
+        }
+        for (int k = 0; k < kItems; k++) mbar_init(&sm->item_full[k], 1);
+        mbar_init(&sm->side_full, 4);
+        mbar_init(&sm->side_free, 4);
         mbar_init(&sm->done, 1);
         sm->failed = 0;
         fence_mbar_init();
@@ -552,23 +852,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Param
     tc_fence_after();
     pdl_wait();
     pdl_trigger();
-    int64_t *prefix = reinterpret_cast<int64_t *>(sm->raw);
+    // The plan's sums lie where the first keys go: these wait for the walking warp, which has read them then.  The
+    // costs of the requests of a small batch are found by whole warps, and lie where the first values go.
+    int64_t *prefix = reinterpret_cast<int64_t *>(sm->k), *each = reinterpret_cast<int64_t *>(sm->v);
+    const bool together = p.n <= kThreads;
+    if (together) {
+        for (int i = warp; i < p.n; i += kThreads / 32) {
+            int64_t sum = cost_of_request(p, request_of(p, i, blockIdx.x == 0 && lane == 0), lane, 32);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+            if (lane == 0) each[i] = sum;
+        }
+        __syncthreads();
+    }
     const int64_t total = plan_prefix<kThreads>(prefix, prefix + kThreads + 1, p.n, [&](int i) {
-        return units_of_request(p, request_of(p, i, blockIdx.x == 0));
+        return together ? each[i] : cost_of_request(p, request_of(p, i, blockIdx.x == 0));
     });
-    const int64_t ranges = total < gridDim.x ? total : gridDim.x;
+    __syncthreads();                                 // everybody has the total
+    // at least kPairCost each, so that every range inside a row tile's units has one
+    const int64_t ranges = total / kPairCost < gridDim.x ? total / kPairCost : gridDim.x;
     if (blockIdx.x < ranges) {
-        Walk walk(p, prefix, blockIdx.x * total / ranges, (blockIdx.x + 1) * total / ranges);
-        __syncthreads();                             // the sums' place is the converting warps' from here on
         if (warp < kSoftWarps) {
             more_registers<kSoftRegs>();
-            softmax_role<D>(p, sm, walk, total, ranges);
-        } else if (warp < kSoftWarps + kConvWarps) {
+            softmax_role<D>(p, sm, total, ranges);
+        } else if (warp < kSoftWarps + 2 * kConvWarps) {
             fewer_registers<kConvRegs>();
-            convert_role<D>(p, sm, walk);
+            convert_role<D>(p, sm, warp >= kSoftWarps + kConvWarps);
         } else {
             fewer_registers<kIssueRegs>();
-            if (warp == kSoftWarps + kConvWarps) issue_role<D>(sm, walk);
+            if (warp == kSoftWarps + 2 * kConvWarps) issue_role<D>(sm);
+            if (warp == kSoftWarps + 2 * kConvWarps + 1) {
+                Walk walk(p, prefix, blockIdx.x * total / ranges, (blockIdx.x + 1) * total / ranges,
+                          [&](int i) { return together ? each[i] : cost_of_request(p, request_of(p, i)); });
+                __syncwarp();
+                walk_role<D>(p, sm, walk);
+            }
         }
     } else if (threadIdx.x == 0) {
         p.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);

@@ -37,15 +37,21 @@
 // Every wait has a limit; one that runs out sets PKV_DEVERR_TIMEOUT, the other
 // waits give up after it, and the CTA drains its products and frees its TMEM.
 #include "pkv_kv8_attention.cuh"
-#include "pkv_prefill.cuh"
+#include "pkv_tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
+constexpr int kRows = 256;              // rows of a CTA, two tiles of 128
+constexpr int kKeys = 128;              // tokens per unit
+constexpr int kSub = kKeys / 16;
+constexpr int kSoftWarps = 8, kConvWarps = 4;
+constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 4);   // and a warpgroup whose first warp issues
 // Registers a thread: launched with 128; 256 x 176 + 128 x 104 + 128 x 56 = 512 x 128.
 constexpr int kSoftRegs = 176, kConvRegs = 104, kIssueRegs = 56;
 static_assert(32 * (kSoftWarps * kSoftRegs + kConvWarps * kConvRegs + 4 * kIssueRegs) <= 65536, "registers");
 static_assert((kThreads + 1 + kThreads / 32) * 8 <= 2 * kKeys * 64, "the plan's sums lie in the raw codes' place");
+constexpr uint32_t kTries = 1u << 22;   // polls before a wait gives up (half a second or more)
 constexpr float kMostSum = 16384.f;     // sum of 64 w that makes R follow the row's maximum
 
 template <int D>
@@ -61,6 +67,101 @@ struct Smem {
     int32_t nan_seen;                   // this CTA has met a V code that is NaN,
     uint8_t nan_units[1024];            // in units of these numbers, modulo 1024
 };
+
+// The keys that rows f0 .. of a tile see: [lo, hi), and the 16-aligned start of their units.
+struct Span {
+    int lo, hi, base, units;
+};
+__device__ __forceinline__ Span span_of(const AttnParams &p, const Req &r, int rt) {
+    const int rows = r.count * p.G, f0 = rt * kRows, f1 = min(rows, f0 + kRows) - 1;
+    const int back = r.len - r.count, pos0 = back + f0 / p.G, pos1 = back + f1 / p.G;
+    Span s;
+    s.lo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
+    s.hi = min(pos1 + 1, r.keys);
+    s.base = s.lo & ~15;
+    s.units = s.hi > s.base ? (s.hi - s.base + kKeys - 1) / kKeys : 1;   // a tile without keys writes zeros
+    return s;
+}
+__device__ __forceinline__ int64_t units_of_request(const AttnParams &p, const Req &r) {
+    const int64_t rows = static_cast<int64_t>(r.count) * p.G;
+    if (r.count <= 0 || rows <= p.short_rows) return 0;
+    int64_t sum = 0;
+    for (int rt = 0; rt * kRows < rows; rt++) sum += span_of(p, r, rt).units;
+    return sum * p.Hkv;
+}
+
+// One stretch of units: a row tile, a KV head, and which of its 128-token units.
+struct Item {
+    Req r;
+    Span s;
+    const int32_t *table;
+    int i, rt, head, ua, ub, tiles;     // tiles: 128-row tiles with rows in them
+    int64_t tile;                       // the row tile's (and head's) first unit
+};
+
+template <int D>
+struct Walk {
+    const AttnParams &p;
+    int64_t u, end, first;
+    int i, rt;
+    int64_t rt_first;                   // first unit of the row tile `rt`
+
+    __device__ __forceinline__ Walk(const AttnParams &p_, const int64_t *prefix, int64_t u0, int64_t u1) : p(p_), u(u0), end(u1) {
+        i = plan_find<kThreads>(prefix, p.n, u, [&](int k) { return units_of_request(p, request_of(p, k)); }, &first);
+        rt = 0;
+        rt_first = first;
+    }
+    __device__ __forceinline__ bool next(Item &x) {
+        if (u >= end) return false;
+        for (;;) {
+            const Req r = request_of(p, i);
+            const int64_t rows = static_cast<int64_t>(r.count) * p.G;
+            if (r.count <= 0 || rows <= p.short_rows || static_cast<int64_t>(rt) * kRows >= rows) {
+                i++;
+                rt = 0;
+                continue;
+            }
+            const Span s = span_of(p, r, rt);
+            const int64_t all = static_cast<int64_t>(s.units) * p.Hkv;
+            if (u >= rt_first + all) {
+                rt_first += all;
+                rt++;
+                continue;
+            }
+            x.r = r;
+            x.s = s;
+            x.i = i;
+            x.rt = rt;
+            x.table = p.tables + static_cast<int64_t>(i) * p.W;
+            x.head = static_cast<int>((u - rt_first) / s.units);
+            x.tile = rt_first + static_cast<int64_t>(x.head) * s.units;
+            x.ua = static_cast<int>(u - x.tile);
+            x.ub = static_cast<int>(end - x.tile < s.units ? end - x.tile : s.units);
+            x.tiles = rows - static_cast<int64_t>(rt) * kRows > 128 ? 2 : 1;
+            u = x.tile + x.ub;
+            return true;
+        }
+    }
+};
+
+template <int D>
+__device__ __forceinline__ bool wait(Smem<D> *sm, uint64_t *bar, uint32_t parity) {
+    if (mbar_try(bar, parity)) return true;
+    volatile int32_t *failed = &sm->failed;
+    for (uint32_t k = 0; k < kTries; k++) {
+        if (mbar_try(bar, parity)) return true;
+        if ((k & 63) == 63 && *failed) return false;
+    }
+    *failed = 1;
+    return false;
+}
+
+// Scores outside columns lo .. hi become -inf (of 32 columns).
+__device__ __forceinline__ void hide(uint32_t (&s)[32], int lo, int hi) {
+#pragma unroll
+    for (int k = 0; k < 32; k++)
+        if (k > hi || k < lo) s[k] = 0xff800000u;
+}
 
 // The factors of two 16-token groups; never zero, so that a hidden score stays -inf.
 __device__ __forceinline__ float2 factors(float cf, float2 ks) {
@@ -109,6 +210,11 @@ __device__ __forceinline__ float2 weights32(const uint32_t (&s)[32], uint32_t (&
         (h ? sums.y : sums.x) = low_of(part) + high_of(part);
     }
     return sums;
+}
+
+// 2^d of an integer d <= 0 (0 below 2^-126, and of -inf).
+__device__ __forceinline__ float power2_down(float d) {
+    return d >= -126.f ? __uint_as_float(static_cast<uint32_t>(static_cast<int>(d) + 127) << 23) : d < 0.f ? 0.f : d;
 }
 
 // Columns 32 c .. of a unit from `c` on, where some row's weights outgrow its reference: the reference
@@ -236,7 +342,7 @@ __device__ __forceinline__ uint32_t nan_dims(const AttnParams &p, const uint8_t 
 
 // ---- softmax warps: a thread per row ----------------------------------------------------------
 template <int D>
-__device__ void softmax_role(const AttnParams &p, Smem<D> *sm, Walk &walk, int64_t total, int64_t ranges) {
+__device__ void softmax_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk, int64_t total, int64_t ranges) {
     constexpr int kPart = kRows * (D + 2);
     const int m = threadIdx.x >> 7, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;      // TMEM lane of the warp
@@ -391,7 +497,7 @@ struct Feed {
 };
 
 template <int D>
-__device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk &walk) {
+__device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk<D> &walk) {
     constexpr int kC = D / 16;                       // 16-byte pieces of a token's codes
     constexpr int kTok = 32 * kConvWarps / kC;       // tokens per round of the threads, a multiple of 16
     constexpr int kRounds = kKeys / kTok, kStep = kRounds < 4 ? kRounds : 4, kRaw = 32 * kConvWarps * 16;
@@ -551,7 +657,7 @@ __device__ void convert_role(const AttnParams &p, Smem<D> *sm, Walk &walk) {
 // The whole warp walks the units, so that addresses and descriptors stay in uniform registers; one
 // lane issues.
 template <int D>
-__device__ void issue_role(Smem<D> *sm, Walk &walk) {
+__device__ void issue_role(Smem<D> *sm, Walk<D> &walk) {
     constexpr uint32_t kQk = f16_idesc(128, kKeys, false), kPv = f16_idesc(128, D, true);
     const uint32_t tmem = __shfl_sync(~0u, sm->tmem, 0);
     uint32_t unit = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
@@ -661,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv8_prefill_kernel(const AttnPara
     });
     const int64_t ranges = total < gridDim.x ? total : gridDim.x;
     if (blockIdx.x < ranges) {
-        Walk walk(p, prefix, blockIdx.x * total / ranges, (blockIdx.x + 1) * total / ranges);
+        Walk<D> walk(p, prefix, blockIdx.x * total / ranges, (blockIdx.x + 1) * total / ranges);
         __syncthreads();                             // the sums' place is the converting warps' from here on
         if (warp < kSoftWarps) {
             more_registers<kSoftRegs>();
