@@ -8,13 +8,14 @@
 // type.  4 bits: of 16 neighbours the scale is e4m3(max |x| / (6 unit)), a code
 // e2m1(x / (scale unit)); both are true quotients, because 16-bit inputs often
 // lie exactly half way between two codes and a product with a reciprocal would
-// move them.
+// move them.  A quotient is such a product with its error x - y (scale unit), exact in a fused
+// multiply-add, brought back once (Markstein's correction): exact where the quotient is a
+// floating-point number, as those middles are; 3 operations where a division takes a dozen.
 //
 // Bound: HBM (every line read and written once), or launch latency for a decode
 // step.
 //
-// Layout.  A warp takes one token and either 256 / (head_dim / 8) query lines or half
-// as many KV heads; a lane moves 16 bytes of a line and keeps the cosines and sines of
+// Layout.  A warp takes one token and a few of its query lines or KV heads; a lane moves 16 bytes of a line and keeps the cosines and sines of
 // its eight elements in registers for all of the warp's lines.  All lines are asked for
 // before the token's position is known, so the chain position -> table row
 // runs beside them.  A pair's other element comes by a shuffle.
@@ -26,7 +27,12 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kQSteps = 8, kKvSteps = 4;       // line steps of a warp: queries; keys and values together
+// Line steps of a warp: queries; keys and values together.  (16384 tokens, 32 query and 8 KV heads x 128: 8 and 4 take
+// 68 us into the 16-bit cache and 101 us into the 4-bit one with the reading back, 4 and 2 68 and 87, 8 and 2 76 and
+// 94, 8 and 1 86 and 111; with three axes and fewer heads 8 and 4 are 6 % faster than 4 and 2.)
+constexpr int q_steps(bool kv4) { return kv4 ? 4 : 8; }
+constexpr int kv_steps(bool kv4) { return kv4 ? 2 : 4; }
+constexpr int kLoadSteps = 2;
 constexpr int kMaxAxes = 8;
 
 struct Rope {
@@ -170,13 +176,19 @@ __device__ __forceinline__ Quantised quantise(const float (&x)[8], float unit, f
     Quantised z;
     z.nan = m > 0x7f800000u;
     z.scale = e4m3x2(__fdiv_rn(__uint_as_float(m), six), 0.f) & 0xffu;
-    const float by = floats_of(z.scale).x * unit;
-    z.codes = 0;
-    if (by > 0.f) {
-        float y[8];
+    const float by = floats_of(z.scale).x * unit, inverse = __frcp_rn(by);
+    float y[8];
+    if (__uint_as_float(m) * inverse < 0x1p64f) {
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float near = x[i] * inverse;
+            y[i] = fmaf(fmaf(-near, by, x[i]), inverse, near);
+        }
+        z.codes = e2m1x8(y);
+    } else {                                          // infinities among them, or far too large; a scale of 0 or NaN
 #pragma unroll
         for (int i = 0; i < 8; i++) y[i] = __fdiv_rn(x[i], by);
-        z.codes = e2m1x8(y);
+        z.codes = by > 0.f ? e2m1x8(y) : 0;
     }
     return z;
 }
@@ -192,6 +204,7 @@ __device__ __forceinline__ uint32_t scale_word(uint32_t scale, int l) {
 template <int D, bool kFp16, bool kKv4>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
     constexpr int kLine = D / 8, kAtOnce = 32 / kLine;             // lanes of a line, lines of a step
+    constexpr int kQSteps = q_steps(kKv4), kKvSteps = kv_steps(kKv4);
     pdl_wait();
     pdl_trigger();
     const int64_t job = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -310,15 +323,15 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const LoadParams p) 
     if (job >= p.jobs) return;
     const int64_t i = job / p.parts;
     const int lane = threadIdx.x & 31, l = lane % kLine;
-    const int h0 = static_cast<int>(job - i * p.parts) * kKvSteps * kAtOnce + lane / kLine;
+    const int h0 = static_cast<int>(job - i * p.parts) * kLoadSteps * kAtOnce + lane / kLine;
     const int64_t slot = p.slots[i];
     const bool live = slot >= 0 && slot < p.num_slots;
     if (slot >= p.num_slots && lane == 0 && p.err) atomicOr(p.err, PKV_DEVERR_SLOT);
     const uint32_t block = live ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(p.bs) : 0;
     const uint32_t offset = static_cast<uint32_t>(slot) - block * static_cast<uint32_t>(p.bs);
-    uint32_t kcode[kKvSteps], vcode[kKvSteps], kscale[kKvSteps], vscale[kKvSteps];
+    uint32_t kcode[kLoadSteps], vcode[kLoadSteps], kscale[kLoadSteps], vscale[kLoadSteps];
 #pragma unroll
-    for (int n = 0; n < kKvSteps; n++) {
+    for (int n = 0; n < kLoadSteps; n++) {
         const int h = h0 + n * kAtOnce;
         kcode[n] = vcode[n] = kscale[n] = vscale[n] = 0;
         if (live && h < p.H) {
@@ -334,7 +347,7 @@ __global__ void __launch_bounds__(kThreads) kv4_load_kernel(const LoadParams p) 
         }
     }
 #pragma unroll
-    for (int n = 0; n < kKvSteps; n++) {
+    for (int n = 0; n < kLoadSteps; n++) {
         const int h = h0 + n * kAtOnce;
         if (h >= p.H) continue;
         const int64_t at = (i * p.H + h) * (2 * D) + 16 * l;
@@ -364,7 +377,7 @@ int check_rope(const pkv_rope *r, int32_t head_dim, int32_t num_tokens, Rope *ou
 }
 
 // The sources and the queries; p's cache is filled in already.
-int check_rows(AppendParams &p, const void *k, const void *v, int32_t head_dim, int32_t dtype, const void *q, void *q_out) {
+int check_rows(AppendParams &p, bool kv4, const void *k, const void *v, int32_t head_dim, int32_t dtype, const void *q, void *q_out) {
     if (!kv8_head_dim(head_dim) || (dtype != PKV_BF16 && dtype != PKV_FP16) || p.T < 0 || p.T >= PKV_MAX_TOKENS || p.H < 1 ||
         p.H > kMaxHeads || p.Hq < 0 || p.Hq > (1 << 20) || p.k_stride < 0 || p.v_stride < 0 || p.q_stride < 0 ||
         p.q_out_stride < 0)
@@ -379,8 +392,9 @@ int check_rows(AppendParams &p, const void *k, const void *v, int32_t head_dim, 
     if (p.T > 1 && (p.k_stride < line || p.v_stride < line || (p.Hq > 0 && (p.q_stride < row || p.q_out_stride < row))))
         return PKV_ERR_INVALID_ARG;
     const int lines = 32 / (head_dim / 8);
-    p.q_parts = (p.Hq + kQSteps * lines - 1) / (kQSteps * lines);
-    p.parts = p.q_parts + (p.H + kKvSteps * lines - 1) / (kKvSteps * lines);
+    const int q_lines = q_steps(kv4) * lines, kv_lines = kv_steps(kv4) * lines;
+    p.q_parts = (p.Hq + q_lines - 1) / q_lines;
+    p.parts = p.q_parts + (p.H + kv_lines - 1) / kv_lines;
     p.jobs = static_cast<int64_t>(p.T) * p.parts;
     p.k = static_cast<const char *>(k);
     p.v = static_cast<const char *>(v);
@@ -424,7 +438,7 @@ int pkv_rope_store(const pkv_rope *rope, const void *k, const void *v, int64_t k
     p.num_slots = num_slots;
     p.bs = 1;
     p.err = d_error;
-    int rc = pkv::check_rows(p, k, v, head_dim, dtype, q, q_out);
+    int rc = pkv::check_rows(p, false, k, v, head_dim, dtype, q, q_out);
     if (rc == PKV_OK && num_tokens > 0) rc = pkv::check_rope(rope, head_dim, num_tokens, &p.rope);
     if (rc != PKV_OK || num_tokens == 0) return rc;
     if (num_slots > 0 && (!k_cache || !v_cache)) return PKV_ERR_INVALID_ARG;
@@ -459,7 +473,7 @@ int pkv_kv4_store(const pkv_kv4_cache *cache, const pkv_rope *rope, const void *
     p.k_six = 6.f * cache->k_unit;
     p.v_six = 6.f * cache->v_unit;
     p.err = d_error;
-    rc = pkv::check_rows(p, k, v, cache->head_dim, dtype, q, q_out);
+    rc = pkv::check_rows(p, true, k, v, cache->head_dim, dtype, q, q_out);
     if (rc == PKV_OK && num_tokens > 0 && rope) rc = pkv::check_rope(rope, cache->head_dim, num_tokens, &p.rope);
     if (rc != PKV_OK || num_tokens == 0) return rc;
     return pkv::launch_append<true>(p, cache->head_dim, dtype, pkv::as_stream(stream));
@@ -488,7 +502,7 @@ int pkv_kv4_load(const pkv_kv4_cache *cache, const int64_t *slots, int32_t count
     p.H = cache->num_heads;
     p.bs = cache->block_size;
     p.err = d_error;
-    const int D = cache->head_dim, lines = 32 / (D / 8) * pkv::kKvSteps;
+    const int D = cache->head_dim, lines = 32 / (D / 8) * pkv::kLoadSteps;
     p.parts = (p.H + lines - 1) / lines;
     p.jobs = static_cast<int64_t>(count) * p.parts;
     const int64_t grid = (p.jobs + pkv::kWarps - 1) / pkv::kWarps;
