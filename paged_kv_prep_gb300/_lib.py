@@ -1102,45 +1102,66 @@ def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_len
 
 def _rope_args(positions, table, axes, interleaved, tokens):
     """The C view of a rotation, and what it points to."""
-    f32, i32 = _kv8_types()[2:4]
-    shape = positions.shape
+    f32, i32 = _KV8[2:4]
+    shape, stride, rows = positions.shape, positions.stride(), table.shape
     if not (positions.dtype is i32 and len(shape) in (1, 2) and shape[-1] >= tokens):
         raise ValueError("positions is int32 [tokens] or [axes, tokens]")
-    if positions.stride(-1) != 1 and shape[-1] > 1:
+    if stride[-1] != 1 and shape[-1] > 1:
         raise ValueError("an axis's positions are contiguous")
-    if not (table.dtype is f32 and table.dim() == 2 and table.is_contiguous()):
+    if not (table.dtype is f32 and len(rows) == 2 and table.is_contiguous()):
         raise ValueError("table is contiguous float32 [max_position, rot_dim]: cosines, then sines")
     count = shape[0] if len(shape) == 2 else 1
-    rows, rot = table.shape
     if axes is not None:
         axes = bytes(axes)
-        if len(axes) != rot // 2:
+        if len(axes) != rows[1] // 2:
             raise ValueError("axes has a row of positions for each of the rot_dim / 2 pairs")
-    return RopeArgs(table.data_ptr(), positions.data_ptr(), axes, positions.stride(0) if count > 1 else 0,
-                    _kv8_size(rows, "max_position"), rot, count, int(bool(interleaved)))
+    if rows[0] >= 1 << 31:
+        raise ValueError("max_position is a 32-bit integer")
+    return RopeArgs(table.data_ptr(), positions.data_ptr(), axes, stride[0] if count > 1 else 0,
+                    rows[0], rows[1], count, 1 if interleaved else 0)
+
+
+def _lines(x, shape, dim, what):
+    """_kv8_rows of [tokens, heads, head_dim], the common case first."""
+    stride = x.stride()
+    if len(shape) == 3 and stride[2] == 1 and stride[1] == dim and shape[0] > 1:
+        return stride[0] * 2
+    return _kv8_rows(x, shape[1] * dim if len(shape) == 3 else shape[-1], what)
 
 
 def _append_rows(k, v, q, q_out, slot_mapping, heads, dim):
     """Checks what a step appends; (tokens, type, strides of k, v, q and q_out in bytes, query heads)."""
-    T = slot_mapping.numel()
-    if not (slot_mapping.dtype is _kv8_types()[4] and slot_mapping.is_contiguous()):
+    T, dtype, shape = slot_mapping.numel(), k.dtype, k.shape
+    if not (slot_mapping.dtype is _KV8[4] and slot_mapping.is_contiguous()):
         raise ValueError("slot_mapping is contiguous int64")
-    if not (k.dtype is v.dtype and k.shape == v.shape and k.shape[0] >= T):
+    if not (dtype is v.dtype and shape == v.shape and shape[0] >= T):
         raise ValueError("k and v have the same shape and type, a row for each slot")
-    kind = _kv8_dtype(k)
-    k_stride, v_stride = _kv8_rows(k, heads * dim, "k"), _kv8_rows(v, heads * dim, "v")
+    kind = _KV8[1].get(dtype)
+    if kind is None:
+        raise ValueError("bfloat16 or float16")
+    if not (len(shape) == 3 and shape[1] == heads and shape[2] == dim):
+        _kv8_rows(k, heads * dim, "k")              # [tokens, heads * head_dim], or refused
+    k_stride, v_stride = _lines(k, shape, dim, "k"), _lines(v, shape, dim, "v")
     if q is None:
         if q_out is not None:
             raise ValueError("q_out without q")
         return T, kind, k_stride, v_stride, 0, 0, 0
     shape = q.shape
-    if not (len(shape) == 3 and shape[2] == dim and shape[0] >= T and q.dtype is k.dtype):
+    if not (len(shape) == 3 and shape[2] == dim and shape[0] >= T and q.dtype is dtype):
         raise ValueError("q is [tokens, q_heads, head_dim] of k's type, a row for each slot")
-    if q_out is not None and not (q_out.shape == shape and q_out.dtype is q.dtype):
+    if q_out is None:
+        return T, kind, k_stride, v_stride, _lines(q, shape, dim, "q"), shape[1] * dim * 2, shape[1]
+    if not (q_out.shape == shape and q_out.dtype is dtype):
         raise ValueError("q_out has q's shape and type")
-    width = shape[1] * dim
-    return (T, kind, k_stride, v_stride, _kv8_rows(q, width, "q"),
-            width * 2 if q_out is None else _kv8_rows(q_out, width, "q_out"), shape[1])
+    return T, kind, k_stride, v_stride, _lines(q, shape, dim, "q"), _lines(q_out, shape, dim, "q_out"), shape[1]
+
+
+def _make_like(x, stream, handle):
+    """A contiguous tensor of x's shape and type that a call makes (see _kv8_make)."""
+    if stream is None:
+        torch = _KV8[0]
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    return _kv8_make(x.shape, x.dtype, x.device, stream, handle)
 
 
 def rope_store(k, v, k_cache, v_cache, slot_mapping, positions, table, axes=None, interleaved=False,
@@ -1155,7 +1176,7 @@ def rope_store(k, v, k_cache, v_cache, slot_mapping, positions, table, axes=None
     2 pairs goes by (None: the first); interleaved: pairs are neighbouring elements.  q: [tokens,
     q_heads, head_dim], rotated into q_out (allocated when not given; may be q).  Returns q_out (None
     without q)."""
-    torch = _kv8_types()[0]
+    torch = (_KV8 or _kv8_types())[0]
     if not (len(k.shape) == 3 and k_cache.shape == v_cache.shape and k_cache.dtype is k.dtype and
             v_cache.dtype is k.dtype and k_cache.is_contiguous() and v_cache.is_contiguous()):
         raise ValueError("k is [tokens, heads, head_dim], the caches contiguous and of its type")
@@ -1172,7 +1193,7 @@ def rope_store(k, v, k_cache, v_cache, slot_mapping, positions, table, axes=None
                               d_error, stream, check)
     handle = _kv8_stream(stream, device)
     if q is not None and q_out is None:
-        q_out = _kv8_make(q.shape, q.dtype, q.device, stream, handle)
+        q_out = _make_like(q, stream, handle)
     rc = lib().pkv_rope_store(C.byref(rope), k.data_ptr(), v.data_ptr(), ks, vs, heads, dim, kind,
                               None if q is None else q.data_ptr(), qs, hq, None if q is None else q_out.data_ptr(), os_,
                               k_cache.data_ptr(), v_cache.data_ptr(), slots, slot_mapping.data_ptr(), T,
@@ -1190,17 +1211,21 @@ def rope_store(k, v, k_cache, v_cache, slot_mapping, positions, table, axes=None
 def _kv4_cache(k_cache, v_cache, k_scale, v_scale, k_unit, v_unit):
     """The C view of a 4-bit cache: codes [num_blocks, heads, block_size, head_dim / 2] and scales
     [num_blocks, heads, block_size, head_dim / 16], one byte an element."""
-    _kv8_types()                # a call's first use: from here on _KV8 is set
+    if _KV8 is None:
+        _kv8_types()            # a call's first use: from here on _KV8 is set
     shape, scales = k_cache.shape, k_scale.shape
-    if not (len(shape) == 4 and v_cache.shape == shape and v_scale.shape == scales and
-            scales[:3] == shape[:3] and len(scales) == 4 and shape[3] == 8 * scales[3]):
+    if not (len(shape) == 4 and v_cache.shape == shape and v_scale.shape == scales and len(scales) == 4):
         raise ValueError("the caches are [num_blocks, heads, block_size, head_dim / 2], the scales "
                          "[num_blocks, heads, block_size, head_dim / 16]")
-    for t in (k_cache, v_cache, k_scale, v_scale):
-        if not (t.itemsize == 1 and t.is_contiguous()):
-            raise ValueError("caches and scales are contiguous, one byte an element")
+    blocks, heads, size, half = shape
+    if not (scales[0] == blocks and scales[1] == heads and scales[2] == size and 8 * scales[3] == half):
+        raise ValueError("a scale for each 16 elements of each line")
+    if not (k_cache.itemsize == 1 and v_cache.itemsize == 1 and k_scale.itemsize == 1 and v_scale.itemsize == 1 and
+            k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and
+            v_scale.is_contiguous()):
+        raise ValueError("caches and scales are contiguous, one byte an element")
     return Kv4CacheArgs(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                        shape[0], shape[2], shape[1], 2 * shape[3], float(k_unit), float(v_unit))
+                        blocks, size, heads, 2 * half, k_unit, v_unit)
 
 
 def kv4_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, positions=None, table=None, axes=None,
@@ -1213,7 +1238,7 @@ def kv4_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, positions=
     v_scale: [num_blocks, heads, block_size, head_dim / 16] (uint8 or float8_e4m3fn); k_unit, v_unit:
     what all keys' and all values' scales are multiplied with.  Returns q_out (None without q)."""
     cache = _kv4_cache(k_cache, v_cache, k_scale, v_scale, k_unit, v_unit)
-    heads, dim = cache.num_heads, cache.head_dim
+    heads, dim = k_cache.shape[1], 2 * k_cache.shape[3]
     T, kind, ks, vs, qs, os_, hq = _append_rows(k, v, q, q_out, slot_mapping, heads, dim)
     if (positions is None) != (table is None):
         raise ValueError("positions and table come together")
@@ -1227,7 +1252,7 @@ def kv4_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, positions=
                              interleaved, q, q_out, k_unit, v_unit, d_error, stream, check)
     handle = _kv8_stream(stream, device)
     if q is not None and q_out is None:
-        q_out = _kv8_make(q.shape, q.dtype, q.device, stream, handle)
+        q_out = _make_like(q, stream, handle)
     rc = lib().pkv_kv4_store(C.byref(cache), None if rope is None else C.byref(rope), k.data_ptr(), v.data_ptr(),
                              ks, vs, kind, None if q is None else q.data_ptr(), qs, hq,
                              None if q is None else q_out.data_ptr(), os_, slot_mapping.data_ptr(), T,
@@ -1252,7 +1277,7 @@ def kv4_load(k_cache, v_cache, k_scale, v_scale, slots, dtype=None, k=None, v=No
     given = k if k is not None else v
     if dtype is None:
         dtype = torch.bfloat16 if given is None else given.dtype
-    kind, shape = _KV8[1].get(dtype), (n, cache.num_heads, cache.head_dim)
+    kind, shape = _KV8[1].get(dtype), (n, k_cache.shape[1], 2 * k_cache.shape[3])
     if kind is None:
         raise ValueError("bfloat16 or float16")
     for t in (k, v):
@@ -1304,14 +1329,14 @@ def kv4_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
     if not (len(table) == 2 and table[0] >= n and query_start_loc.numel() >= n + 1):
         raise ValueError("block_tables [n, W], query_start_loc [n + 1], seq_lens [n]")
     shape = q.shape
-    if not (len(shape) == 3 and shape[2] == cache.head_dim):
+    if not (len(shape) == 3 and shape[2] == 2 * k_cache.shape[3]):
         raise ValueError("q is [tokens, q_heads, head_dim]")
     T, hq, d = shape
     window = _kv8_size(window, "window")
-    kind, q_stride = _kv8_dtype(q), _kv8_rows(q, hq * d, "q")
+    kind, q_stride = _kv8_dtype(q), _lines(q, shape, d, "q")
     if out is not None and not (out.shape == shape and out.dtype is q.dtype):
         raise ValueError("out has q's shape and type")
-    out_stride = hq * d * 2 if out is None else _kv8_rows(out, hq * d, "out")
+    out_stride = hq * d * 2 if out is None else _lines(out, shape, d, "out")
     if not (lse is None or lse.shape == (T, hq) and lse.dtype is f32 and lse.is_contiguous()):
         raise ValueError("lse is contiguous float32 [tokens, q_heads]")
     if not (workspace is None or workspace.is_contiguous()):
@@ -1324,7 +1349,7 @@ def kv4_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
                                  softmax_scale, window, k_unit, v_unit, out, lse, workspace, d_error, stream, check)
     handle = _kv8_stream(stream, device)
     if out is None:
-        out = _kv8_make(shape, q.dtype, q.device, stream, handle)
+        out = _make_like(q, stream, handle)
     if lse is None:
         lse = _kv8_make((T, hq), f32, q.device, stream, handle)
     if workspace is None:
