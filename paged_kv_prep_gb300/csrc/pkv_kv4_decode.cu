@@ -550,7 +550,7 @@ int launch(const Kv4Params &p, int sms, cudaStream_t s) {
     const int least = (p.Hkv + kWarps - 1) / kWarps, full = sms > least ? sms : least;
     const int grid = most < static_cast<int64_t>(full) * kWarps ? static_cast<int>((most + kWarps - 1) / kWarps) : full;
     PKV_CUDA_TRY(launch_pdl(kv4_decode_kernel<D, NT>, dim3(grid), dim3(32 * kWarps), smem, s, p));
-    return p.whole ? PKV_OK : kv8_launch_merge(p, D, 8 * NT, grid * kWarps, p.Hkv, s);
+    return p.whole ? PKV_OK : kv4_launch_merge(p, D, 8 * NT, grid * kWarps, p.Hkv, sms, s);
 }
 
 }  // namespace

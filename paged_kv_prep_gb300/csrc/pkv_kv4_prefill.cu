@@ -912,7 +912,7 @@ int launch(const Kv4Params &p, int sms, cudaStream_t s) {
     const int rc = kv8_allow_smem(reinterpret_cast<const void *>(kv4_prefill_kernel<D>), static_cast<int>(smem), set);
     if (rc != PKV_OK) return rc;
     PKV_CUDA_TRY(launch_pdl(kv4_prefill_kernel<D>, dim3(sms), dim3(kThreads), smem, s, p));
-    return kv8_launch_merge(p, D, kRows, sms, 1, s);
+    return kv4_launch_merge(p, D, kRows, sms, 1, sms, s);
 }
 
 }  // namespace
