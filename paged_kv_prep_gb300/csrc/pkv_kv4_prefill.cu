@@ -322,11 +322,11 @@ __device__ __forceinline__ bool row_weights(int h, uint32_t ts, float a, float t
 // Loads a warp's 32 query rows (`mine`: where this lane's row begins, -1: no row) as f16, each scaled by a power of
 // two 2^(14 - E) (negated for a negative softmax scale, so that a larger S is a larger x), into rows row0 ..
 // of a tile; returns this lane's E.  All loads are on their way at once.
-template <int D>
+template <int D, bool fp16>
 __device__ __forceinline__ int load_rows(const Kv4Params &p, char *qs, int row0, int64_t mine) {
     constexpr int kLine = D / 8, kAtOnce = 32 / kLine;                // lanes of a row, rows of a step
     const int lane = threadIdx.x & 31, c = lane % kLine;
-    const bool fp16 = p.fp16 != 0;
+    const float sign = p.scale_log2 < 0.f ? -1.f : 1.f;
     uint4 raw[kLine];
 #pragma unroll
     for (int i = 0; i < kLine; i++) {
@@ -345,7 +345,7 @@ __device__ __forceinline__ int load_rows(const Kv4Params &p, char *qs, int row0,
         const int e = row_exponent((most & 0xffffu) > (most >> 16) ? two.x : two.y);
         const int theirs = __shfl_sync(~0u, e, lane % kAtOnce * kLine);
         if (lane / kAtOnce == i) own = theirs;
-        const float f = p.scale_log2 < 0.f ? -power2(14 - e) : power2(14 - e);
+        const float f = sign * power2(14 - e);
         uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
         for (int k = 0; k < 4; k++) {
@@ -359,13 +359,12 @@ __device__ __forceinline__ int load_rows(const Kv4Params &p, char *qs, int row0,
 }
 
 // ---- softmax warps: a thread per row ----------------------------------------------------------
-template <int D>
+template <int D, bool fp16>
 __device__ void softmax_role(const Kv4Params &p, Smem<D> *sm, int64_t total, int64_t ranges) {
     constexpr int kPart = kRows * (D + 2);
     const int m = threadIdx.x >> 7, row = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21;      // TMEM lane of the warp
     const uint32_t ts = sm->tmem + lanes + m * 128, to = sm->tmem + lanes + 256 + m * D;
-    const bool fp16 = p.fp16 != 0;
     uint32_t unit = 0, s_phase = 0, o_phase[2] = {0, 0}, h_phase = 0, side = 0;
     int4 note = make_int4(-1, 0, 0, 0);
 
@@ -382,7 +381,7 @@ __device__ void softmax_role(const Kv4Params &p, Smem<D> *sm, int64_t total, int
     auto load = [&](const Item &x) {
         const int f = row_of(x), j = f / p.G;
         const int64_t at = static_cast<int64_t>(x.start + j) * p.q_stride + 2 * static_cast<int64_t>(x.head * p.G + f - j * p.G) * D;
-        const int e = load_rows<D>(p, sm->q[m], row & ~31, f < x.count * p.G ? at : -1);
+        const int e = load_rows<D, fp16>(p, sm->q[m], row & ~31, f < x.count * p.G ? at : -1);
         fence_async_shared();
         warp_arrive(&sm->q_full[m]);
         return fmaxf(fabsf(p.scale_log2) * power2(e - 14), 1e-37f);          // never zero, so that a hidden score stays -inf
@@ -816,7 +815,7 @@ __device__ void issue_role(Smem<D> *sm) {
         if (mbar_try(&sm->done, 0)) break;
 }
 
-template <int D>
+template <int D, bool fp16>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Params p) {
     extern __shared__ char s_raw[];
     // the swizzle goes by address bits: the operand tiles start on 1024 bytes
@@ -874,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Param
     if (blockIdx.x < ranges) {
         if (warp < kSoftWarps) {
             more_registers<kSoftRegs>();
-            softmax_role<D>(p, sm, total, ranges);
+            softmax_role<D, fp16>(p, sm, total, ranges);
         } else if (warp < kSoftWarps + 2 * kConvWarps) {
             fewer_registers<kConvRegs>();
             convert_role<D>(p, sm, warp >= kSoftWarps + kConvWarps);
@@ -904,14 +903,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Param
     }
 }
 
-template <int D>
+template <int D, bool fp16>
 int launch(const Kv4Params &p, int sms, cudaStream_t s) {
     constexpr size_t smem = sizeof(Smem<D>) + 1024;
     static_assert(smem <= 227 * 1024, "shared memory");
     static bool set[64] = {false};
-    const int rc = kv8_allow_smem(reinterpret_cast<const void *>(kv4_prefill_kernel<D>), static_cast<int>(smem), set);
+    const int rc = kv8_allow_smem(reinterpret_cast<const void *>(kv4_prefill_kernel<D, fp16>), static_cast<int>(smem), set);
     if (rc != PKV_OK) return rc;
-    PKV_CUDA_TRY(launch_pdl(kv4_prefill_kernel<D>, dim3(sms), dim3(kThreads), smem, s, p));
+    PKV_CUDA_TRY(launch_pdl(kv4_prefill_kernel<D, fp16>, dim3(sms), dim3(kThreads), smem, s, p));
     return kv4_launch_merge(p, D, kRows, sms, 1, sms, s);
 }
 
@@ -922,7 +921,8 @@ int64_t kv4_prefill_workspace(int32_t head_dim, int sms) {
 }
 
 int kv4_launch_prefill(const Kv4Params &p, int32_t head_dim, int sms, cudaStream_t s) {
-    return head_dim == 64 ? launch<64>(p, sms, s) : launch<128>(p, sms, s);
+    if (p.fp16) return head_dim == 64 ? launch<64, true>(p, sms, s) : launch<128, true>(p, sms, s);
+    return head_dim == 64 ? launch<64, false>(p, sms, s) : launch<128, false>(p, sms, s);
 }
 
 }  // namespace pkv
