@@ -49,8 +49,9 @@ constexpr float kHead = 9.f;            // how far below a row's maximum (log2) 
 constexpr float kMostSum = 32768.f;     // sum of 64 w that makes it move
 constexpr float kHuge = 0x1p20f;        // a reference from which on a logit's rounding may count
 // Costs, in units of a row tile that one warpgroup's half of the units takes: a unit of two tiles, and what a
-// row tile costs beside its units (queries, first scores, output).
-constexpr int kPairCost = 2, kTileCost = 6;
+// row tile costs beside its units (queries, first scores, output).  A mixed call with 3 for the latter 954 us, with 6
+// 858, 10 817, 14 810; long chunks 488, 479, 472 and 473.
+constexpr int kPairCost = 2, kTileCost = 12;
 
 // Kinds of units: of two tiles, a row tile's last of this CTA, the CTA's last; no unit at all.
 constexpr int kPair = 1, kTileEnd = 2, kEnd = 4, kNone = 8;
