@@ -715,7 +715,8 @@ typedef struct {
  *   q, q_out: [num_q_heads][head_dim] a token, strides likewise; q_out may be q itself.
  *   num_q_heads 0: no queries;
  *   k_cache, v_cache: num_slots lines of num_heads * head_dim elements of dtype;
- *   slot_mapping: as in pkv_kv_cache_write (-1: not stored; the query is rotated all the same).
+ *   slot_mapping: as in pkv_kv_cache_write (-1: not stored; the query is rotated all the same);
+ *                 a call's slots are distinct.
  * Pointers and strides are multiples of 16 bytes (PKV_ERR_ALIGN).  One launch, capturable.
  */
 int pkv_rope_store(const pkv_rope *rope, const void *k, const void *v, int64_t k_stride_bytes,
@@ -815,6 +816,7 @@ int pkv_kv4_attention(const pkv_kv4_cache *cache, const void *q, int64_t q_strid
  * uniforms of the request's last row.  Weights are fp32 differences, at most 1 (NaN
  * counts as 0), and are added up as whole multiples of 2^-40 (to nearest even), so that
  * the result does not depend on an order; u times the total is rounded once to fp64.
+ * vocab is at most 2^22 (the sums fit 64 bits whatever the weights are).
  *   target_probs, draft_probs: dtype PKV_BF16, PKV_FP16 or PKV_FP32, [num_rows][vocab],
  *       rows *_stride elements apart; uniforms: float32 in [0, 1);
  *   tokens [n][max_drafts + 1]: the drafts that stand, the drawn token, then -1;

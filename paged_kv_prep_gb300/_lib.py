@@ -1174,8 +1174,8 @@ def rope_store(k, v, k_cache, v_cache, slot_mapping, positions, table, axes=None
     slot_mapping: int64, -1: not stored; positions: int32 [tokens] or [axes, tokens]; table: float32
     [max_position, rot_dim], cosines then sines; axes: the row of positions that each of the rot_dim /
     2 pairs goes by (None: the first); interleaved: pairs are neighbouring elements.  q: [tokens,
-    q_heads, head_dim], rotated into q_out (allocated when not given; may be q).  Returns q_out (None
-    without q)."""
+    q_heads, head_dim], rotated into q_out (may be q; allocated for the slots' tokens when not given).
+    Returns q_out (None without q)."""
     torch = (_KV8 or _kv8_types())[0]
     if not (len(k.shape) == 3 and k_cache.shape == v_cache.shape and k_cache.dtype is k.dtype and
             v_cache.dtype is k.dtype and k_cache.is_contiguous() and v_cache.is_contiguous()):
@@ -1193,7 +1193,7 @@ def rope_store(k, v, k_cache, v_cache, slot_mapping, positions, table, axes=None
                               d_error, stream, check)
     handle = _kv8_stream(stream, device)
     if q is not None and q_out is None:
-        q_out = _make_like(q, stream, handle)
+        q_out = _make_like(q if q.shape[0] == T else q[:T], stream, handle)
     rc = lib().pkv_rope_store(C.byref(rope), k.data_ptr(), v.data_ptr(), ks, vs, heads, dim, kind,
                               None if q is None else q.data_ptr(), qs, hq, None if q is None else q_out.data_ptr(), os_,
                               k_cache.data_ptr(), v_cache.data_ptr(), slots, slot_mapping.data_ptr(), T,
@@ -1252,7 +1252,7 @@ def kv4_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, positions=
                              interleaved, q, q_out, k_unit, v_unit, d_error, stream, check)
     handle = _kv8_stream(stream, device)
     if q is not None and q_out is None:
-        q_out = _make_like(q, stream, handle)
+        q_out = _make_like(q if q.shape[0] == T else q[:T], stream, handle)
     rc = lib().pkv_kv4_store(C.byref(cache), None if rope is None else C.byref(rope), k.data_ptr(), v.data_ptr(),
                              ks, vs, kind, None if q is None else q.data_ptr(), qs, hq,
                              None if q is None else q_out.data_ptr(), os_, slot_mapping.data_ptr(), T,

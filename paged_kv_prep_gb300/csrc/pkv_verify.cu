@@ -379,7 +379,7 @@ extern "C" int pkv_verify_drafts(const void *target_probs, int64_t target_stride
                                  const int32_t *draft_ids, const int32_t *query_start_loc, int32_t n,
                                  const float *uniforms, int32_t max_drafts, int32_t *tokens, int32_t *accepted,
                                  int32_t *d_error, pkv_stream_t stream) {
-    if (n < 0 || n > PKV_MAX_BATCH || num_rows < 0 || num_rows >= PKV_MAX_TOKENS || vocab < 1 || vocab > (1 << 30) ||
+    if (n < 0 || n > PKV_MAX_BATCH || num_rows < 0 || num_rows >= PKV_MAX_TOKENS || vocab < 1 || vocab > (1 << 22) ||
         max_drafts < 0 || max_drafts >= PKV_MAX_TOKENS || target_stride < 0 || draft_stride < 0 ||
         target_stride > (1LL << 40) || draft_stride > (1LL << 40) || (dtype != PKV_BF16 && dtype != PKV_FP16 && dtype != PKV_FP32))
         return PKV_ERR_INVALID_ARG;

@@ -134,6 +134,7 @@ def test_attention_refusals(L, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(p=None), INVALID), (dict(ids=None), INVALID), (dict(qsl=None), INVALID), (dict(u=None), INVALID),
     (dict(tokens=None), INVALID), (dict(acc=None), INVALID), (dict(dtype=3), INVALID), (dict(vocab=0), INVALID),
+    (dict(vocab=(1 << 22) + 1, ps=1 << 23, qs=1 << 23), INVALID),
     (dict(rows=-1), INVALID), (dict(n=-1), INVALID), (dict(n=16385), INVALID), (dict(most=-1), INVALID),
     (dict(ps=999), INVALID), (dict(qs=999), INVALID), (dict(ps=-1), INVALID), (dict(p=P + 2), ALIGN), (dict(q=P + 2), ALIGN),
     (dict(ids=P + 2), ALIGN), (dict(u=P + 1), ALIGN), (dict(n=0), OK), (dict(n=0, qsl=None), OK)])

@@ -317,3 +317,20 @@ def test_many_tokens(tokens):
     assert torch.equal(bits(out), bits(s.rotated(s.q).half()))
     ref.store(s.rotated(s.k).double(), s.v.double(), want[:2], want[2:], s.slots, 1.0, 1.0)
     check_stored(dev, want, s, s.rotated(s.k).double(), (1.0, 1.0))
+
+
+def test_more_rows_than_slots():
+    """A padded step: rows past the slots are not touched, and what is allocated is for the slots' tokens."""
+    s = Step(20, 2, 2, 64, 64, torch.bfloat16, skip=False)
+    q, k, v = s.split(s.rows.cuda())
+    dev, want = [x.cuda() for x in s.cache4()], s.cache4()
+    slots = s.slots[:13].contiguous()
+    out = pkv.kv4_store(k, v, *dev, slots.cuda(), q=q, **s.rope())
+    assert out.shape == (13, 4, 64) and torch.equal(bits(out), bits(s.rotated(s.q).bfloat16()[:13]))
+    keys = s.rotated(s.k).double()
+    ref.store(keys, s.v.double(), want[:2], want[2:], slots, 1.0, 1.0)
+    for a, b in zip(dev[2:], want[2:]):
+        assert torch.equal(a.cpu(), b)
+    given = torch.full_like(q, 7.0).contiguous()
+    pkv.kv4_store(k, v, *dev, slots.cuda(), q=q, q_out=given, **s.rope())
+    assert torch.equal(given[:13], out) and (given[13:] == 7.0).all()

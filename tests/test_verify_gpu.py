@@ -196,3 +196,13 @@ def test_a_single_row_needs_no_draft_and_no_requests_no_rows():
     assert none[0].shape == (0, 4) and none[1].shape == (0,)
     empty = pkv.verify_drafts(target[:0].cuda(), torch.zeros(0, dtype=torch.int32).cuda(), torch.zeros(3, dtype=torch.int32).cuda(), u[:0].cuda(), 1)
     assert empty[0].tolist() == [[-1, -1], [-1, -1]] and empty[1].tolist() == [0, 0]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_largest_vocabulary_of_weights_that_are_no_probabilities(dtype):
+    """2^22 tokens of weight 1 (and a stretch of smaller ones): a total of almost 2^62."""
+    vocab = 1 << 22
+    p = torch.ones(3, vocab, dtype=dtype)
+    p[1, 1000:2000000] = 0.25
+    p[2] = torch.rand(vocab, generator=torch.Generator().manual_seed(12)).to(dtype)
+    check(p, torch.zeros(3, dtype=torch.int32), [0, 1, 2, 3], torch.tensor([0.999, 0.4, 0.6]), 0)
