@@ -79,15 +79,21 @@ int pkv_kv4_attention(const pkv_kv4_cache *cache, const void *q, int64_t q_strid
     p.err = d_error;
     cudaStream_t s = pkv::as_stream(stream);
     // The prefill kernel takes the requests of many rows.  It needs head_dim <= 128 (two accumulators beside two
-    // score tiles in TMEM); otherwise the decode kernel's row tiles take everything.  Where the requests have
-    // many rows on average the step has prompt chunks, and the others are single tokens as a rule: the
-    // decode kernel then takes what fits its eight-row tiles, which go through the cache faster than sixteen.
+    // score tiles in TMEM); otherwise the decode kernel's row tiles take everything.  Up to 32 rows, two of the
+    // decode kernel's tiles, it would be mostly empty: 96 requests of two to six tokens with five heads a KV head
+    // under a window of 4096: 228 us; with the requests of more than 16 rows on the prefill kernel 294 us, of more than 8
+    // 374 us.  Where the requests have many rows on average the step has prompt chunks, and the others are single
+    // tokens as a rule: the decode kernel then takes what fits its eight-row tiles, which go through the cache
+    // faster than sixteen (a step of chunks and decodes 938 us; with up to 32 rows and tiles of sixteen 979 us).
     const bool chunks = static_cast<int64_t>(num_tokens) * p.G > 32LL * n && p.G <= 8;
     const int rows = chunks ? 8 : pkv::kKv4PrefillRows;
     const bool prefill = cache->head_dim <= 128 && num_tokens > n && static_cast<int64_t>(num_tokens - n + 1) * p.G > rows;
-    // Tables of at most 256 tokens and tiles enough for two warps an SM: a warp takes a whole row tile, and
-    // no merge follows.
-    p.whole = static_cast<int64_t>(p.W) * p.bs <= 256 && static_cast<int64_t>(n) * p.Hkv >= 2 * sms;
+    // A warp takes a whole row tile, and no merge follows, where the tables hold at most 64 tokens, or at most 256 and
+    // the batch two tiles an SM.  Single tokens, 8 KV heads, whole and cut: tables of 64
+    // tokens, 8 requests 9.6 and 11.2 us, 2048 requests 68 and 78; of 256 tokens, 32 requests 18.1 and 13.2, 64 17.8 and
+    // 17.9, 128 18.3 and 22.9, 2048 128 and 127; of 512 tokens, 128 requests 29.1 and 27.5, 32 27.6 and 18.7.
+    const int64_t most = static_cast<int64_t>(p.W) * p.bs;
+    p.whole = most <= 64 || (most <= 256 && static_cast<int64_t>(n) * p.Hkv >= 2 * sms);
     p.short_rows = prefill ? rows : 0x7fffffff;
     // one 8-row tile holds every request that the decode kernel takes
     const bool one_tile = (num_tokens <= n && p.G <= 8) || (prefill && chunks);

@@ -30,6 +30,15 @@
 //
 // Every wait has a limit; one that runs out sets PKV_DEVERR_TIMEOUT, the other
 // waits give up after it, and the CTA drains its products and frees its TMEM.
+//
+// Measured: two chunks of 2048 tokens, 32 query and 8 KV heads of 128, contexts up to 16384 (522 GFLOP) 473 us
+// with the merge, 1.10 PFLOP/s, 58 % of the measured rate of bf16 products.  A unit of 256 rows x 128 tokens takes 3900 cycles of
+// which the tensor pipe works 2048 (the rest is the way scores -> weights -> products with its barriers: without
+// any exponentials and conversions 390 us remain of 495, before the second products began by halves); a row tile 25000
+// cycles beside its units.  What was slower, against 495 us for those chunks: two issuing warps 551; scores in halves
+// of 64 tokens, two in TMEM 536; fetching codes ahead into L2 518; waits that sleep in hardware 537.  Codes copied to
+// shared memory (by bulk copies or by warps of their own) instead of into registers: 1530 us for a step of chunks
+// and decodes that takes 989 so.
 #include "pkv_kv4_attention.cuh"
 #include "pkv_tcgen05.cuh"
 
