@@ -9,6 +9,10 @@ device memory and streams only.
     row = state.add_request(token_ids, num_computed, [blocks_g0, ...])
     batch = state.prepare_batch(rows, num_scheduled_tokens)
     kv_cache_write(k, v, k_cache, v_cache, batch.slot_mapping[0])
+
+A cache held in 8 bits: ``kv8_store``, ``kv8_attention``, ``kv8_evict``.  Keys and queries rotated by
+position on their way into a cache: ``rope_store``, and ``kv4_store`` into one held in 4 bits, which
+``kv4_load`` and ``kv4_attention`` read.  ``verify_drafts`` decides which drafted tokens of a step stand.
 """
 from ._lib import (  # noqa: F401
     ADVANCE, LIVE_TABLES, SCHEDULE_SETTLED, DEVERR_BLOCK, DEVERR_DUP, DEVERR_OUTPUT_FULL, DEVERR_TABLE_FULL, DEVERR_TIMEOUT, DEVERR_COUNT, DEVERR_POSITION, DEVERR_ROW, DEVERR_SLOT,
