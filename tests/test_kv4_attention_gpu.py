@@ -330,6 +330,37 @@ def test_many_requests():
     check(Case([(1 + x % 3, x + 2) for x in lens] + [(30, 100)], 16, 8, 4, 128, seed=21), window=100)
 
 
+@pytest.mark.parametrize("d,bs,window", [(64, 16, 0), (128, 32, 9)])
+def test_many_chunks(d, bs, window):
+    """More requests than a CTA has threads, of more rows than the decode kernel takes; single and no tokens between them."""
+    gen = torch.Generator().manual_seed(3)
+    runs = torch.randint(9, 80, (1500,), generator=gen).tolist()
+    check(Case([(0 if x % 7 == 0 else 1 if x % 11 == 0 else x, x + x % 5) for x in runs], bs, 2, 4, d, seed=24), window=window)
+
+
+def test_two_graphs_share_a_workspace():
+    """Replayed in turn on one stream: a call leaves nothing in the workspace that the next one reads."""
+    cases = [Case(MIXED + [(1, 3000)], 16, 2, 4, 128, seed=25), Case(CHUNKS, 16, 2, 4, 128, seed=26)]
+    args = [c.args() for c in cases]
+    work = torch.empty(pkv.kv4_attention_workspace(128), dtype=torch.uint8, device="cuda")
+    work.fill_(0xff)
+    want = [pkv.kv4_attention(*a) for a in args]
+    got = [[torch.zeros_like(x) for x in w] for w in want]
+    graphs, stream = [], torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for a, (out, lse) in zip(args, got):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            pkv.kv4_attention(*a, out=out, lse=lse, workspace=work)
+        graphs.append(graph)
+    for which in (0, 1, 1, 0, 1):
+        for x in got[which]:
+            x.zero_()
+        graphs[which].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, w) for x, w in zip(got[which], want[which]))
+
+
 @pytest.mark.parametrize("reqs", [[(1, 5), (1, 3)], [(2, 4), (1, 3)]], ids=["decodes", "mixed"])
 @pytest.mark.parametrize("heads,d", [(1024, 256), (1024, 64), (1023, 128)])
 def test_more_heads_than_warps(heads, d, reqs):
