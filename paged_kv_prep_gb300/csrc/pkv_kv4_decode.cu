@@ -26,11 +26,13 @@
 // Measured, with the merge: 256 single tokens, 32 query and 8 KV heads of 128, contexts up to 8192 (1.16 GB) 224 us,
 // 77 % of the copy rate; four of 64 query heads on 65536 to 131072 tokens (455 MB) 97 us, 69 %; 96 requests
 // of two to six tokens, 40 query heads, a window of 4096 (411 MB; 656 MB are read, as a request of more than 16 rows
-// takes two tiles) 228 us.
-// Instructions bound it next to HBM: 129 for 1 KB of codes with eight rows, 176 with sixteen, 0.6 a cycle issued, the
-// integer pipe 50 % busy with the conversions.  Twelve warps an SM: 227 us for the 256, sixteen (fewer registers) 242,
-// ten 264, fourteen 262; a second unit on its way changes nothing.  Tiles of 32 rows with the queries in shared memory
-// 240 us for the 96 requests where sixteen rows took 227.
+// takes two tiles) 218 us.
+// Instructions bound it next to HBM: 129 for 1 KB of codes with eight rows, 0.6 a cycle issued, the
+// integer pipe 50 % busy with the conversions.  Tiles of eight rows: twelve warps an SM, 224 us for the 256; eight 262, ten
+// 264, fourteen 262, sixteen (fewer registers) 242; a second unit on its way changes nothing.  Tiles of sixteen rows, head_dim
+// 128: eight warps with the queries in shared memory, 218 us for the 96 requests; twelve so 222, queries in registers
+// 227 and (twelve, spilling) 232; 24 rows 262; as many groups of eight rows as a request needs, up to 32, 269.
+// Of head_dim 64 twelve warps 274 us where eight take 326; of 256 queries in registers 223 where shared memory takes 227.
 #include "pkv_kv4_attention.cuh"
 #include "pkv_tcgen05.cuh"
 
@@ -60,7 +62,12 @@ __device__ __forceinline__ int at(int token, int piece) {
 }
 
 template <int D, int NT>
-constexpr int warps_of() { return D == 256 ? 8 : 12; }
+constexpr int warps_of() { return D == 256 || (D == 128 && NT > 1) ? 8 : 12; }
+
+// Queries of tiles of sixteen rows lie in shared memory (with the accumulator they are more than the registers that
+// leave enough warps): fragments of two steps, 16 bytes a lane, for each eight rows.  For D = 256 registers spill either way.
+template <int D, int NT>
+constexpr int query_bytes() { return NT > 1 && D < 256 ? 8 * NT * D * 2 : 0; }
 
 // Units of a request: 32-token units of its visible range, once per tile of 8 * NT rows.
 template <int NT>
@@ -110,28 +117,32 @@ struct Tile {
     float top[NT][2], sum[NT][2];          // R and the sum of w, of columns 2t, 2t + 1
 
     __device__ __forceinline__ void run(const Kv4Params &p, const Req &r, const int32_t *table, int head, int rt, int ua, int ub,
-                                        Stage<D> *ring) {
+                                        Stage<D> *ring, uint4 *queries) {
         constexpr int S = D / 16;
+        constexpr bool kShared = query_bytes<D, NT>() > 0;
         constexpr int kPieces = D / 32;                    // 16-byte pieces of a token's codes
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         const int rows = r.count * p.G;
         const bool fp16 = p.fp16 != 0;
 
-        // row positions of this lane's columns, and the tile's key range
-        int pos[NT][2];
         float cf[NT][2];
-        uint32_t qb[NT][S][2];
+        uint32_t qb[kShared ? 1 : NT][S][2];
+        __syncwarp();                          // the last tile's queries have been read
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
             const int f = rt * 8 * NT + nt * 8 + g;
             const int j = f / p.G;
             const char *row = p.q + static_cast<int64_t>(r.start + j) * p.q_stride +
                               2 * static_cast<int64_t>(head * p.G + f - j * p.G) * D;
-            const int e = load_row<D>(qb[nt], row, f < rows, t, fp16, p.scale_log2 < 0.f);
+            uint32_t(&fr)[S][2] = qb[kShared ? 0 : nt];
+            const int e = load_row<D>(fr, row, f < rows, t, fp16, p.scale_log2 < 0.f);
+            if constexpr (kShared) {
+#pragma unroll
+                for (int j2 = 0; j2 < S; j2 += 2)
+                    queries[(j2 / 2 * NT + nt) * 32 + lane] = make_uint4(fr[j2][0], fr[j2][1], fr[j2 + 1][0], fr[j2 + 1][1]);
+            }
 #pragma unroll
             for (int c = 0; c < 2; c++) {
-                const int fc = rt * 8 * NT + nt * 8 + 2 * t + c;
-                pos[nt][c] = fc < rows ? r.len - r.count + fc / p.G : -1;
                 // never zero, so that a hidden score stays -inf
                 cf[nt][c] = fmaxf(fabsf(p.scale_log2) * power2(__shfl_sync(~0u, e, (2 * t + c) * 4) - 14), 1e-37f);
                 top[nt][c] = -INFINITY;
@@ -142,6 +153,11 @@ struct Tile {
 #pragma unroll
                 for (int c = 0; c < 4; c++) o[nt][j2][c] = 0.f;
         }
+        // position of the row in column 2 t + c of eight rows, -1 where there is none
+        auto pos_of = [&](int nt, int c) {
+            const int f = rt * 8 * NT + nt * 8 + 2 * t + c;
+            return f < rows ? r.len - r.count + f / p.G : -1;
+        };
         const int first_row = rt * 8 * NT, last_row = min(rows, first_row + 8 * NT) - 1;
         const int pos_first = r.len - r.count + first_row / p.G, pos_last = r.len - r.count + last_row / p.G;
         const int base = r.lo & ~(kUnit - 1);
@@ -266,11 +282,14 @@ struct Tile {
                     a[i] = mul_f16x2(a[i], sa);
                     b[i] = mul_f16x2(b[i], sb);
                 }
+                const uint32_t f0[4] = {a[0], b[0], a[1], b[1]}, f1[4] = {a[2], b[2], a[3], b[3]};
 #pragma unroll
-                for (int half = 0; half < 2; half++) {
-                    const uint32_t f[4] = {a[2 * half], b[2 * half], a[2 * half + 1], b[2 * half + 1]};
-#pragma unroll
-                    for (int nt = 0; nt < NT; nt++) mma_f16(x[q][nt], f, qb[nt][step + half][0], qb[nt][step + half][1]);
+                for (int nt = 0; nt < NT; nt++) {
+                    uint4 y;
+                    if constexpr (kShared) y = queries[(step / 2 * NT + nt) * 32 + lane];
+                    else y = make_uint4(qb[nt][step][0], qb[nt][step][1], qb[nt][step + 1][0], qb[nt][step + 1][1]);
+                    mma_f16(x[q][nt], f0, y.x, y.y);
+                    mma_f16(x[q][nt], f1, y.z, y.w);
                 }
             };
 #pragma unroll
@@ -302,15 +321,18 @@ struct Tile {
             const bool whole = mask == ~0u && s0 >= all_lo && s0 + kUnit <= all_hi;
             if (!whole) {
 #pragma unroll
-                for (int q = 0; q < 2; q++)
+                for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++)
+                    for (int col = 0; col < 2; col++) {
+                        const int pos = pos_of(nt, col), lo = lo_of(p, pos);
 #pragma unroll
-                        for (int c = 0; c < 4; c++) {
-                            const int tok = 16 * q + g + 8 * (c >> 1), s = s0 + tok;
-                            const bool ok = ((mask >> tok) & 1) && s <= pos[nt][c & 1] && s >= lo_of(p, pos[nt][c & 1]);
-                            if (!ok) x[q][nt][c] = -INFINITY;
-                        }
+                        for (int q = 0; q < 2; q++)
+#pragma unroll
+                            for (int h = 0; h < 2; h++) {
+                                const int tok = 16 * q + g + 8 * h, s = s0 + tok;
+                                if (!((mask >> tok) & 1) || s > pos || s < lo) x[q][nt][2 * h + col] = -INFINITY;
+                            }
+                    }
             }
             // R moves only where a row's values outgrow it (or it has seen nothing yet)
             bool grow = false;
@@ -508,6 +530,7 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv4_decode_kernel(c
         int64_t u = range * total / ranges;
         const int64_t end = (range + 1) * total / ranges;
         Stage<D> *ring = reinterpret_cast<Stage<D> *>(s_ring) + warp * kDepth;
+        uint4 *queries = reinterpret_cast<uint4 *>(s_ring + sizeof(Stage<D>) * kDepth * kWarps + warp * query_bytes<D, NT>());
         int64_t first;
         int i = plan_find<kThreads>(s_prefix, p.n, u, units, &first);
         while (u < end) {
@@ -526,7 +549,7 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv4_decode_kernel(c
             const int ua = p.whole ? 0 : static_cast<int>(u - tile);
             const int ub = p.whole ? per : static_cast<int>(end - tile < per ? end - tile : per);
             Tile<D, NT> x;
-            x.run(p, r, p.tables + static_cast<int64_t>(i) * p.W, head, rt, ua, ub, ring);
+            x.run(p, r, p.tables + static_cast<int64_t>(i) * p.W, head, rt, ua, ub, ring, queries);
             if (ua == 0 && ub == per) {
                 x.write(p, r, head, rt);
             } else {
@@ -546,7 +569,7 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv4_decode_kernel(c
 template <int D, int NT>
 int launch(const Kv4Params &p, int sms, cudaStream_t s) {
     constexpr int kWarps = warps_of<D, NT>();
-    constexpr size_t smem = sizeof(Stage<D>) * kDepth * kWarps;
+    constexpr size_t smem = (sizeof(Stage<D>) * kDepth + query_bytes<D, NT>()) * kWarps;
     static_assert(smem <= 220 * 1024, "shared memory");
     static bool set[64] = {false};
     const int rc = kv8_allow_smem(reinterpret_cast<const void *>(kv4_decode_kernel<D, NT>), static_cast<int>(smem), set);
