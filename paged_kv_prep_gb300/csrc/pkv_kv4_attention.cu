@@ -81,7 +81,7 @@ int pkv_kv4_attention(const pkv_kv4_cache *cache, const void *q, int64_t q_strid
     // The prefill kernel takes the requests of many rows.  It needs head_dim <= 128 (two accumulators beside two
     // score tiles in TMEM); otherwise the decode kernel's row tiles take everything.  Up to 32 rows, two of the
     // decode kernel's tiles, it would be mostly empty: 96 requests of two to six tokens with five heads a KV head
-    // under a window of 4096: 228 us; with the requests of more than 16 rows on the prefill kernel 294 us, of more than 8
+    // under a window of 4096: 218 us; with the requests of more than 16 rows on the prefill kernel 294 us, of more than 8
     // 374 us.  Where the requests have many rows on average the step has prompt chunks, and the others are single
     // tokens as a rule: the decode kernel then takes what fits its eight-row tiles, which go through the cache
     // faster than sixteen (a step of chunks and decodes 938 us; with up to 32 rows and tiles of sixteen 979 us).
