@@ -1099,6 +1099,24 @@ def kv8_evict(k_cache, v_cache, k_scale, v_scale, weights, block_tables, seq_len
 
 # -- appending with the rotation by position ----------------------------------
 
+_SHORT = None
+
+
+def _short():
+    """The calls from here on in C++ (csrc/pkv_marshal.cpp), with their operands in the common form.  They give
+    NotImplemented, and have done nothing, for any other form; the functions below then check it."""
+    global _SHORT
+    if _SHORT is None:
+        import torch  # noqa: F401  (its libraries are there from here on)
+
+        try:
+            from . import _marshal
+        except ImportError as e:
+            raise RuntimeError("paged_kv_prep_gb300: _marshal.so is not built, or for another torch (run "
+                               "paged_kv_prep_gb300.build.build() or __graft_entry__.build())") from e
+        _SHORT = _marshal
+    return _SHORT
+
 
 def _rope_args(positions, table, axes, interleaved, tokens):
     """The C view of a rotation, and what it points to."""
@@ -1176,6 +1194,10 @@ def rope_store(k, v, k_cache, v_cache, slot_mapping, positions, table, axes=None
     2 pairs goes by (None: the first); interleaved: pairs are neighbouring elements.  q: [tokens,
     q_heads, head_dim], rotated into q_out (may be q; allocated for the slots' tokens when not given).
     Returns q_out (None without q)."""
+    made = (_SHORT or _short()).rope_store(k, v, k_cache, v_cache, slot_mapping, positions, table, axes, interleaved, q, q_out,
+                                            d_error, stream, check)
+    if made is not NotImplemented:
+        return made
     torch = (_KV8 or _kv8_types())[0]
     if not (len(k.shape) == 3 and k_cache.shape == v_cache.shape and k_cache.dtype is k.dtype and
             v_cache.dtype is k.dtype and k_cache.is_contiguous() and v_cache.is_contiguous()):
@@ -1237,6 +1259,10 @@ def kv4_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, positions=
     k_cache, v_cache: one byte an element, [num_blocks, heads, block_size, head_dim / 2]; k_scale,
     v_scale: [num_blocks, heads, block_size, head_dim / 16] (uint8 or float8_e4m3fn); k_unit, v_unit:
     what all keys' and all values' scales are multiplied with.  Returns q_out (None without q)."""
+    made = (_SHORT or _short()).kv4_store(k, v, k_cache, v_cache, k_scale, v_scale, slot_mapping, positions, table, axes,
+                                           interleaved, q, q_out, k_unit, v_unit, d_error, stream, check)
+    if made is not NotImplemented:
+        return made
     cache = _kv4_cache(k_cache, v_cache, k_scale, v_scale, k_unit, v_unit)
     heads, dim = k_cache.shape[1], 2 * k_cache.shape[3]
     T, kind, ks, vs, qs, os_, hq = _append_rows(k, v, q, q_out, slot_mapping, heads, dim)
@@ -1269,6 +1295,10 @@ def kv4_load(k_cache, v_cache, k_scale, v_scale, slots, dtype=None, k=None, v=No
     """Read the lines of ``slots`` (int64) of the 4-bit cache back as 16-bit values
     (``pkv_kv4_load``).  dtype: bfloat16 (the default) or float16; k, v: contiguous [slots, heads,
     head_dim], allocated when not given.  A negative slot gives zeros.  Returns (k, v)."""
+    made = (_SHORT or _short()).kv4_load(k_cache, v_cache, k_scale, v_scale, slots, dtype, k, v, k_unit, v_unit, d_error, stream,
+                                          check)
+    if made is not NotImplemented:
+        return made
     cache = _kv4_cache(k_cache, v_cache, k_scale, v_scale, k_unit, v_unit)
     torch = _KV8[0]
     n = slots.numel()
@@ -1322,6 +1352,11 @@ def kv4_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_sta
 
     The cache as in ``kv4_store``; everything else as in ``kv8_attention``, which also adds up weights.
     workspace: uint8, kv4_attention_workspace bytes.  Returns (out, lse)."""
+    made = (_SHORT or _short()).kv4_attention(q, k_cache, v_cache, k_scale, v_scale, block_tables, query_start_loc, seq_lens,
+                                               softmax_scale, window, k_unit, v_unit, out, lse, workspace, d_error, stream,
+                                               check)
+    if made is not NotImplemented:
+        return made
     cache = _kv4_cache(k_cache, v_cache, k_scale, v_scale, k_unit, v_unit)
     torch, _, f32 = _KV8[:3]
     _kv8_int32(block_tables, query_start_loc, seq_lens)
@@ -1383,6 +1418,10 @@ def verify_drafts(target_probs, draft_ids, query_start_loc, uniforms, max_drafts
     float32 [rows] in [0, 1); draft_probs: like target_probs, the distributions the drafts were drawn
     from (None: drafts are certain).  Rows may be apart by a stride.  Returns (tokens int32 [n,
     max_drafts + 1]: the drafts that stand, the drawn token, then -1; accepted int32 [n])."""
+    made = (_SHORT or _short()).verify_drafts(target_probs, draft_ids, query_start_loc, uniforms, max_drafts, draft_probs, tokens,
+                                               accepted, d_error, stream, check)
+    if made is not NotImplemented:
+        return made
     torch, kinds, f32, i32 = _kv8_types()[:4]
     kind = 2 if target_probs.dtype is f32 else kinds.get(target_probs.dtype)
     if kind is None or target_probs.dim() != 2:

@@ -1,4 +1,5 @@
-"""Build the CUDA library ``libpkv.so`` in-tree with nvcc for sm_103a.
+"""Build the CUDA library ``libpkv.so`` in-tree with nvcc for sm_103a, and the
+binding's C++ part ``_marshal.so`` against it and torch's libraries.
 
 Each translation unit is compiled in its own nvcc process (in parallel), then
 linked into one shared library with the CUDA runtime linked statically.  The
@@ -7,9 +8,11 @@ ptxas resource report of every kernel is kept in ``_build/ptxas.log``.
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +20,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIBRARY = os.path.join(HERE, "libpkv.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -32,15 +36,33 @@ def sources():
 
 
 def _inputs():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(
+    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(
         os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIBRARY):
+    if not (os.path.exists(LIBRARY) and os.path.exists(MARSHAL)):
         return False
-    t = os.path.getmtime(LIBRARY)
+    t = min(os.path.getmtime(LIBRARY), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def marshal_commands(nvcc):
+    """The compiler's and the linker's command for ``_marshal.so``."""
+    cxx = os.environ.get("CXX") or shutil.which("g++")
+    if not cxx:
+        raise RuntimeError("g++ not found: it is required to build _marshal.so")
+    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    include = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
+    obj = os.path.join(BUILD, "pkv_marshal.o")
+    compile_it = [cxx, "-c", os.path.join(CSRC, "pkv_marshal.cpp"), "-o", obj, "-O2", "-std=c++17", "-fPIC"]
+    for path in include:
+        compile_it += ["-isystem" if path is not INCLUDE else "-I", path]
+    link = [cxx, "-shared", "-o", MARSHAL + ".tmp", obj, "-L", HERE, "-l:" + os.path.basename(LIBRARY), "-L",
+            os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    return compile_it, link
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -58,6 +80,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [nvcc, "-c", src, "-o", obj] + common
         procs.append((src, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                  stderr=subprocess.STDOUT)))
+    compile_it, link_marshal = marshal_commands(nvcc)
+    procs.append((compile_it[2], compile_it, subprocess.Popen(compile_it, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     log = []
     failed = []
     for src, cmd, p in procs:
@@ -70,13 +94,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         f.write("\n".join(log))
     if failed:
         msg = "\n".join(f"{s}:\n{c}\n{t}" for s, c, t in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"the compiler failed:\n{msg}")
     tmp = LIBRARY + ".tmp"
     link = [nvcc, "-shared", "-o", tmp] + objs + ARCH + ["-Xcompiler", "-fPIC"]
     r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, LIBRARY)
+    r = subprocess.run(link_marshal, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
+    os.replace(MARSHAL + ".tmp", MARSHAL)
     if verbose:
         print("\n".join(log))
     return LIBRARY
