@@ -20,7 +20,7 @@
 // warp's lines.  All lines are asked for before the token's position is known, so the chain position -> table row
 // runs beside them.  A pair's other element comes by a shuffle.
 //
-// Measured, 16384 tokens, 32 query and 8 KV heads of 128: into the 16-bit cache (407 MB) 68 us, 88 % of the
+// Measured, 16384 tokens, 32 query and 8 KV heads of 128: into the 16-bit cache (407 MB) 61 us, 98 % of the
 // copy rate; into the 4-bit one (321 MB, three axes) 75 us, 63 %, bound by instructions (0.71 a cycle issued, half of
 // them the conversions' on the integer pipe), and reading the lines back (120 MB, most of it from and to L2) 16 us.
 // With divisions instead of corrected products 115 us for the two where 101 remained (8 and 4 steps a warp).
@@ -32,11 +32,14 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-// Line steps of a warp: queries; keys and values together.  (16384 tokens, 32 query and 8 KV heads x 128: 8 and 4 take
-// 68 us into the 16-bit cache and 101 us into the 4-bit one with the reading back, 4 and 2 68 and 87, 8 and 2 76 and
-// 94, 8 and 1 86 and 111; with three axes and fewer heads 8 and 4 are 6 % faster than 4 and 2.)
-constexpr int q_steps(bool kv4) { return kv4 ? 4 : 8; }
-constexpr int kv_steps(bool kv4) { return kv4 ? 2 : 4; }
+// Line steps of a warp: queries; keys and values together.  Threads of a CTA, and CTAs that an SM holds, by the cache.
+// (16384 tokens, 32 query and 8 KV heads x 128, and 6007 of fewer heads on three axes, both into the 16-bit cache: 61.1 and 19.4
+// us; 8 and 4 steps 60.9 and 20.0, 7 and 2 66.8 and 19.3; with CTAs of 128 threads 61.6 and 20.2, of 32 60.7 and 20.8;
+// without streaming loads and stores 63.6 and 20.5.  Into the 4-bit cache, with the reading back: 87 us; 8 and 4 steps 101, 8 and 2
+// 94, CTAs of 64 threads 91; more warps an SM than these registers leave 89 and 95.)
+constexpr int kQSteps = 4, kKvSteps = 2;
+constexpr int threads_of(bool kv4) { return kv4 ? 128 : 64; }
+constexpr int resident_of(bool kv4) { return kv4 ? 8 : 12; }
 constexpr int kLoadSteps = 2;
 constexpr int kMaxAxes = 8;
 
@@ -207,9 +210,9 @@ __device__ __forceinline__ uint32_t scale_word(uint32_t scale, int l) {
 }
 
 template <int D, bool kFp16, bool kKv4>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(threads_of(kKv4), resident_of(kKv4)) append_kernel(const AppendParams p) {
     constexpr int kLine = D / 8, kAtOnce = 32 / kLine;             // lanes of a line, lines of a step
-    constexpr int kQSteps = q_steps(kKv4), kKvSteps = kv_steps(kKv4);
+    constexpr int kWarps = threads_of(kKv4) / 32;
     pdl_wait();
     pdl_trigger();
     const int64_t job = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
 #pragma unroll
         for (int i = 0; i < kQSteps; i++) {
             raw[i] = make_uint4(0, 0, 0, 0);
-            if (h0 + i * kAtOnce < p.Hq) raw[i] = *reinterpret_cast<const uint4 *>(src + 2LL * D * (h0 + i * kAtOnce));
+            if (h0 + i * kAtOnce < p.Hq) raw[i] = __ldcs(reinterpret_cast<const uint4 *>(src + 2LL * D * (h0 + i * kAtOnce)));
         }
         if (!make_turn<D>(p.rope, t, w, p.err)) return;
 #pragma unroll
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
             float x[8];
             turned<kFp16>(p.rope, w, raw[i], x);
             if (w.on) raw[i] = rounded<kFp16>(x);
-            if (h0 + i * kAtOnce < p.Hq) *reinterpret_cast<uint4 *>(dst + 2LL * D * (h0 + i * kAtOnce)) = raw[i];
+            if (h0 + i * kAtOnce < p.Hq) __stcs(reinterpret_cast<uint4 *>(dst + 2LL * D * (h0 + i * kAtOnce)), raw[i]);
         }
         return;
     }
@@ -247,8 +250,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         const int h = h0 + i * kAtOnce;
         rk[i] = rv[i] = make_uint4(0, 0, 0, 0);
         if (h < p.H) {
-            rk[i] = __ldg(reinterpret_cast<const uint4 *>(ksrc + 2LL * D * h));
-            rv[i] = __ldg(reinterpret_cast<const uint4 *>(vsrc + 2LL * D * h));
+            rk[i] = __ldcs(reinterpret_cast<const uint4 *>(ksrc + 2LL * D * h));
+            rv[i] = __ldcs(reinterpret_cast<const uint4 *>(vsrc + 2LL * D * h));
         }
     }
     if (!make_turn<D>(p.rope, t, w, p.err)) return;
@@ -285,8 +288,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
             if (w.on) rk[i] = rounded<kFp16>(x);
             if (h < p.H) {
                 const int64_t at = (slot * p.H + h) * (2 * D) + 16 * l;
-                *reinterpret_cast<uint4 *>(p.kc + at) = rk[i];
-                *reinterpret_cast<uint4 *>(p.vc + at) = rv[i];
+                __stcs(reinterpret_cast<uint4 *>(p.kc + at), rk[i]);
+                __stcs(reinterpret_cast<uint4 *>(p.vc + at), rv[i]);
             }
         }
     }
@@ -397,7 +400,7 @@ int check_rows(AppendParams &p, bool kv4, const void *k, const void *v, int32_t 
     if (p.T > 1 && (p.k_stride < line || p.v_stride < line || (p.Hq > 0 && (p.q_stride < row || p.q_out_stride < row))))
         return PKV_ERR_INVALID_ARG;
     const int lines = 32 / (head_dim / 8);
-    const int q_lines = q_steps(kv4) * lines, kv_lines = kv_steps(kv4) * lines;
+    const int q_lines = kQSteps * lines, kv_lines = kKvSteps * lines;
     p.q_parts = (p.Hq + q_lines - 1) / q_lines;
     p.parts = p.q_parts + (p.H + kv_lines - 1) / kv_lines;
     p.jobs = static_cast<int64_t>(p.T) * p.parts;
@@ -405,7 +408,8 @@ int check_rows(AppendParams &p, bool kv4, const void *k, const void *v, int32_t 
     p.v = static_cast<const char *>(v);
     p.q = static_cast<const char *>(q);
     p.q_out = static_cast<char *>(q_out);
-    return (p.jobs + kWarps - 1) / kWarps > 0x7fffffff ? PKV_ERR_INVALID_ARG : PKV_OK;
+    const int warps = threads_of(kv4) / 32;
+    return (p.jobs + warps - 1) / warps > 0x7fffffff ? PKV_ERR_INVALID_ARG : PKV_OK;
 }
 
 template <bool kKv4>
@@ -414,7 +418,8 @@ int launch_append(const AppendParams &p, int32_t head_dim, int32_t dtype, cudaSt
     auto kernel = head_dim == 64    ? (h ? append_kernel<64, true, kKv4> : append_kernel<64, false, kKv4>)
                   : head_dim == 128 ? (h ? append_kernel<128, true, kKv4> : append_kernel<128, false, kKv4>)
                                     : (h ? append_kernel<256, true, kKv4> : append_kernel<256, false, kKv4>);
-    PKV_CUDA_TRY(launch_pdl(kernel, dim3(static_cast<unsigned>((p.jobs + kWarps - 1) / kWarps)), dim3(kThreads), 0, s, p));
+    constexpr int warps = threads_of(kKv4) / 32;
+    PKV_CUDA_TRY(launch_pdl(kernel, dim3(static_cast<unsigned>((p.jobs + warps - 1) / warps)), dim3(32 * warps), 0, s, p));
     return PKV_OK;
 }
 
