@@ -10,7 +10,8 @@
 // lie exactly half way between two codes and a product with a reciprocal would
 // move them.  A quotient is such a product with its error x - y (scale unit), exact in a fused
 // multiply-add, brought back once (Markstein's correction): exact where the quotient is a
-// floating-point number, as those middles are; 3 operations where a division takes a dozen.
+// floating-point number, as those middles are; 3 operations where a division takes a dozen.  A scale's reciprocal is
+// the hardware's approximation after one step of Newton's.
 //
 // Bound: HBM (every line read and written once), or launch latency for a decode
 // step.
@@ -21,9 +22,10 @@
 // runs beside them.  A pair's other element comes by a shuffle.
 //
 // Measured, 16384 tokens, 32 query and 8 KV heads of 128: into the 16-bit cache (407 MB) 61 us, 98 % of the
-// copy rate; into the 4-bit one (321 MB, three axes) 75 us, 63 %, bound by instructions (0.71 a cycle issued, half of
-// them the conversions' on the integer pipe), and reading the lines back (120 MB, most of it from and to L2) 16 us.
-// With divisions instead of corrected products 115 us for the two where 101 remained (8 and 4 steps a warp).
+// copy rate; into the 4-bit one and the lines read back (321 and 120 MB, three axes) 82 us, 79 %: the append takes 69, bound
+// by instructions (half of them conversions and maxima on the integer pipe), the reading 13.5, most of it from and to L2.
+// The two with divisions 115 us where 101 remained; with the scale's quotient a division 85.7 where 84.3 remained, with maxima
+// of bit patterns 84.3 and 83.7.
 #include "pkv_kv4.cuh"
 #include "pkv_kv8_attention.cuh"
 
@@ -35,12 +37,12 @@ constexpr int kWarps = kThreads / 32;
 // Line steps of a warp: queries; keys and values together.  Threads of a CTA, and CTAs that an SM holds, by the cache.
 // (16384 tokens, 32 query and 8 KV heads x 128, and 6007 of fewer heads on three axes, both into the 16-bit cache: 61.1 and 19.4
 // us; 8 and 4 steps 60.9 and 20.0, 7 and 2 66.8 and 19.3; with CTAs of 128 threads 61.6 and 20.2, of 32 60.7 and 20.8;
-// without streaming loads and stores 63.6 and 20.5.  Into the 4-bit cache, with the reading back: 87 us; 8 and 4 steps 101, 8 and 2
-// 94, CTAs of 64 threads 91; more warps an SM than these registers leave 89 and 95.)
+// without streaming loads and stores 63.6 and 20.5.  Into the 4-bit cache, with the reading back: 82 us; 8 and 2 steps 88,
+// 4 and 1 92, CTAs of 64 threads 91, of 256 87; eight CTAs an SM 82.6, six 87, nine 89.)
 constexpr int kQSteps = 4, kKvSteps = 2;
 constexpr int threads_of(bool kv4) { return kv4 ? 128 : 64; }
-constexpr int resident_of(bool kv4) { return kv4 ? 8 : 12; }
-constexpr int kLoadSteps = 2;
+constexpr int resident_of(bool kv4) { return kv4 ? 7 : 12; }
+constexpr int kLoadSteps = 4;            // (append and reading back together: 82.6 us; two 83.7, one 88.0)
 constexpr int kMaxAxes = 8;
 
 struct Rope {
@@ -59,7 +61,7 @@ struct AppendParams {
     uint8_t *kc, *vc, *ks, *vs;
     const int64_t *slots;
     int64_t num_slots, jobs;
-    float k_unit, v_unit, k_six, v_six;               // six times the unit
+    float k_unit, v_unit, k_six, v_six, k_sixth, v_sixth;      // six times the unit, and its reciprocal
     int32_t T, Hq, H, bs, q_parts, parts;
     int32_t *err;
 };
@@ -171,22 +173,35 @@ __device__ __forceinline__ uint4 rounded(const float (&x)[8]) {
                       pack_out(x[6], x[7], kFp16));
 }
 
+// The largest of three, NaN if one is.
+__device__ __forceinline__ float nan_max3(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+__device__ __forceinline__ float rcp_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Eight of a group's 16 elements (the neighbouring lane has the others): codes, and the group's scale.
 struct Quantised {
     uint32_t codes, scale;
     bool nan;
 };
-__device__ __forceinline__ Quantised quantise(const float (&x)[8], float unit, float six) {
-    uint32_t m = 0;                                   // magnitudes order as their bits, NaN above all
-#pragma unroll
-    for (int i = 0; i < 8; i++) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(~0u, m, 1));
+__device__ __forceinline__ Quantised quantise(const float (&x)[8], float unit, float six, float sixth) {
+    float most = nan_max3(nan_max3(nan_max3(fabsf(x[0]), fabsf(x[1]), fabsf(x[2])), fabsf(x[3]), fabsf(x[4])), fabsf(x[5]), fabsf(x[6]));
+    most = nan_max3(most, fabsf(x[7]), 0.f);
+    most = nan_max3(most, __shfl_xor_sync(~0u, most, 1), 0.f);
     Quantised z;
-    z.nan = m > 0x7f800000u;
-    z.scale = e4m3x2(__fdiv_rn(__uint_as_float(m), six), 0.f) & 0xffu;
-    const float by = floats_of(z.scale).x * unit, inverse = __frcp_rn(by);
+    z.nan = most != most;
+    const float first = most * sixth;                 // corrected where it is not far past the largest scale
+    z.scale = e4m3x2(first < 1024.f ? fmaf(fmaf(-first, six, most), sixth, first) : first, 0.f) & 0xffu;
+    const float by = floats_of(z.scale).x * unit, guess = rcp_fast(by), inverse = fmaf(fmaf(-by, guess, 1.f), guess, guess);
     float y[8];
-    if (__uint_as_float(m) * inverse < 0x1p64f) {
+    if (most * inverse < 0x1p64f) {
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             const float near = x[i] * inverse;
@@ -267,9 +282,9 @@ __global__ void __launch_bounds__(threads_of(kKv4), resident_of(kKv4)) append_ke
         float x[8];
         turned<kFp16>(p.rope, w, rk[i], x);
         if constexpr (kKv4) {
-            Quantised a = quantise(x, p.k_unit, p.k_six);
+            Quantised a = quantise(x, p.k_unit, p.k_six, p.k_sixth);
             widen8<kFp16>(rv[i], x);
-            Quantised b = quantise(x, p.v_unit, p.v_six);
+            Quantised b = quantise(x, p.v_unit, p.v_six, p.v_sixth);
             // a NaN value is noted in the line's first key scale
             const uint32_t nan = __ballot_sync(~0u, b.nan) >> (mine * kLine);
             if (b.nan) b.scale = b.codes = 0;
@@ -482,6 +497,8 @@ int pkv_kv4_store(const pkv_kv4_cache *cache, const pkv_rope *rope, const void *
     p.v_unit = cache->v_unit;
     p.k_six = 6.f * cache->k_unit;
     p.v_six = 6.f * cache->v_unit;
+    p.k_sixth = 1.f / p.k_six;
+    p.v_sixth = 1.f / p.v_six;
     p.err = d_error;
     rc = pkv::check_rows(p, true, k, v, cache->head_dim, dtype, q, q_out);
     if (rc == PKV_OK && num_tokens > 0 && rope) rc = pkv::check_rope(rope, cache->head_dim, num_tokens, &p.rope);
