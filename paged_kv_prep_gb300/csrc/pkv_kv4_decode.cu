@@ -23,16 +23,17 @@
 // A range that ends inside a request leaves a partial result (R, sum, O) that a second
 // kernel merges in a fixed order.
 //
-// Measured, with the merge: 256 single tokens, 32 query and 8 KV heads of 128, contexts up to 8192 (1.16 GB) 224 us,
-// 77 % of the copy rate; four of 64 query heads on 65536 to 131072 tokens (455 MB) 97 us, 69 %; 96 requests
-// of two to six tokens, 40 query heads, a window of 4096 (411 MB; 656 MB are read, as a request of more than 16 rows
-// takes two tiles) 218 us.
+// Measured, with the merge: 256 single tokens, 32 query and 8 KV heads of 128, contexts up to 8192 (1.16 GB) 221 us,
+// 78 % of the copy rate; four of 64 query heads on 65536 to 131072 tokens (455 MB) 96 us, 70 %; 96 requests
+// of two to six tokens, 40 query heads, a window of 4096 (411 MB; a request of more than 16 rows takes two tiles,
+// which both go through its lines) 218 us.
 // Instructions bound it next to HBM: 129 for 1 KB of codes with eight rows, 0.6 a cycle issued, the
-// integer pipe 50 % busy with the conversions.  Tiles of eight rows: twelve warps an SM, 224 us for the 256; eight 262, ten
-// 264, fourteen 262, sixteen (fewer registers) 242; a second unit on its way changes nothing.  Tiles of sixteen rows, head_dim
-// 128: eight warps with the queries in shared memory, 218 us for the 96 requests; twelve so 222, queries in registers
+// integer pipe 50 % busy with the conversions.  Tiles of eight rows: twelve warps an SM, 221 us for the 256; eight 262, ten
+// 264, thirteen 261, fourteen 246, sixteen (spilling) 236; queries in registers 224; a second unit on its way 224.  Tiles of
+// sixteen rows: eight warps 218 us for the 96 requests; twelve 222, queries in registers
 // 227 and (twelve, spilling) 232; 24 rows 262; as many groups of eight rows as a request needs, up to 32, 269.
-// Of head_dim 64 twelve warps 274 us where eight take 326; of 256 queries in registers 223 where shared memory takes 227.
+// Of head_dim 64 sixteen warps 151 us for the 256 where twelve take 159, with sixteen rows twelve 274 where eight take 326; of
+// 256 queries in registers 223 us (128 requests of up to five tokens) where shared memory takes 227.
 #include "pkv_kv4_attention.cuh"
 #include "pkv_tcgen05.cuh"
 
@@ -61,13 +62,14 @@ __device__ __forceinline__ int at(int token, int piece) {
     return token * 128 + 16 * (piece ^ (token & 6) ^ ((token & 1) << 2));
 }
 
+// Warps of an SM.  Four schedulers share them, so that numbers between these are slower than both neighbours.
 template <int D, int NT>
-constexpr int warps_of() { return D == 256 || (D == 128 && NT > 1) ? 8 : 12; }
+constexpr int warps_of() { return D == 64 ? (NT > 1 ? 12 : 16) : D == 128 && NT == 1 ? 12 : 8; }
 
-// Queries of tiles of sixteen rows lie in shared memory (with the accumulator they are more than the registers that
-// leave enough warps): fragments of two steps, 16 bytes a lane, for each eight rows.  For D = 256 registers spill either way.
+// Queries lie in shared memory (with the accumulator they are more than the registers that leave enough warps): fragments
+// of two steps, 16 bytes a lane, for each eight rows.  For D = 256 registers spill either way.
 template <int D, int NT>
-constexpr int query_bytes() { return NT > 1 && D < 256 ? 8 * NT * D * 2 : 0; }
+constexpr int query_bytes() { return D < 256 ? 8 * NT * D * 2 : 0; }
 
 // Units of a request: 32-token units of its visible range, once per tile of 8 * NT rows.
 template <int NT>
