@@ -6,7 +6,7 @@
 // Bound: latency (the note, the request, the references, the rows come one after the other); the pieces lie in L2.
 //
 // Layout.  A CTA belongs to one note.  Row tiles of chunks have 256 rows in two or three pieces: a warp takes four rows, all
-// of their loads on their way at once.  Single tokens have eight rows: a warp each, or, where few requests
+// of their loads on their way at once.  Few tokens have eight rows or sixteen: a warp each, or, where few requests
 // are cut into long chains, four warps a row, which share out its pieces and meet in shared memory; few notes are
 // real then, so a CTA looks at several.
 // Measured: 256 decodes 9.9 us, four long ones 13.8 us, a mixed call's chunks 20.8 us (one warp a row
@@ -127,31 +127,34 @@ __global__ void __launch_bounds__(kThreads) kv4_merge_kernel(const AttnParams p,
                                     0, nullptr);
 }
 
-// Tiles of eight rows; a CTA looks at up to 32 workers' notes.
+// Eight rows of tiles of `rows`; a CTA looks at up to 32 workers' notes.
 template <int D>
-__global__ void __launch_bounds__(kChainThreads) kv4_merge_chains_kernel(const AttnParams p, int workers, int stride) {
+__global__ void __launch_bounds__(kChainThreads) kv4_merge_chains_kernel(const AttnParams p, int rows, int workers, int stride) {
     __shared__ float s_acc[8][kTeamWarps][D + 1];
     static_assert(kChainThreads / 32 == 8 * kTeamWarps, "eight rows");
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) / kTeamWarps;
+    const int lane = threadIdx.x & 31, row = (threadIdx.x >> 5) / kTeamWarps, eights = rows / 8;
+    const int step = gridDim.x / eights, first = blockIdx.x / eights, row0 = 8 * (blockIdx.x - first * eights);
     // neighbouring workers, which begin the same request's heads, go to different CTAs
-    const int mine = blockIdx.x + lane * gridDim.x;
+    const int mine = first + lane * step;
     uint32_t real = __ballot_sync(~0u, mine < workers && p.meta[mine < workers ? mine : 0].x >= 0);
     for (; real; real &= real - 1) {
-        const int worker = blockIdx.x + (__ffs(real) - 1) * gridDim.x;
-        merge_rows<D, 1, kTeamWarps, 4>(p, 8, stride, worker, p.meta[worker], row, (threadIdx.x >> 5) % kTeamWarps, s_acc[row]);
+        const int worker = first + (__ffs(real) - 1) * step;
+        merge_rows<D, 1, kTeamWarps, 4>(p, rows, stride, worker, p.meta[worker], row0 + row, (threadIdx.x >> 5) % kTeamWarps, s_acc[row]);
         __syncthreads();                               // the sums have been read
     }
 }
 
 template <int D>
 int launch(const AttnParams &p, int rows, int workers, int stride, int sms, cudaStream_t s) {
-    // chains: the row tiles (of all heads) that the batch can have are an eighth of the workers or fewer
+    // chains: the row tiles (of all heads) that the batch can have are an eighth of the workers or fewer (calls of two
+    // requests' four drafts on 60000 tokens 54 us so, 71 with a warp a row; of eight single tokens of 16 heads 19.6 and 24)
     const int64_t tiles = (static_cast<int64_t>(p.T) * p.G / rows + p.n) * p.Hkv;
-    if (rows == 8 && tiles * 8 <= workers) {
+    if (rows <= 16 && tiles * 8 <= workers) {
         const int grid = workers < 32 * sms ? sms : (workers + 31) / 32;
-        PKV_CUDA_TRY(launch_pdl(kv4_merge_chains_kernel<D>, dim3(workers < grid ? workers : grid), dim3(kChainThreads), 0, s, p, workers, stride));
+        PKV_CUDA_TRY(launch_pdl(kv4_merge_chains_kernel<D>, dim3((workers < grid ? workers : grid) * (rows / 8)), dim3(kChainThreads), 0, s, p,
+                                rows, workers, stride));
         return PKV_OK;
     }
     constexpr int kTileRows = D == 256 ? 2 : 4;
