@@ -330,6 +330,13 @@ def test_many_requests():
     check(Case([(1 + x % 3, x + 2) for x in lens] + [(30, 100)], 16, 8, 4, 128, seed=21), window=100)
 
 
+@pytest.mark.parametrize("group,run", [(1, 3), (4, 4), (7, 2), (16, 1), (12, 2)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_long_chains_of_pieces(d, group, run):
+    """Few requests, long contexts: every row in many pieces, the last tile of few rows, one request next to nothing."""
+    check(Case([(run, 7000), (1, 3), (run, 2001)], 16, 2, group, d, seed=27))
+
+
 @pytest.mark.parametrize("d,bs,window", [(64, 16, 0), (128, 32, 9)])
 def test_many_chunks(d, bs, window):
     """More requests than a CTA has threads, of more rows than the decode kernel takes; single and no tokens between them."""
