@@ -337,6 +337,18 @@ def test_long_chains_of_pieces(d, group, run):
     check(Case([(run, 7000), (1, 3), (run, 2001)], 16, 2, group, d, seed=27))
 
 
+@pytest.mark.parametrize("d,heads", [(64, 2), (128, 2), (128, 1)])
+@pytest.mark.parametrize("reqs", [[(300, 700), (1, 90), (0, 5), (1, 1), (5, 260), (1, 2000)], [(70, 70)], [(9, 500)]])
+def test_small_batches_with_chunks(reqs, d, heads):
+    """Between narrow tables and wide ones the kernels change; a window ends a request's units early."""
+    for width in (None, 20000):
+        case = Case(reqs, 16, heads, 4, d, seed=28)
+        if width:
+            case.tables = torch.cat([case.tables, torch.full((len(reqs), width - case.tables.shape[1]), -1, dtype=torch.int32)], 1)
+        check(case)
+        check(case, window=100)
+
+
 @pytest.mark.parametrize("d,bs,window", [(64, 16, 0), (128, 32, 9)])
 def test_many_chunks(d, bs, window):
     """More requests than a CTA has threads, of more rows than the decode kernel takes; single and no tokens between them."""
