@@ -94,13 +94,14 @@ int pkv_kv4_attention(const pkv_kv4_cache *cache, const void *q, int64_t q_strid
     // 17.9, 128 18.3 and 22.9, 2048 128 and 127; of 512 tokens, 128 requests 29.1 and 27.5, 32 27.6 and 18.7.
     const int64_t most = static_cast<int64_t>(p.W) * p.bs;
     p.whole = most <= 64 || (most <= 256 && static_cast<int64_t>(n) * p.Hkv >= 2 * sms);
-    // The prefill kernel takes everything, without a second pair of launches, where the requests have more than 32 rows on
+    // The prefill kernel takes everything, without a second pair of launches, where the requests have more than 8 rows on
     // average and there is one of them, or no more row tiles of single tokens than SMs, and of 128-token units, by the
     // tables' width, no more than 32 an SM.  8 KV heads, two chunks of 300 tokens and single tokens, alone and with
     // the decode kernel: 16 on 1000 tokens 52 and 61 us, on 4000 82 and 83, on 16000 198 and 160; 32 on 1000 68 and 63, on
-    // 4000 120 and 100; a chunk of 256 tokens by itself 29 and 36.
+    // 4000 120 and 100; a chunk of 256 tokens by itself 29 and 36; eight requests of two to six tokens, five heads a KV head, on
+    // up to 2000 tokens 29 and 37, of two to five on up to 8000 with one KV head 31 and 55.
     const int64_t tiles = static_cast<int64_t>(n) * p.Hkv;
-    const bool alone = prefill && static_cast<int64_t>(num_tokens) * p.G > 32LL * n &&
+    const bool alone = prefill && static_cast<int64_t>(num_tokens) * p.G > 8LL * n &&
                        (n == 1 || (tiles <= sms && tiles * (most / 128 + 1) <= 32LL * sms));
     p.short_rows = alone ? 0 : prefill ? rows : 0x7fffffff;
     // one 8-row tile holds every request that the decode kernel takes
