@@ -77,7 +77,7 @@ __device__ __forceinline__ void merge_rows(const AttnParams &p, int rows, int st
             for (int i = 0; i < kRows; i++) {
                 // a piece without a reference adds nothing, unless its logits were NaN
                 const float f = m[b][i] == -INFINITY ? (l[b][i] == 0.f ? 0.f : NAN) : exp2_fast(m[b][i] - top[i]);
-                if (f != 0.f) {
+                if (f != 0.f || l[b][i] != l[b][i]) {  // a NaN counts however small its piece is
                     sum[i] = fmaf(f, l[b][i], sum[i]);
 #pragma unroll
                     for (int c = 0; c < kPer; c++) acc[i][c] = fmaf(f, y[b][i][c], acc[i][c]);
