@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(kMergeThreads) kv8_merge_kernel(const AttnPara
 #pragma unroll
             for (int k = 0; k < kBatch; k++) {
                 const float f2 = __shfl_sync(~0u, fac, k1 + k);
-                if (k1 + k < n && f2 != 0.f) {
+                if (k1 + k < n) {                        // 0 times NaN is NaN: a NaN counts however small its piece is
 #pragma unroll
                     for (int c = 0; c < kPer; c++) acc[c] = fmaf(f2, y[k][c], acc[c]);
                 }

@@ -1,0 +1,37 @@
+"""kv8_attention: a NaN value in a piece of a request that weighs nothing beside the others."""
+import pytest
+
+import paged_kv_prep_gb300 as pkv
+from tests.test_kv8_attention_gpu import Case, compare
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_kv_prep_gb300 import build as pbuild
+    pbuild.build()
+    yield
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("reqs", [[(1, 3100), (1, 900)], [(4, 3100), (3, 900)], [(300, 3000), (1, 900)]],
+                         ids=["decodes", "drafts", "chunk"])
+def test_a_nan_in_a_piece_whose_weights_vanish(reqs, d):
+    """The first third of each context has logits of 0, the rest of 2 d: 0 times NaN is NaN."""
+    case = Case(reqs, 16, 2, 4, d, seed=31)
+    case.q.fill_(2.0)
+    case.scales[0].fill_(1.0)
+    for i, (_, x) in enumerate(reqs):
+        s = torch.arange(x)
+        slot = case.tables[i].long()[s // 16] * 16 + s % 16
+        case.caches[0][slot] = torch.where(s < x // 3, 0, 0x38).to(torch.uint8)[:, None, None]      # 0 and 1
+        if i == 0:
+            case.caches[1][slot[10], 1, 5] = 127
+    out, lse = pkv.kv8_attention(*case.args(), softmax_scale=1.0)
+    compare(case, out, lse, case.reference(1.0, 0))
+    nan = out[:case.starts[1]].isnan()
+    # the queries of the chunk stand behind the NaN's token
+    assert nan[:, 4:, 5].all() and not nan[:, :4].any() and int(nan.sum()) == 4 * nan.shape[0]
