@@ -81,9 +81,9 @@ __device__ __forceinline__ Req request_of(const AttnParams &p, int i, bool repor
     return r;
 }
 
-// First position that a query at `pos` sees.
+// First position that a query at `pos` sees.  (Before position 0, pos - window may pass the smallest integer.)
 __device__ __forceinline__ int32_t lo_of(const AttnParams &p, int32_t pos) {
-    return p.window > 0 ? max(0, pos - p.window + 1) : 0;
+    return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
 }
 
 // Value scales below 2^-100 (an unwritten block's zero among them) count as 2^-100, so that their

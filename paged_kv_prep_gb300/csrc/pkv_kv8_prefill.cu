@@ -76,7 +76,7 @@ __device__ __forceinline__ Span span_of(const AttnParams &p, const Req &r, int r
     const int rows = r.count * p.G, f0 = rt * kRows, f1 = min(rows, f0 + kRows) - 1;
     const int back = r.len - r.count, pos0 = back + f0 / p.G, pos1 = back + f1 / p.G;
     Span s;
-    s.lo = p.window > 0 ? max(0, pos0 - p.window + 1) : 0;
+    s.lo = lo_of(p, pos0);
     s.hi = min(pos1 + 1, r.keys);
     s.base = s.lo & ~15;
     s.units = s.hi > s.base ? (s.hi - s.base + kKeys - 1) / kKeys : 1;   // a tile without keys writes zeros

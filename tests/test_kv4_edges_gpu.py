@@ -1,7 +1,10 @@
-"""kv4_attention where a request's pieces are far apart in size; against the plain implementation in 64 bits, with
-the tolerances of test_kv4_attention_gpu."""
+"""kv4_attention where a request's pieces are far apart in size, and at the ends of the integers that count its
+positions; against the plain implementation in 64 bits, with the tolerances of test_kv4_attention_gpu."""
+import math
+
 import pytest
 
+import paged_kv_prep_gb300 as pkv
 from tests.test_kv4_attention_gpu import Case, check
 
 pytestmark = pytest.mark.gpu
@@ -33,3 +36,17 @@ def test_a_nan_in_a_piece_whose_weights_vanish(reqs, d):
             case.scales[0][int(case.tables[i, 0]), 1, 10, 2] = 127
     out, lse = check(case, scale=1.0)
     assert out[0, 4:].isnan().all() and out[0, :4].isfinite().all() and out[case.starts[1]:case.starts[2]].isfinite().all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("reqs", [[(6, 2), (1, 40), (9, 3)], [(70, 5), (1, 40)]], ids=["drafts", "chunk"])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5])
+def test_windows_of_all_positions_before_the_first(reqs, d, window):
+    """More queries than cached tokens: the first ones stand before position 0 and see nothing, the others see what
+    they would without a window."""
+    case = Case(reqs, 16, 2, 4, d, seed=32)
+    out, lse = check(case, window=window)
+    plain = pkv.kv4_attention(*case.args())
+    assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
+    c, x = reqs[0]
+    assert (lse[:c - x] == -math.inf).all() and lse[c - x:c].isfinite().all()

@@ -1,4 +1,4 @@
-"""kv8_attention: a NaN value in a piece of a request that weighs nothing beside the others."""
+"""kv8_attention: a NaN value in a piece of a request that weighs nothing beside the others, and the largest windows."""
 import pytest
 
 import paged_kv_prep_gb300 as pkv
@@ -35,3 +35,14 @@ def test_a_nan_in_a_piece_whose_weights_vanish(reqs, d):
     nan = out[:case.starts[1]].isnan()
     # the queries of the chunk stand behind the NaN's token
     assert nan[:, 4:, 5].all() and not nan[:, :4].any() and int(nan.sum()) == 4 * nan.shape[0]
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("reqs", [[(6, 2), (1, 40), (9, 3)], [(70, 5), (1, 40)]], ids=["drafts", "chunk"])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 5])
+def test_windows_of_all_positions_before_the_first(reqs, d, window):
+    """More queries than cached tokens: the first ones stand before position 0."""
+    a = Case(reqs, 16, 2, 4, d, seed=32).args()
+    out, lse = pkv.kv8_attention(*a, window=window)
+    plain = pkv.kv8_attention(*a)
+    assert torch.equal(out, plain[0]) and torch.equal(lse, plain[1])
