@@ -580,7 +580,7 @@ int launch(const Kv4Params &p, int sms, cudaStream_t s) {
     // One CTA an SM, or as many as the longest requests the tables can name would give a unit a warp; but a
     // warp for each KV head at least, or the batch would have no range.
     const int64_t tiles = static_cast<int64_t>(p.T) * p.G / (8 * NT) + p.n;
-    const int64_t most = tiles * (static_cast<int64_t>(p.W) * p.bs / kUnit + 2) * p.Hkv;
+    const int64_t most = tiles * most_units(p, kUnit) * p.Hkv;
     const int least = (p.Hkv + kWarps - 1) / kWarps, full = sms > least ? sms : least;
     const int grid = most < static_cast<int64_t>(full) * kWarps ? static_cast<int>((most + kWarps - 1) / kWarps) : full;
     PKV_CUDA_TRY(launch_pdl(kv4_decode_kernel<D, NT>, dim3(grid), dim3(32 * kWarps), smem, s, p));

@@ -51,13 +51,16 @@ inline int64_t kv8_most_workers(int sms) {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Positions that are seen lie below this, so that the end of a unit, or of the one after it, fits 32 bits.
+constexpr int32_t kMostKeys = 0x7fffffff - 4095;
+
 // One request's share of the batch.
 struct Req {
     int32_t start;                 // its first token in the batch
     int32_t count;                 // scheduled tokens (0: nothing to do)
-    int32_t len;                   // cached tokens, those of this step included
+    int32_t len;                   // cached tokens, those of this step included; 0 where the batch has less
     int32_t lo;                    // first key that any of its queries sees
-    int32_t keys;                  // keys that its block table can name
+    int32_t keys;                  // keys that its block table can name, below kMostKeys
 };
 
 __device__ __forceinline__ Req request_of(const AttnParams &p, int i, bool report = false) {
@@ -65,12 +68,12 @@ __device__ __forceinline__ Req request_of(const AttnParams &p, int i, bool repor
     const int32_t a = p.qsl[i], b = p.qsl[i + 1];
     r.start = a;
     r.count = b - a;
-    r.len = p.lens[i];
+    r.len = max(p.lens[i], 0);
     if (a < 0 || b < a || b > p.T) {
         if (report && p.err) atomicOr(p.err, PKV_DEVERR_COUNT);
         r.count = 0;
     }
-    const int64_t cap = static_cast<int64_t>(p.W) * p.bs;
+    const int64_t width = static_cast<int64_t>(p.W) * p.bs, cap = width < kMostKeys ? width : kMostKeys;
     if (r.len > cap && report && p.err && r.count > 0) atomicOr(p.err, PKV_DEVERR_BLOCK);
     r.keys = r.len < cap ? r.len : static_cast<int32_t>(cap);
     r.lo = 0;
@@ -98,6 +101,13 @@ __device__ __forceinline__ int32_t block_of(const AttnParams &p, const int32_t *
         return -1;
     }
     return b < 0 ? -1 : b;
+}
+
+// Units of `tokens` that the tables' longest request can have, and two; no more than 2^20, which is more than any launch
+// has warps, so that a product with row tiles and heads fits 64 bits.
+inline int64_t most_units(const AttnParams &p, int tokens) {
+    const int64_t units = static_cast<int64_t>(p.W) * p.bs / tokens + 2;
+    return units < (1 << 20) ? units : 1 << 20;
 }
 
 // Prefix sums of the requests' units: thread c of the CTA holds requests c * per .. (c + 1) * per - 1.
