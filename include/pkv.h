@@ -639,7 +639,7 @@ int pkv_kv8_attention_workspace(int32_t num_tokens, int32_t num_q_heads, int32_t
  * A row that sees nothing gives 0 and -inf.  Tokens past query_start_loc[n] are
  * not written.  Device errors: PKV_DEVERR_COUNT (query_start_loc descends or
  * leaves the batch: the request is skipped), PKV_DEVERR_BLOCK (a block id past
- * the cache, a position past the table or one of the last 4096 below 2^31: not seen).
+ * the cache, a position past the table or in a block that ends past 2^31 - 4096: not seen).
  * The products' operands are f16 (a code is exact in f16, a query after scaling its
  * row by a power of two, a softmax weight times its value scale is rounded);
  * sums and softmax statistics are fp32.

@@ -67,7 +67,7 @@ int pkv_kv4_attention(const pkv_kv4_cache *cache, const void *q, int64_t q_strid
     p.num_blocks = cache->num_blocks;
     p.n = n;
     p.T = num_tokens;
-    p.W = table_width;
+    p.set_table(table_width, cache->block_size);
     p.bs = cache->block_size;
     p.Hkv = cache->num_heads;
     p.G = num_q_heads / cache->num_heads;

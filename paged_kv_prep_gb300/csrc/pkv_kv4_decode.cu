@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT>(), 1) kv4_decode_kernel(c
             const int ua = p.whole ? 0 : static_cast<int>(u - tile);
             const int ub = p.whole ? per : static_cast<int>(end - tile < per ? end - tile : per);
             Tile<D, NT> x;
-            x.run(p, r, p.tables + static_cast<int64_t>(i) * p.W, head, rt, ua, ub, ring, queries);
+            x.run(p, r, p.tables + static_cast<int64_t>(i) * p.table_row, head, rt, ua, ub, ring, queries);
             if (ua == 0 && ub == per) {
                 x.write(p, r, head, rt);
             } else {

@@ -635,7 +635,7 @@ __device__ void walk_role(const Kv4Params &p, Smem<D> *sm, Walk &walk) {
             mbar_arrive(&sm->item_full[items % kItems]);
         }
         items++;
-        table = p.tables + static_cast<int64_t>(x.i) * p.W;
+        table = p.tables + static_cast<int64_t>(x.i) * p.table_row;
         s = x.base + x.ua * kKeys + 16 * g;
         entry = s / p.bs;
         offset = s - entry * p.bs;

@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(kWThreads, 2) kv8_weights_kernel(const AttnPar
     auto find_blocks = [&](const Unit &x, int parity) {
         if (tid < kTokens) {
             const int s = x.s0 + tid;
-            const int b = s >= x.r.lo && s < x.r.keys ? block_of(p, p.tables + static_cast<int64_t>(x.i) * p.W, s) : -1;
+            const int b = s >= x.r.lo && s < x.r.keys ? block_of(p, p.tables + static_cast<int64_t>(x.i) * p.table_row, s) : -1;
             sm.block[parity][tid] = b;
             sm.slot[parity][tid] = b < 0 ? kNone : static_cast<uint32_t>(b) * static_cast<uint32_t>(p.bs) + static_cast<uint32_t>(s % p.bs);
         }
@@ -572,7 +572,7 @@ int pkv_kv8_attention(const pkv_kv8_cache *cache, const void *q, int64_t q_strid
     p.num_blocks = cache->num_blocks;
     p.n = n;
     p.T = num_tokens;
-    p.W = table_width;
+    p.set_table(table_width, cache->block_size);
     p.bs = cache->block_size;
     p.Hkv = cache->num_heads;
     p.G = num_q_heads / cache->num_heads;

@@ -9,6 +9,9 @@
 
 namespace pkv {
 
+// Positions that are seen lie below this, so that the end of a unit, or of the one after it, fits 32 bits.
+constexpr int32_t kMostKeys = 0x7fffffff - 4095;
+
 struct AttnParams {
     const char *q;                 // [T][Hq][D], bytes below
     int64_t q_stride;
@@ -22,7 +25,8 @@ struct AttnParams {
     const int32_t *qsl;
     const int32_t *lens;
     int64_t num_blocks;
-    int32_t n, T, W;
+    int32_t n, T, W;               // W: a table's entries that are looked at, those of blocks below kMostKeys
+    int32_t table_row;             // entries of a table
     int32_t bs, Hkv, G;
     int32_t window;
     int32_t fp16;
@@ -32,6 +36,13 @@ struct AttnParams {
     float *part;                   // partial results, see pkv_kv8_decode.cu
     int4 *meta;
     int32_t *err;
+
+    // A table's width and what of it is looked at (a limit here costs the kernels nothing; one in request_of cost a step of
+    // chunks and decodes 16 us of 802).
+    void set_table(int32_t width, int32_t block_size) {
+        table_row = width;
+        W = width < kMostKeys / block_size ? width : kMostKeys / block_size;
+    }
 
     // The table's entry for a position, unchecked but for the table's end (-1 past it).
     __device__ __forceinline__ int32_t table_at(const int32_t *table, int32_t pos) const {
@@ -51,16 +62,13 @@ inline int64_t kv8_most_workers(int sms) {
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Positions that are seen lie below this, so that the end of a unit, or of the one after it, fits 32 bits.
-constexpr int32_t kMostKeys = 0x7fffffff - 4095;
-
 // One request's share of the batch.
 struct Req {
     int32_t start;                 // its first token in the batch
     int32_t count;                 // scheduled tokens (0: nothing to do)
-    int32_t len;                   // cached tokens, those of this step included; 0 where the batch has less
+    int32_t len;                   // cached tokens, those of this step included
     int32_t lo;                    // first key that any of its queries sees
-    int32_t keys;                  // keys that its block table can name, below kMostKeys
+    int32_t keys;                  // keys that its block table can name
 };
 
 __device__ __forceinline__ Req request_of(const AttnParams &p, int i, bool report = false) {
@@ -68,12 +76,12 @@ __device__ __forceinline__ Req request_of(const AttnParams &p, int i, bool repor
     const int32_t a = p.qsl[i], b = p.qsl[i + 1];
     r.start = a;
     r.count = b - a;
-    r.len = max(p.lens[i], 0);
+    r.len = p.lens[i];
     if (a < 0 || b < a || b > p.T) {
         if (report && p.err) atomicOr(p.err, PKV_DEVERR_COUNT);
         r.count = 0;
     }
-    const int64_t width = static_cast<int64_t>(p.W) * p.bs, cap = width < kMostKeys ? width : kMostKeys;
+    const int64_t cap = static_cast<int64_t>(p.W) * p.bs;
     if (r.len > cap && report && p.err && r.count > 0) atomicOr(p.err, PKV_DEVERR_BLOCK);
     r.keys = r.len < cap ? r.len : static_cast<int32_t>(cap);
     r.lo = 0;
@@ -86,7 +94,7 @@ __device__ __forceinline__ Req request_of(const AttnParams &p, int i, bool repor
 
 // First position that a query at `pos` sees.  (Before position 0, pos - window may pass the smallest integer.)
 __device__ __forceinline__ int32_t lo_of(const AttnParams &p, int32_t pos) {
-    return p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
+    return p.window > 0 ? max(0, max(pos, 0) - p.window + 1) : 0;
 }
 
 // Value scales below 2^-100 (an unwritten block's zero among them) count as 2^-100, so that their

@@ -132,7 +132,7 @@ struct Walk {
             x.s = s;
             x.i = i;
             x.rt = rt;
-            x.table = p.tables + static_cast<int64_t>(i) * p.W;
+            x.table = p.tables + static_cast<int64_t>(i) * p.table_row;
             x.head = static_cast<int>((u - rt_first) / s.units);
             x.tile = rt_first + static_cast<int64_t>(x.head) * s.units;
             x.ua = static_cast<int>(u - x.tile);

@@ -53,18 +53,18 @@ def test_windows_of_all_positions_before_the_first(reqs, d, window):
 
 @pytest.mark.parametrize("reqs", [(1, 4), (40, 8)], ids=["decode", "chunk"])
 def test_lengths_up_to_the_largest_integer(reqs):
-    """Tables that name one block of 2^24 tokens for all of 2^31 positions, of which the last 4096 are not seen.  Logits of
-    0 and values of 1: the output is 1, the log-sum the logarithm of the visible tokens' number (half a step of fp32 there
+    """Tables that name one block of 2^24 tokens for all of 2^31 positions, of which those of the last are not seen.  Logits
+    of 0 and values of 1: the output is 1, the log-sum the logarithm of the visible tokens' number (half a step of fp32 there
     is 2^-20; the sum's, logarithm's and product's roundings are less than four)."""
     T, group = reqs
-    bs, most = 1 << 24, 2 ** 31 - 4096
+    bs, most = 1 << 24, 2 ** 31 - (1 << 24)
     codes = [torch.full((bs, 64), c, dtype=torch.uint8, device="cuda") for c in (0, 0x38)]
     scales = [torch.ones(1, 1, device="cuda") for _ in range(2)]
     table = torch.zeros(1, 128, dtype=torch.int32, device="cuda")
     q = torch.ones(T, group, 64, dtype=torch.bfloat16, device="cuda")
     starts = torch.tensor([0, T], dtype=torch.int32, device="cuda")
     word = torch.zeros(1, dtype=torch.int32, device="cuda")
-    for length, window in ((2 ** 31 - 1, 0), (most, 0), (most + 60, 100), (2 ** 31 - 1, 1000), (most, 100), (-2 ** 31, 0), (-2 ** 31, 5)):
+    for length, window in ((2 ** 31 - 1, 0), (most, 0), (most + 60, 100), (2 ** 31 - 1, 1000), (most, 100), (-7, 0), (-7, 5)):
         word.zero_()
         out, lse = pkv.kv8_attention(q, *codes, *scales, table, starts, torch.tensor([length], dtype=torch.int32, device="cuda"),
                                      window=window, d_error=word.data_ptr())
