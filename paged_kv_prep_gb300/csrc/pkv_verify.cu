@@ -331,7 +331,11 @@ __global__ void __launch_bounds__(kThreads, kResident) verify_kernel(const Verif
         if (mates > 1) cluster_arrive();               // this CTA has read the others' sums
         if (total > 0) {
             found = true;
-            int64_t aim = __double2ll_rd(__dmul_rn(static_cast<double>(u), __ll2double_rn(total)));
+            const double near = __ll2double_rn(total);
+            double product = __dmul_rn(static_cast<double>(u), near);
+            // rounded once: what a total past 2^53 loses in fp64 (2^8 at most) times u's 24 bits is exact
+            if (total >> 53) product = __fma_rn(u, near, __dmul_rn(u, __ll2double_rn(total - __double2ll_rn(near))));
+            int64_t aim = __double2ll_rd(product);
             aim = aim >= total ? total - 1 : aim < 0 ? 0 : aim;
             if (before <= aim && aim < before + mine) {
                 const int32_t token = walk.find(from, to, aim - before);
