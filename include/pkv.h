@@ -787,6 +787,7 @@ int pkv_kv4_attention_workspace(int32_t head_dim, int64_t *bytes);
  * Attention of a prepared batch's queries over the 4-bit cache.  Everything is as in
  * pkv_kv8_attention (without its weights): which positions a query sees, rows that
  * see nothing, device errors, the layout of q, out and lse.  out and q do not overlap.
+ * softmax_scale * log2(e) * k_unit is finite in fp32 (PKV_ERR_INVALID_ARG).
  * The products' operands are f16: a value without its unit (code * scale, six bits) and a
  * query after scaling its row by a power of two are exact in it, a softmax weight is
  * rounded; sums and softmax statistics are fp32.

@@ -1,5 +1,7 @@
 // Host side of the attention over the 4-bit paged cache: argument checks, which
 // kernels take which requests.
+#include <cmath>
+
 #include "pkv_kv4_attention.cuh"
 
 namespace pkv {
@@ -35,6 +37,9 @@ int pkv_kv4_attention(const pkv_kv4_cache *cache, const void *q, int64_t q_strid
         (dtype != PKV_BF16 && dtype != PKV_FP16) || num_q_heads < 1 || num_q_heads % cache->num_heads ||
         table_width < 0 || window < 0 || q_stride_bytes < 0 || out_stride_bytes < 0)
         return PKV_ERR_INVALID_ARG;
+    // the kernels take the larger of a row's factor and a tiny number, which would hide a NaN
+    const float scale_log2 = softmax_scale * pkv::kLog2e * cache->k_unit;
+    if (!std::isfinite(scale_log2)) return PKV_ERR_INVALID_ARG;
     const int64_t row = 2LL * num_q_heads * cache->head_dim;
     // (query, head) rows are counted in 32 bits, with room for a last tile
     if (static_cast<int64_t>(num_tokens) * (num_q_heads / cache->num_heads) >= (1LL << 31) - 1024 || row >= (1LL << 31))
@@ -73,7 +78,7 @@ int pkv_kv4_attention(const pkv_kv4_cache *cache, const void *q, int64_t q_strid
     p.G = num_q_heads / cache->num_heads;
     p.window = window;
     p.fp16 = dtype == PKV_FP16;
-    p.scale_log2 = softmax_scale * pkv::kLog2e * cache->k_unit;
+    p.scale_log2 = scale_log2;
     p.meta = static_cast<int4 *>(workspace);
     p.part = reinterpret_cast<float *>(p.meta + pkv::kv8_most_workers(sms));
     p.err = d_error;
