@@ -1104,7 +1104,8 @@ _SHORT = None
 
 def _short():
     """The calls from here on in C++ (csrc/pkv_marshal.cpp), with their operands in the common form.  They give
-    NotImplemented, and have done nothing, for any other form; the functions below then check it."""
+    NotImplemented, and have done nothing, for any other form; the functions below then check it.  Without
+    _marshal.so they take every call, for 10 us and more of the host's time."""
     global _SHORT
     if _SHORT is None:
         import torch  # noqa: F401  (its libraries are there from here on)
@@ -1112,10 +1113,18 @@ def _short():
         try:
             from . import _marshal
         except ImportError as e:
-            raise RuntimeError("paged_kv_prep_gb300: _marshal.so is not built, or for another torch (run "
-                               "paged_kv_prep_gb300.build.build() or __graft_entry__.build())") from e
+            import warnings
+
+            warnings.warn("paged_kv_prep_gb300: _marshal.so is not built, or for another torch; calls are marshalled in "
+                          f"Python ({e}; paged_kv_prep_gb300.build.build() builds it)", RuntimeWarning, stacklevel=3)
+            _marshal = _NoShort
         _SHORT = _marshal
     return _SHORT
+
+
+class _NoShort:
+    """In the place of _marshal.so: no call is of its common form."""
+    rope_store = kv4_store = kv4_load = kv4_attention = verify_drafts = staticmethod(lambda *a: NotImplemented)
 
 
 def _rope_args(positions, table, axes, interleaved, tokens):

@@ -3,7 +3,9 @@ binding's C++ part ``_marshal.so`` against it and torch's libraries.
 
 Each translation unit is compiled in its own nvcc process (in parallel), then
 linked into one shared library with the CUDA runtime linked statically.  The
-ptxas resource report of every kernel is kept in ``_build/ptxas.log``.
+ptxas resource report of every kernel is kept in ``_build/ptxas.log``.  The library
+needs nvcc alone; where torch is not installed ``_marshal.so``, which only calls on
+torch's tensors use, is left out.
 """
 from __future__ import annotations
 
@@ -40,19 +42,23 @@ def _inputs():
         os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
 
 
+def torch_path():
+    """Where torch is installed, None where it is not."""
+    spec = importlib.util.find_spec("torch")
+    return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
+
+
 def up_to_date() -> bool:
-    if not (os.path.exists(LIBRARY) and os.path.exists(MARSHAL)):
+    built = [LIBRARY] + ([MARSHAL] if torch_path() else [])
+    if not all(map(os.path.exists, built)):
         return False
-    t = min(os.path.getmtime(LIBRARY), os.path.getmtime(MARSHAL))
+    t = min(map(os.path.getmtime, built))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
-def marshal_commands(nvcc):
+def marshal_commands(nvcc, torch):
     """The compiler's and the linker's command for ``_marshal.so``."""
-    cxx = os.environ.get("CXX") or shutil.which("g++")
-    if not cxx:
-        raise RuntimeError("g++ not found: it is required to build _marshal.so")
-    torch = importlib.util.find_spec("torch").submodule_search_locations[0]
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "g++"
     include = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(torch, "include"),
                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
@@ -65,6 +71,38 @@ def marshal_commands(nvcc):
     return compile_it, link
 
 
+def _begin_marshal(nvcc):
+    """Starts on ``_marshal.so`` beside the library: (its link command, the compiler's command, its process or why there
+    is none); None where torch is not installed."""
+    torch = torch_path()
+    if not torch:
+        return None
+    compile_it, link = marshal_commands(nvcc, torch)
+    try:
+        return link, compile_it, subprocess.Popen(compile_it, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    except OSError as e:
+        return link, compile_it, e
+
+
+def _compiled(process):
+    """Waits for the compiler: why it failed, or None."""
+    if isinstance(process, OSError):
+        return str(process)
+    out, _ = process.communicate()
+    return out.decode(errors="replace") if process.returncode else None
+
+
+def _link_marshal(link, compile_it, error):
+    """Links ``_marshal.so`` against the library; what fails here leaves the library built."""
+    cmd = compile_it
+    if error is None:
+        r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        cmd, error = link, r.stdout.decode(errors="replace") if r.returncode else None
+    if error is not None:
+        raise RuntimeError(f"libpkv.so is built, _marshal.so is not (it needs g++ and torch's headers):\n{' '.join(cmd)}\n{error}")
+    os.replace(MARSHAL + ".tmp", MARSHAL)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIBRARY
@@ -72,6 +110,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     common = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",
                      "-I", INCLUDE, "-I", CSRC, "-Xptxas", "-v", "--expt-relaxed-constexpr"]
+    marshal = _begin_marshal(nvcc)
     procs = []
     objs = []
     for src in sources():
@@ -80,8 +119,6 @@ def build(force: bool = False, verbose: bool = False) -> str:
         cmd = [nvcc, "-c", src, "-o", obj] + common
         procs.append((src, cmd, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                                  stderr=subprocess.STDOUT)))
-    compile_it, link_marshal = marshal_commands(nvcc)
-    procs.append((compile_it[2], compile_it, subprocess.Popen(compile_it, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     log = []
     failed = []
     for src, cmd, p in procs:
@@ -90,6 +127,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         log.append(f"== {os.path.basename(src)}\n{text}")
         if p.returncode != 0:
             failed.append((src, " ".join(cmd), text))
+    if marshal:
+        marshal = *marshal[:2], _compiled(marshal[2])
     with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
         f.write("\n".join(log))
     if failed:
@@ -101,10 +140,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
     os.replace(tmp, LIBRARY)
-    r = subprocess.run(link_marshal, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n" + r.stdout.decode(errors="replace"))
-    os.replace(MARSHAL + ".tmp", MARSHAL)
+    if marshal:
+        _link_marshal(*marshal)
     if verbose:
         print("\n".join(log))
     return LIBRARY
