@@ -1108,14 +1108,18 @@ def _short():
     _marshal.so they take every call, for 10 us and more of the host's time."""
     global _SHORT
     if _SHORT is None:
-        import torch  # noqa: F401  (its libraries are there from here on)
+        import torch            # its libraries are there from here on
+
+        from . import build
 
         try:
+            if build.marshal_abi() != build.abi(torch.__version__):
+                raise ImportError(f"built for {build.marshal_abi() or 'nothing that is known'}, not for {build.abi(torch.__version__)}")
             from . import _marshal
         except ImportError as e:
             import warnings
 
-            warnings.warn("paged_kv_prep_gb300: _marshal.so is not built, or for another torch; calls are marshalled in "
+            warnings.warn("paged_kv_prep_gb300: _marshal.so is not built, or for another torch or Python; calls are marshalled in "
                           f"Python ({e}; paged_kv_prep_gb300.build.build() builds it)", RuntimeWarning, stacklevel=3)
             _marshal = _NoShort
         _SHORT = _marshal

@@ -12,6 +12,7 @@ from __future__ import annotations
 import glob
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sysconfig
@@ -23,6 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIBRARY = os.path.join(HERE, "libpkv.so")
 MARSHAL = os.path.join(HERE, "_marshal.so")
+MARSHAL_ABI = os.path.join(BUILD, "marshal.abi")       # what _marshal.so was built for
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -48,8 +50,31 @@ def torch_path():
     return spec.submodule_search_locations[0] if spec and spec.submodule_search_locations else None
 
 
+def abi(torch_version) -> str:
+    """What ``_marshal.so`` goes by: torch's inlined layouts, Python's and its API."""
+    return f"torch {torch_version}, {sysconfig.get_config_var('SOABI')}"
+
+
+def marshal_abi() -> str:
+    """What the ``_marshal.so`` that is there was built for ("" where that is not known)."""
+    try:
+        with open(MARSHAL_ABI) as f:
+            return f.read()
+    except OSError:
+        return ""
+
+
+def _torch_version(torch):
+    """torch.__version__, without importing it."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return re.search(r"^__version__\s*=\s*['\"]([^'\"]*)", f.read(), re.M).group(1)
+
+
 def up_to_date() -> bool:
-    built = [LIBRARY] + ([MARSHAL] if torch_path() else [])
+    torch = torch_path()
+    if torch and marshal_abi() != abi(_torch_version(torch)):
+        return False
+    built = [LIBRARY] + ([MARSHAL] if torch else [])
     if not all(map(os.path.exists, built)):
         return False
     t = min(map(os.path.getmtime, built))
@@ -100,7 +125,11 @@ def _link_marshal(link, compile_it, error):
         cmd, error = link, r.stdout.decode(errors="replace") if r.returncode else None
     if error is not None:
         raise RuntimeError(f"libpkv.so is built, _marshal.so is not (it needs g++ and torch's headers):\n{' '.join(cmd)}\n{error}")
+    if os.path.exists(MARSHAL_ABI):
+        os.remove(MARSHAL_ABI)                         # a build that ends here is none
     os.replace(MARSHAL + ".tmp", MARSHAL)
+    with open(MARSHAL_ABI, "w") as f:
+        f.write(abi(_torch_version(torch_path())))
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -21,7 +21,7 @@ open(sys.argv[sys.argv.index("-o") + 1], "w").close()
 @pytest.fixture
 def places(tmp_path, monkeypatch):
     """A build into a folder of its own: a function that makes the compilers (nvcc, g++)."""
-    for name in ("BUILD", "LIBRARY", "MARSHAL"):
+    for name in ("BUILD", "LIBRARY", "MARSHAL", "MARSHAL_ABI"):
         monkeypatch.setattr(pbuild, name, str(tmp_path / name.lower()))
 
     def compilers(fails=False, missing=False):
@@ -40,6 +40,29 @@ def test_both_are_built(places):
     assert os.path.exists(pbuild.LIBRARY) and os.path.exists(pbuild.MARSHAL) and pbuild.up_to_date()
     os.remove(pbuild.MARSHAL)
     assert not pbuild.up_to_date()
+
+
+@pytest.mark.parametrize("what", ["torch", "Python", "unknown"])
+def test_the_bindings_part_is_built_again_for_another_torch_or_python(places, monkeypatch, what):
+    pbuild.build()
+    assert pbuild.up_to_date() and pbuild.marshal_abi() == pbuild.abi(torch.__version__)
+    if what == "torch":
+        monkeypatch.setattr(pbuild, "_torch_version", lambda path: "2.0.0")
+    elif what == "Python":
+        monkeypatch.setattr(pbuild.sysconfig, "get_config_var", lambda name: "cpython-399")
+    else:
+        os.remove(pbuild.MARSHAL_ABI)
+    assert not pbuild.up_to_date()
+    pbuild.build()
+    assert pbuild.up_to_date()
+
+
+def test_the_bindings_part_of_another_torch_is_not_imported(places, monkeypatch):
+    monkeypatch.setattr(_lib, "_SHORT", None)
+    pbuild.build()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    with pytest.warns(RuntimeWarning, match="for another torch or Python.*not for torch .*other"):
+        assert _lib._short() is _lib._NoShort
 
 
 def test_the_library_needs_no_torch(places, monkeypatch):
