@@ -641,8 +641,9 @@ int pkv_kv8_attention_workspace(int32_t num_tokens, int32_t num_q_heads, int32_t
  * leaves the batch: the request is skipped), PKV_DEVERR_BLOCK (a block id past
  * the cache, a position past the table or in a block that ends past 2^31 - 4096: not seen).
  * The products' operands are f16 (a code is exact in f16, a query after scaling its
- * row by a power of two, a softmax weight times its value scale is rounded);
- * sums and softmax statistics are fp32.
+ * row by a power of two where it is at least 2^-28 of the row's largest element, bf16:
+ * 2^-31; a smaller one is off by at most 2^-39 of the largest; a softmax weight times
+ * its value scale is rounded); sums and softmax statistics are fp32.
  */
 int pkv_kv8_attention(const pkv_kv8_cache *cache, const void *q, int64_t q_stride_bytes,
                       int32_t dtype, int32_t num_q_heads, const int32_t *block_tables,
@@ -788,9 +789,10 @@ int pkv_kv4_attention_workspace(int32_t head_dim, int64_t *bytes);
  * pkv_kv8_attention (without its weights): which positions a query sees, rows that
  * see nothing, device errors, the layout of q, out and lse.  out and q do not overlap.
  * softmax_scale * log2(e) * k_unit is finite in fp32 (PKV_ERR_INVALID_ARG).
- * The products' operands are f16: a value without its unit (code * scale, six bits) and a
- * query after scaling its row by a power of two are exact in it, a softmax weight is
- * rounded; sums and softmax statistics are fp32.
+ * The products' operands are f16: a value without its unit (code * scale, six bits) is exact
+ * in it, and so is a query, after scaling its row by a power of two, where it is at least 2^-28
+ * (fp16; bf16: 2^-31) of the row's largest element; a smaller one is off by at most 2^-39 of
+ * the largest.  A softmax weight is rounded; sums and softmax statistics are fp32.
  */
 int pkv_kv4_attention(const pkv_kv4_cache *cache, const void *q, int64_t q_stride_bytes,
                       int32_t dtype, int32_t num_q_heads, const int32_t *block_tables,

@@ -5,8 +5,8 @@
 // softmax_scale * log2(e) * k_unit, with k = code * scale exact in f16 (an e2m1 value has two
 // significant bits, an e4m3 scale four).  R, a row's reference, is 11 to 15 below the running
 // maximum of x.  w = 2^(x - R) <= 2^15 is rounded to f16 for the second product: off by 2^-11 of
-// itself, or by 2^-25 where it is below 2^-14: 2^-36 of the largest weight, at most 2^-14 of the
-// output (nonzero values are less than 2^22 apart).  out = v_unit * sum w v / sum w, lse = R ln 2 +
+// itself, or by 2^-25 where it is below 2^-14, which is 2^-36 of the largest weight: n such tokens put
+// the output off by n 2^-36 of the largest |value| at most.  out = v_unit * sum w v / sum w, lse = R ln 2 +
 // ln sum w, both sums in fp32.
 //
 // Bound: HBM, 2 * (D / 2 + D / 16) bytes per (cached token, KV head), each read once; next to it

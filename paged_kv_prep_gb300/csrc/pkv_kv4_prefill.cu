@@ -7,8 +7,9 @@
 // unit, rounded up to an integer, and then follows lazily: it moves only when the sum of 64 w,
 // which is needed anyway, exceeds 2^15, and by a whole power of two, so that
 // weights which are f16 already are not rounded again (unless they turn subnormal).
-// w is off by 2^-11 of itself, or by 2^-25 where it is below 2^-14: 2^-33 of the largest weight, at
-// most 2^-11 of the output (nonzero values are less than 2^22 apart).
+// w is off by 2^-11 of itself, or by 2^-25 where it is below 2^-14, and as much again if the reference
+// moves after it: 2^-32 of the largest weight together, so n such tokens put the output off by
+// n 2^-32 of the largest |value| at most.
 //
 // Bound: the tensor pipe (4 D flops per visible pair); beside it per tile of
 // 256 rows x 128 tokens 32768 exponentials and 32768 codes turned into f16 and scaled.

@@ -206,8 +206,9 @@ __device__ __forceinline__ float2 widen2(uint32_t x, bool fp16) {
 }
 
 // Queries go into the products as f16 after a power of two has brought their row's largest
-// magnitude into [2^14, 2^15): a bf16 or fp16 value keeps all its bits unless it is 2^-28 times
-// smaller than the row's largest, and what is then lost is below fp32's own rounding of the sum.
+// magnitude into [2^14, 2^15): a value keeps all its bits from 2^-28 (fp16; bf16: 2^-31) of the
+// row's largest on; a smaller one is off by 2^-39 of the largest at most, below fp32's own rounding of
+// a sum that the largest is part of.
 // Returns the exponent E with 2^E <= largest (clamped), so that the factor is 2^(14 - E).
 __device__ __forceinline__ int row_exponent(float largest) {
     const int e = static_cast<int>(__float_as_uint(largest) >> 23) - 127;
