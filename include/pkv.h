@@ -789,6 +789,9 @@ int pkv_kv4_attention_workspace(int32_t head_dim, int64_t *bytes);
  * pkv_kv8_attention (without its weights): which positions a query sees, rows that
  * see nothing, device errors, the layout of q, out and lse.  out and q do not overlap.
  * softmax_scale * log2(e) * k_unit is finite in fp32 (PKV_ERR_INVALID_ARG).
+ * Any n, num_tokens and table_width that hold the batch give the same result but for rounding; the choice of
+ * kernels goes by them, so a call is fastest without idle requests, without rows behind the
+ * last request and with a table no wider than the longest one needs.
  * The products' operands are f16: a value without its unit (code * scale, six bits) is exact
  * in it, and so is a query, after scaling its row by a power of two, where it is at least 2^-28
  * (fp16; bf16: 2^-31) of the row's largest element; a smaller one is off by at most 2^-39 of

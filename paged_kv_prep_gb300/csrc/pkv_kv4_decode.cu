@@ -26,7 +26,9 @@
 // Measured, with the merge: 256 single tokens, 32 query and 8 KV heads of 128, contexts up to 8192 (1.16 GB) 221 us,
 // 78 % of the copy rate; four of 64 query heads on 65536 to 131072 tokens (455 MB) 96 us, 70 %; 96 requests
 // of two to six tokens, 40 query heads, a window of 4096 (411 MB; a request of more than 16 rows takes two tiles,
-// which both go through its lines) 218 us.
+// which both go through its lines) 220 us.  Of head_dim 256, 4 KV heads: 256 single tokens as many bytes 218 us; 96 requests
+// of two to six tokens 198 us (324 bytes of registers spilled a thread); prompt chunks, which the prefill kernel does not
+// take, 2330 us for the 522 GFLOP that it does in 460 of head_dim 128.
 // Instructions bound it next to HBM: 129 for 1 KB of codes with eight rows, 0.6 a cycle issued, the
 // integer pipe 50 % busy with the conversions.  Tiles of eight rows: twelve warps an SM, 221 us for the 256; eight 262, ten
 // 264, thirteen 261, fourteen 246, sixteen (spilling) 236; queries in registers 224; a second unit on its way 224.  Tiles of

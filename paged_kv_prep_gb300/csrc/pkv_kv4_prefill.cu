@@ -32,14 +32,14 @@
 // Every wait has a limit; one that runs out sets PKV_DEVERR_TIMEOUT, the other
 // waits give up after it, and the CTA drains its products and frees its TMEM.
 //
-// Measured: two chunks of 2048 tokens, 32 query and 8 KV heads of 128, contexts up to 16384 (522 GFLOP) 473 us
-// with the merge, 1.10 PFLOP/s, 58 % of the measured rate of bf16 products.  A unit of 256 rows x 128 tokens takes 3900 cycles of
-// which the tensor pipe works 2048 (the rest is the way scores -> weights -> products with its barriers: without
-// any exponentials and conversions 390 us remain of 495, before the second products began by halves); a row tile 25000
-// cycles beside its units.  What was slower, against 495 us for those chunks: two issuing warps 551; scores in halves
-// of 64 tokens, two in TMEM 536; fetching codes ahead into L2 518; waits that sleep in hardware 537.  Codes copied to
-// shared memory (by bulk copies or by warps of their own) instead of into registers: 1530 us for a step of chunks
-// and decodes that takes 989 so.
+// Measured: two chunks of 2048 tokens, 32 query and 8 KV heads of 128, contexts up to 16384 (522 GFLOP) 460 us
+// with the merge, 1.13 PFLOP/s, 60 % of the measured rate of bf16 products.  A unit of 256 rows x 128 tokens takes 3900 cycles of
+// which the tensor pipe works 2048 (the rest is the way scores -> weights -> products with its barriers); a row tile 25000
+// cycles beside its units.  What was slower, in turn with the form of its time (465 to 500 us, not this one): two issuing warps,
+// 1.13 times as long; scores in halves of 64 tokens, two in TMEM, 1.08; fetching codes ahead into L2, 1.04; waits that sleep
+// in hardware, 1.08; codes copied to shared memory (by bulk copies or by warps of their own) instead of into registers,
+// 1.55 for a step of chunks and decodes.  Without any exponentials and conversions a form that took 495 us, whose second
+// products did not begin by halves, took 390.
 #include "pkv_kv4_attention.cuh"
 #include "pkv_tcgen05.cuh"
 
@@ -60,7 +60,7 @@ constexpr float kMostSum = 32768.f;     // sum of 64 w that makes it move
 constexpr float kHuge = 0x1p20f;        // a reference from which on a logit's rounding may count
 // Costs, in units of a row tile that one warpgroup's half of the units takes: a unit of two tiles, and what a
 // row tile costs beside its units (queries, first scores, output).  A mixed call with 3 for the latter 954 us, with 6
-// 858, 10 817, 14 810; long chunks 488, 479, 472 and 473.
+// 858, 10 817, 12 813, 14 810; long chunks with 3 488, 6 479, 10 472, 14 473.
 constexpr int kPairCost = 2, kTileCost = 12;
 
 // Kinds of units: of two tiles, a row tile's last of this CTA, the CTA's last; no unit at all.
@@ -684,7 +684,7 @@ __device__ void walk_role(const Kv4Params &p, Smem<D> *sm, Walk &walk) {
 
 // ---- issuing warp ------------------------------------------------------------------------------
 // The whole warp goes through the units, so that addresses and descriptors stay in uniform registers; one
-// lane issues.  (A warp for each tile: 551 us where this takes 486, the tiles' products delay each other.)
+// lane issues.  (A warp for each tile took 1.13 times as long: the tiles' products delay each other.)
 // Operand descriptors as in smem_desc: the upper word is the same for all, the lower one holds the address.
 constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) { return ((addr & 0x3ffffu) >> 4) | (lead >> 4 << 16); }

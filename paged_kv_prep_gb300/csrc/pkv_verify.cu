@@ -16,8 +16,8 @@
 // warp works out for itself which drafts stand, a lane per draft.  The warps' totals meet through
 // distributed shared memory; the warp whose stretch holds the aim walks it again (from L2) to
 // name the token, while the other CTAs make room for the next requests'.
-// Measured: 256 requests of up to four drafts over 131072 fp32 probabilities (198 MB read) 41 us,
-// 4.8 TB/s, 71 % of the measured copy rate.  Six instructions an element: with every element's place checked
+// Measured: 256 requests of up to four drafts over 131072 fp32 probabilities (188 MB of rows) 41 us,
+// 4.6 TB/s, 68 % of the measured copy rate (199 MB are read in all).  Six instructions an element: with every element's place checked
 // (thirty) 58 us.  CTAs of 256 threads 44 us; clusters of four 42 us, of two 54 us; four loads at a
 // time 44 us.  The rest is latency: offsets, drafts, their probabilities, the row come one after the
 // other, and the last wave's walk for the token.
