@@ -9,6 +9,7 @@ torch's tensors use, is left out.
 """
 from __future__ import annotations
 
+import contextlib
 import glob
 import importlib.util
 import os
@@ -125,7 +126,7 @@ def _link_marshal(link, compile_it, error):
         cmd, error = link, r.stdout.decode(errors="replace") if r.returncode else None
     if error is not None:
         raise RuntimeError(f"libpkv.so is built, _marshal.so is not (it needs g++ and torch's headers):\n{' '.join(cmd)}\n{error}")
-    if os.path.exists(MARSHAL_ABI):
+    with contextlib.suppress(FileNotFoundError):
         os.remove(MARSHAL_ABI)                         # a build that ends here is none
     os.replace(MARSHAL + ".tmp", MARSHAL)
     with open(MARSHAL_ABI, "w") as f:
